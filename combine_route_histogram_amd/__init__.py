@@ -44,6 +44,12 @@ MDC_MAX_COMBINE_WORLD = 64
 MDC_FLAG_FFN_PIPELINE = 0x1
 MDC_FLAG_SPIN_SHIFT = 8
 MDC_STATUS_BYTES = 256
+MDC_DTYPE_BF16, MDC_DTYPE_FP16, MDC_DTYPE_FP32 = 0, 1, 2
+MDC_GATE_SOFTMAX, MDC_GATE_SIGMOID = 0, 1
+MDC_MAX_GATE_EXPERTS = 2048
+MDC_MAX_GATE_GROUPS = 64
+MDC_QUANT_NONE, MDC_QUANT_INT8, MDC_QUANT_FP8 = 0, 1, 2
+MDC_MAX_NORM_HIDDEN = 32768
 
 EXPORTS = (
     "mdc_status_string", "mdc_abi_version",
@@ -51,6 +57,7 @@ EXPORTS = (
     "mdc_dispatch", "mdc_combine_workspace", "mdc_combine_workspace_size", "mdc_combine",
     "mdc_ffn_workspace", "mdc_ffn_workspace_size", "mdc_ffn", "mdc_dispatch_quant", "mdc_dispatch_quant_gather",
     "mdc_ffn_quant_input", "mdc_dispatch_noalloc", "mdc_dispatch_ffn",
+    "mdc_gate", "mdc_add_rms_norm", "mdc_gmm_fp8", "mdc_ffn_fp8_workspace", "mdc_ffn_fp8", "mdc_ffn_fp8_quant_input",
 )
 
 
@@ -59,6 +66,18 @@ class mdc_shape(ctypes.Structure):
                 ("hidden", ctypes.c_int32), ("topk", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("capacity", ctypes.c_int64), ("mask_per_route", ctypes.c_int32),
                 ("zero_experts", ctypes.c_int32), ("copy_experts", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class mdc_gate_params(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class mdc_norm_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("quant", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _P = ctypes.c_void_p
@@ -94,6 +113,12 @@ _sig("mdc_ffn_quant_input", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P
 _sig("mdc_dispatch_noalloc", _SHP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P)
 _sig("mdc_dispatch_ffn", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
      _SZ, _P)
+_sig("mdc_gate", _SHP, ctypes.POINTER(mdc_gate_params), _P, _P, _P, _P, _P)
+_sig("mdc_add_rms_norm", ctypes.POINTER(mdc_norm_params), _P, _P, _P, _P, _P, _P, _P, _P)
+_sig("mdc_gmm_fp8", ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P)
+_sig("mdc_ffn_fp8_workspace", _SHP, ctypes.c_int32, ctypes.POINTER(_SZ))
+_sig("mdc_ffn_fp8", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
+_sig("mdc_ffn_fp8_quant_input", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
 MDC_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -246,6 +271,13 @@ def mdc_ffn_workspace(shape: Shape, inter_n: int) -> int:
     out = _SZ(0)
     sh = shape.c()
     _check(_lib.mdc_ffn_workspace(ctypes.byref(sh), int(inter_n), ctypes.byref(out)), "mdc_ffn_workspace")
+    return int(out.value)
+
+
+def mdc_ffn_fp8_workspace(shape: Shape, inter_n: int) -> int:
+    out = _SZ(0)
+    sh = shape.c()
+    _check(_lib.mdc_ffn_fp8_workspace(ctypes.byref(sh), int(inter_n), ctypes.byref(out)), "mdc_ffn_fp8_workspace")
     return int(out.value)
 
 
@@ -467,6 +499,178 @@ def prepare_dispatch_ffn(shape: Shape, inter_n: int, x, expand_q, dynamic_scales
     return Prepared(_lib.mdc_dispatch_ffn, args, "mdc_dispatch_ffn", (sh, _tensors(locals())))
 
 
+# ---- gate, norm and fp8 products: these also check that their tensors are on one GPU, and run there ----
+
+_DTYPES = {torch.bfloat16: MDC_DTYPE_BF16, torch.float16: MDC_DTYPE_FP16, torch.float32: MDC_DTYPE_FP32}
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_SCORES = {"softmax": MDC_GATE_SOFTMAX, "sigmoid": MDC_GATE_SIGMOID}
+
+
+class DevicePrepared(Prepared):
+    """A Prepared whose tensors live on the GPU `device`; it launches there whatever the current device is."""
+    __slots__ = ("_device",)
+
+    def __init__(self, fn, args, name, keep, device):
+        super().__init__(fn, args, name, keep)
+        self._device = device
+
+    def _launch(self) -> int:
+        if self._device is None or torch.cuda.current_device() == self._device:
+            return self._fn(*self._args)
+        with torch.cuda.device(self._device):
+            return self._fn(*self._args)
+
+    def __call__(self) -> None:
+        st = self._launch()
+        if st != MDC_OK:
+            raise MdcError(st, self._name)
+
+
+def _one_device(*tensors) -> Optional[int]:
+    """Index of the GPU that holds all tensor arguments (raw pointers pass; None if there are only those)."""
+    device = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("mdc: tensors must be on a GPU")
+        if device is None:
+            device = d
+        elif d != device:
+            raise ValueError(f"mdc: tensors are on different GPUs ({device} and {d})")
+    return device
+
+
+def _device_stream(stream, device: Optional[int]) -> Optional[int]:
+    if stream is None and device is not None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _run_on_device(p: DevicePrepared, check: bool) -> int:
+    st = p._launch()
+    if check:
+        _check(st, p._name)
+    return st
+
+
+def prepare_gate(shape: Shape, logits, bias, expert_ids, expert_scales, score: str = "softmax", groups: int = 1,
+                 topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+                 stream=None) -> DevicePrepared:
+    """Routes and weights from router logits [W*BS][E + Z + C] (bf16, fp16 or fp32); bias fp32 or None."""
+    n = shape.num_experts + shape.zero_experts + shape.copy_experts
+    tokens = shape.world * shape.bs
+    _need(logits, "logits", tuple(_DTYPES), tokens * n)
+    _need(bias, "bias", torch.float32, n)
+    _need(expert_ids, "expert_ids", torch.int32, tokens * shape.topk)
+    _need(expert_scales, "expert_scales", torch.float32, tokens * shape.topk)
+    if score not in _SCORES:
+        raise ValueError(f"mdc: score must be softmax or sigmoid, got {score!r}")
+    sh = shape.c()
+    pr = mdc_gate_params(_DTYPES[logits.dtype], _SCORES[score], int(groups), int(topk_groups), int(group_top),
+                         1 if renormalise else 0, float(scale))
+    device = _one_device(logits, bias, expert_ids, expert_scales)
+    args = (sh, pr, _ptr(logits), _ptr(bias), _ptr(expert_ids), _ptr(expert_scales), _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_gate, args, "mdc_gate", (logits, bias, expert_ids, expert_scales), device)
+
+
+def prepare_add_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=None, q_scale=None,
+                         eps: float = 1e-6, stream=None) -> DevicePrepared:
+    """Residual addition and RMS norm of the rows of x [..., H] (bf16 or fp16).
+
+    residual and residual_out are of x's dtype or fp32 (both the same), weight
+    [H] of x's dtype or fp32; q int8 with q_scale [rows], or e4m3 (or uint8)
+    with q_scale [rows][ceil(H / 128)].
+    """
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"mdc: x must be bf16 or fp16, got {x.dtype}")
+    H = weight.numel()
+    if x.dim() < 1 or x.shape[-1] != H:
+        raise ValueError(f"mdc: x has rows of {x.shape[-1] if x.dim() else 0} elements, weight holds {H}")
+    numel = x.numel()
+    rows = numel // H if H else 0
+    wide = (x.dtype, torch.float32)
+    _need(weight, "weight", wide, H)
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        _need(t, name, wide, numel)
+    res_dtype = x.dtype if residual is None and residual_out is None else \
+        (residual if residual is not None else residual_out).dtype
+    if residual_out is not None and residual_out.dtype != res_dtype:
+        raise ValueError(f"mdc: residual_out must be {res_dtype} as residual, got {residual_out.dtype}")
+    _need(y, "y", x.dtype, numel)
+    quant = MDC_QUANT_NONE
+    if q is not None:
+        _need(q, "q", (torch.int8,) + _E4M3, numel)
+        quant = MDC_QUANT_INT8 if q.dtype == torch.int8 else MDC_QUANT_FP8
+        _need(q_scale, "q_scale", torch.float32, rows * (1 if quant == MDC_QUANT_INT8 else -(-H // 128)))
+    elif q_scale is not None:
+        raise ValueError("mdc: q_scale without q")
+    pr = mdc_norm_params(rows, H, _DTYPES[x.dtype], _DTYPES[res_dtype], _DTYPES[weight.dtype], quant, float(eps))
+    device = _one_device(x, residual, weight, residual_out, y, q, q_scale)
+    args = (pr, _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(q), _ptr(q_scale),
+            _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_add_rms_norm, args, "mdc_add_rms_norm",
+                          (x, residual, weight, residual_out, y, q, q_scale), device)
+
+
+def prepare_gmm_fp8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None) -> DevicePrepared:
+    """Grouped fp8 product: a [A][K], a_scale [A][ceil(K/128)], w [L][n][K] (or [n][K]), w_scale
+    [L][ceil(n/128)][ceil(K/128)], y [A][n] bf16; expert_token_nums [L], or None with one expert."""
+    if a.dim() != 2 or w.dim() not in (2, 3):
+        raise ValueError("mdc: a must have 2 dimensions, w 2 or 3")
+    A, K = a.shape
+    L, n = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2]
+    if w.shape[-1] != K:
+        raise ValueError(f"mdc: w has rows of {w.shape[-1]} elements, a of {K}")
+    nk = -(-K // 128)
+    _need(a, "a", _E4M3, A * K)
+    _need(a_scale, "a_scale", torch.float32, A * nk)
+    _need(expert_token_nums, "expert_token_nums", torch.int64, L)
+    _need(w, "w", _E4M3, L * n * K)
+    _need(w_scale, "w_scale", torch.float32, L * -(-n // 128) * nk)
+    _need(y, "y", _BF16, A * n)
+    device = _one_device(a, a_scale, expert_token_nums, w, w_scale, y)
+    args = (A, L, n, K, _ptr(a), _ptr(a_scale), _ptr(expert_token_nums), _ptr(w), _ptr(w_scale), _ptr(y),
+            _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_gmm_fp8, args, "mdc_gmm_fp8", (a, a_scale, expert_token_nums, w, w_scale, y),
+                          device)
+
+
+def _check_ffn_fp8_weights(shape: Shape, N: int, expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace) -> None:
+    L, H, A = shape.local_experts, shape.hidden, shape.capacity
+    _need(expert_token_nums, "expert_token_nums", torch.int64, L)
+    _need(w1, "w1", _E4M3, L * N * H)
+    _need(w1_scale, "w1_scale", torch.float32, L * (N // 128) * (H // 128))
+    _need(w2, "w2", _E4M3, L * H * (N // 2))
+    _need(w2_scale, "w2_scale", torch.float32, L * (H // 128) * (N // 256))
+    _need(y, "y", _BF16, A * H)
+
+
+def prepare_ffn_fp8(shape: Shape, inter_n: int, expand_x, expert_token_nums, w1, w1_scale, w2, w2_scale, y,
+                    workspace, stream=None) -> DevicePrepared:
+    _need(expand_x, "expand_x", _BF16, shape.capacity * shape.hidden)
+    _check_ffn_fp8_weights(shape, int(inter_n), expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace)
+    keep = (expand_x, expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace)
+    device = _one_device(*keep)
+    args = (shape.c(), int(inter_n), _ptr(expand_x), _ptr(expert_token_nums), _ptr(w1), _ptr(w1_scale), _ptr(w2),
+            _ptr(w2_scale), _ptr(y), _ptr(workspace), _nbytes(workspace), _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_ffn_fp8, args, "mdc_ffn_fp8", keep, device)
+
+
+def prepare_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_scales, expert_token_nums, w1,
+                                w1_scale, w2, w2_scale, y, workspace, stream=None) -> DevicePrepared:
+    _need(expand_q, "expand_q", _E4M3, shape.capacity * shape.hidden)
+    _need(dynamic_scales, "dynamic_scales", torch.float32, shape.capacity * (shape.hidden // 128))
+    _check_ffn_fp8_weights(shape, int(inter_n), expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace)
+    keep = (expand_q, dynamic_scales, expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace)
+    device = _one_device(*keep)
+    args = (shape.c(), int(inter_n), _ptr(expand_q), _ptr(dynamic_scales), _ptr(expert_token_nums), _ptr(w1),
+            _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), _ptr(y), _ptr(workspace), _nbytes(workspace),
+            _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_ffn_fp8_quant_input, args, "mdc_ffn_fp8_quant_input", keep, device)
+
+
 # ----------------------------------------------------------------------------
 # one-shot calls (marshal and launch)
 # ----------------------------------------------------------------------------
@@ -541,6 +745,34 @@ def mdc_dispatch_ffn(shape: Shape, inter_n: int, x, expand_q, dynamic_scales, as
     return _run(prepare_dispatch_ffn(shape, inter_n, x, expand_q, dynamic_scales, assist_info, ep_recv_counts,
                                      expert_token_nums, expanded_row_idx, w1, w1_scale, w2, w2_scale, y,
                                      dispatch_workspace, ffn_workspace, stream, expert_scales, expand_scales), check)
+
+
+def mdc_gate(shape: Shape, logits, bias, expert_ids, expert_scales, score: str = "softmax", groups: int = 1,
+             topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None,
+             check: bool = True) -> int:
+    return _run_on_device(prepare_gate(shape, logits, bias, expert_ids, expert_scales, score, groups, topk_groups,
+                                       group_top, renormalise, scale, stream), check)
+
+
+def mdc_add_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=None, q_scale=None, eps: float = 1e-6,
+                     stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_add_rms_norm(x, weight, residual, residual_out, y, q, q_scale, eps, stream), check)
+
+
+def mdc_gmm_fp8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_gmm_fp8(a, a_scale, expert_token_nums, w, w_scale, y, stream), check)
+
+
+def mdc_ffn_fp8(shape: Shape, inter_n: int, expand_x, expert_token_nums, w1, w1_scale, w2, w2_scale, y, workspace,
+                stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_ffn_fp8(shape, inter_n, expand_x, expert_token_nums, w1, w1_scale, w2, w2_scale, y,
+                                          workspace, stream), check)
+
+
+def mdc_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_scales, expert_token_nums, w1, w1_scale,
+                            w2, w2_scale, y, workspace, stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_ffn_fp8_quant_input(shape, inter_n, expand_q, dynamic_scales, expert_token_nums, w1,
+                                                      w1_scale, w2, w2_scale, y, workspace, stream), check)
 
 
 def alloc_dispatch_outputs(shape: Shape, device="cuda"):

@@ -10,8 +10,8 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-# kernel sources compiled into the one library; mdc_common.h is shared by both
-SRCS = [os.path.join(PKG, "csrc", "mdc_dispatch.hip"), os.path.join(PKG, "csrc", "mdc_ffn.hip")]
+# kernel sources compiled into the one library; mdc_common.h is shared by all
+SRCS = [os.path.join(PKG, "csrc", f"mdc_{name}.hip") for name in ("dispatch", "ffn", "gate", "norm", "gmm")]
 INC = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libmdc.so")
 # the memory-ceiling probes the benchmark times beside the library (a library of their own)

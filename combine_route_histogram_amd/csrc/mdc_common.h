@@ -74,6 +74,8 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int k) {
 // Host side
 // ---------------------------------------------------------------------------
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Argument checks shared by every entry point.  MDC_ERR_INVALID: the fields do

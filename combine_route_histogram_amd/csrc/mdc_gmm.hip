@@ -1,0 +1,484 @@
+// libmdc: grouped products in fp8 (e4m3) with a scale for each block of 128,
+// and the expert FFN built on them, for AMD Instinct MI355X (gfx950):
+// mdc_gmm_fp8, mdc_ffn_fp8, mdc_ffn_fp8_quant_input.
+
+#include "mdc_fp8.h"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// y[r][c] = sum over k-blocks b of sa[r][b] sw[e][c / 128][b] P_b[r][c], where
+// P_b is the plain product over 128 columns.  v_mfma_f32_16x16x128_f8f6f4
+// multiplies exactly one such block: each instruction starts from zero, and
+// its 16 x 16 result is added to the fp32 accumulators with the block's scale
+// by four FMAs per lane, which run beside the next matrix instructions.
+//
+// The weight block is the first operand and the token block the second: lane l
+// supplies row l % 16 of each and receives C[4 (l / 16) + i][l % 16], i < 4,
+// i.e. four consecutive output columns of one token, so that one scale per
+// lane serves a 16 x 16 block.  The 32 bytes a lane supplies are the 16-byte
+// chunks l / 16 and 4 + l / 16 of its row's 128: which k they are does not
+// matter, as long as both operands agree.
+// ---------------------------------------------------------------------------
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ v4f mfma_block(v8i w, v8i t) {
+  // formats 0, 0: both operands e4m3; no hardware scales
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, t, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
+
+__device__ __forceinline__ float gmm_silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+// One grouped product.
+struct Gmm {
+  const uint8_t* a;        // [A][K] e4m3
+  const float* a_scale;    // [A][nk]
+  const int64_t* nums;     // [L], or NULL: one expert with all A rows
+  const uint8_t* w;        // [L][Nw][K] e4m3
+  const float* w_scale;    // [L][ceil(Nw / 128)][nk]
+  uint16_t* y;             // [A][Nw] bf16
+  float* g;                // SwiGLU: [A][Nw / 2] fp32
+  int A, L, Nw, K, nk;
+};
+
+// ---------------------------------------------------------------------------
+// Rows and tiles of the experts.  Every workgroup works out the plan from the
+// counts by itself, in LDS: rows[e], tiles[e] = first row and first m-tile of
+// expert e, e <= L.
+// ---------------------------------------------------------------------------
+struct GmmTable {
+  int* rows;    // [L + 1]
+  int* tiles;   // [L + 1]
+};
+constexpr size_t gmm_table_bytes(int L) { return 2 * sizeof(int) * ((size_t)L + 1); }
+
+// Inclusive sum over the workgroup's threads; wave_total holds one value per
+// wavefront and one more.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t n = __shfl_up(v, o, 64);
+    if (lane >= o) v += n;
+  }
+  if (lane == 63) wave_total[wave] = v;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) v += wave_total[w];
+  __syncthreads();
+  return v;
+}
+
+// mtiles(n): m-tiles of an expert with n rows.
+template <int THREADS, typename F>
+__device__ __forceinline__ void gmm_plan(const Gmm& g, GmmTable t, int64_t* wave_total, F mtiles) {
+  int64_t carry = 0;
+  int tcarry = 0;
+  for (int e0 = 0; e0 < g.L; e0 += THREADS) {
+    const int e = e0 + threadIdx.x;
+    int64_t n = 0;
+    if (e < g.L) n = g.nums == nullptr ? g.A : min(max(g.nums[e], (int64_t)0), (int64_t)g.A);
+    const int64_t end = carry + block_scan<THREADS>(n, wave_total);
+    const int hi = (int)min(end, (int64_t)g.A), lo = (int)min(end - n, (int64_t)g.A);
+    const int m = mtiles(hi - lo);
+    const int tend = tcarry + (int)block_scan<THREADS>(m, wave_total);
+    if (e < g.L) {
+      t.rows[e + 1] = hi;
+      t.tiles[e + 1] = tend;
+    }
+    if (e0 + THREADS < g.L) {   // the last thread's ends start the next run
+      if (threadIdx.x == THREADS - 1) {
+        wave_total[0] = end;
+        wave_total[1] = tend;
+      }
+      __syncthreads();
+      carry = wave_total[0];
+      tcarry = (int)wave_total[1];
+      __syncthreads();
+    }
+  }
+  if (threadIdx.x == 0) t.rows[0] = t.tiles[0] = 0;
+  __syncthreads();
+}
+
+// Expert that m-tile m belongs to: the number of experts whose tiles end at or
+// before m.
+__device__ __forceinline__ int gmm_expert(const GmmTable& t, int L, int m) {
+  const int lane = threadIdx.x & 63;
+  int e = 0;
+  for (int e0 = 0; e0 < L; e0 += 64) {
+    const int i = e0 + lane;
+    e += __popcll(__ballot(i < L && t.tiles[i + 1] <= m));
+  }
+  return __builtin_amdgcn_readfirstlane(e);
+}
+
+// ---------------------------------------------------------------------------
+// Experts with few rows: what counts is to stream the weights.  A workgroup
+// takes up to 64 rows of an expert and 32 weight rows (SwiGLU: 16 gate rows and
+// the 16 up rows that go with them); its four wavefronts split the k-blocks
+// into four runs and join their sums through LDS.  Weights and rows go from
+// memory straight to registers, DEPTH k-blocks ahead.
+// ---------------------------------------------------------------------------
+constexpr int kThinRows = 64;
+constexpr int kThinThreads = 256;
+constexpr int kThinWaves = kThinThreads / 64;
+constexpr int kThinW = 32;   // weight rows of a tile
+
+template <bool GLU, int MB, int DEPTH>
+__device__ __forceinline__ void thin_tile(const Gmm& g, int e, int row0, int rows, int nt, v4f* red) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int K = g.K, nk = g.nk, Nw = g.Nw;
+  const int n0 = nt * (GLU ? kThinW / 2 : kThinW);
+  constexpr unsigned kOut = 0x80000000u;   // past every buffer: reads zero
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(g.a_scale + (int64_t)row0 * nk), (short)0, rows * nk * 4, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.w + (int64_t)e * Nw * K), (short)0, Nw * K, 0x00020000);
+  const int wb = (Nw + kFp8Block - 1) / kFp8Block;
+  const float* ws0 = g.w_scale + ((int64_t)e * wb + n0 / kFp8Block) * nk;
+  const float* ws1 = GLU ? g.w_scale + ((int64_t)e * wb + (Nw / 2 + n0) / kFp8Block) * nk : ws0;
+  // lane offsets of the weight rows and token rows, without k
+  unsigned wo[2], to[MB], so[MB];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = (GLU ? n0 + j * (Nw / 2) : n0 + 16 * j) + r16;
+    wo[j] = row < Nw ? (unsigned)row * (unsigned)K : kOut;
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    to[i] = (unsigned)((16 * i + r16) * K);
+    so[i] = (unsigned)((16 * i + r16) * nk) * 4u;
+  }
+  struct Step {
+    v4i w[2][2], t[MB][2];
+    float sa[MB], sw[2];
+  };
+  auto load = [&](Step& s, int b) {
+    const unsigned k0 = (unsigned)b * kFp8Block + 16u * quad, k1 = k0 + 64u;
+    const bool in0 = k0 < (unsigned)K, in1 = k1 < (unsigned)K;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, in0 ? wo[j] + k0 : kOut, 0, 0);
+      s.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, in1 ? wo[j] + k1 : kOut, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      s.t[i][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, in0 ? to[i] + k0 : kOut, 0, 0);
+      s.t[i][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, in1 ? to[i] + k1 : kOut, 0, 0);
+      s.sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[i] + (unsigned)b * 4u, 0, 0));
+    }
+    s.sw[0] = ws0[b];
+    s.sw[1] = GLU ? ws1[b] : s.sw[0];
+  };
+  v4f acc[MB][2];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Step& s) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const v8i t = join(s.t[i][0], s.t[i][1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const v4f p = mfma_block(join(s.w[j][0], s.w[j][1]), t);
+        const float sc = s.sa[i] * s.sw[j];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc, acc[i][j][r]);
+      }
+    }
+  };
+  const int per = (nk + kThinWaves - 1) / kThinWaves;
+  const int beg = min(nk, wave * per), end = min(nk, beg + per);
+  Step ring[DEPTH];
+  if (beg < end) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(ring[d], min(beg + d, end - 1));
+    int b = beg;
+    for (; b + DEPTH <= end; b += DEPTH)
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        compute(ring[d]);
+        load(ring[d], min(b + d + DEPTH, end - 1));   // (past the run: its last block again, unused)
+      }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (b + d < end) compute(ring[d]);
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) red[(wave * MB * 2 + i * 2 + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  auto total = [&](int block) {
+    v4f s = red[block * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kThinWaves; ++w) {
+      const v4f p = red[(w * MB * 2 + block) * 64 + lane];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r] += p[r];
+    }
+    return s;
+  };
+  if (GLU) {
+    for (int i = wave; i < MB; i += kThinWaves) {
+      const v4f gate = total(2 * i), up = total(2 * i + 1);
+      v4f out;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) out[r] = gmm_silu(gate[r]) * up[r];
+      const int row = 16 * i + r16;
+      if (row < rows)
+        *reinterpret_cast<v4f*>(g.g + (int64_t)(row0 + row) * (Nw / 2) + n0 + 4 * quad) = out;
+    }
+  } else {
+    for (int i = wave; i < 2 * MB; i += kThinWaves) {
+      const v4f s = total(i);
+      const int row = 16 * (i >> 1) + r16, col = n0 + 16 * (i & 1) + 4 * quad;
+      if (row < rows && col < Nw)
+        *reinterpret_cast<v4b*>(g.y + (int64_t)(row0 + row) * Nw + col) = __builtin_convertvector(s, v4b);
+    }
+  }
+  __syncthreads();   // red is free again
+}
+
+template <bool GLU>
+__global__ __launch_bounds__(kThinThreads, 2) void k_gmm_thin(Gmm g) {
+  extern __shared__ int gmm_table[];
+  __shared__ v4f red[kThinWaves * (kThinRows / 16) * 2 * 64];
+  __shared__ int64_t wave_total[kThinWaves];
+  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
+  gmm_plan<kThinThreads>(g, tab, wave_total, [](int n) { return (n + kThinRows - 1) / kThinRows; });
+  const int nn = (GLU ? g.Nw / 2 + kThinW / 2 - 1 : g.Nw + kThinW - 1) / (GLU ? kThinW / 2 : kThinW);
+  const int T = tab.tiles[g.L] * nn;
+  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+    const int m = t / nn, nt = t - m * nn;
+    const int e = gmm_expert(tab, g.L, m);
+    const int first = tab.rows[e];
+    const int row0 = first + (m - tab.tiles[e]) * kThinRows;
+    const int rows = min(tab.rows[e + 1] - row0, kThinRows);
+    if (rows <= 16) thin_tile<GLU, 1, 4>(g, e, row0, rows, nt, red);
+    else if (rows <= 32) thin_tile<GLU, 2, 4>(g, e, row0, rows, nt, red);
+    else if (rows <= 48) thin_tile<GLU, 3, 3>(g, e, row0, rows, nt, red);
+    else thin_tile<GLU, 4, 3>(g, e, row0, rows, nt, red);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows to fp8: one scale per 128 columns, 16 lanes x 8 values per block.
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+
+// rows in use: min(sum of the counts, A)
+__device__ __forceinline__ int64_t rows_in_use(const int64_t* nums, int L, int64_t A) {
+  const int lane = threadIdx.x & 63;
+  int64_t total = 0;
+  for (int e = lane; e < L; e += 64) total += min(max(nums[e], (int64_t)0), A);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);
+  return min(total, A);
+}
+
+// x [rows][128 nb] bf16 -> q, s.  Clears the workspace's status block.
+__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_rows(const v4u* __restrict__ x, uint2* __restrict__ q,
+                                                                  float* __restrict__ s,
+                                                                  const int64_t* __restrict__ nums, int L, int64_t A,
+                                                                  int nb, mdc_device_status* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = mdc_device_status{0, 0, 0, 0};
+  const int64_t n = rows_in_use(nums, L, A) * nb * 16;   // vectors of 8
+  for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < (n + 63) / 64 * 64;
+       i += (int64_t)gridDim.x * kQuantThreads) {
+    const v4u v = i < n ? x[i] : v4u{0u, 0u, 0u, 0u};
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = max(m, max(abs_bits(bf16_lo(v[w])), abs_bits(bf16_hi(v[w]))));
+    const Fp8Scaler f(row16_max(m));
+    if (i < n) {
+      q[i] = uint2{f.codes4(bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])),
+                   f.codes4(bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3]))};
+      if ((i & 15) == 0) s[i >> 4] = f.scale;
+    }
+  }
+}
+
+// g (fp32) -> q, s.  One workgroup per (expert, row), rows strided.
+__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g, uint2* __restrict__ q, float* __restrict__ s,
+                                                                  mdc_device_status* status) {
+  extern __shared__ int gmm_table[];
+  __shared__ int64_t wave_total[kQuantThreads / 64];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = mdc_device_status{0, 0, 0, 0};
+  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
+  gmm_plan<kQuantThreads>(g, tab, wave_total, [](int n) { return n; });   // here a tile is a row
+  const int nvec = g.Nw / 2 / 8;   // a multiple of 16
+  for (int m = blockIdx.x; m < tab.tiles[g.L]; m += gridDim.x) {
+    const int e = gmm_expert(tab, g.L, m);
+    const int first = tab.rows[e];
+    const int row = first + (m - tab.tiles[e]);
+    const v4f* src = reinterpret_cast<const v4f*>(g.g + (int64_t)row * (g.Nw / 2));
+    for (int i = threadIdx.x; i < (nvec + 63) / 64 * 64; i += kQuantThreads) {
+      const v4f z = {0.f, 0.f, 0.f, 0.f};
+      const v4f a = i < nvec ? src[2 * i] : z, b = i < nvec ? src[2 * i + 1] : z;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = max(mx, max(abs_bits(a[r]), abs_bits(b[r])));
+      const Fp8Scaler f(row16_max(mx));
+      if (i < nvec) {
+        q[(int64_t)row * nvec + i] = uint2{f.codes4(a[0], a[1], a[2], a[3]), f.codes4(b[0], b[1], b[2], b[3])};
+        if ((i & 15) == 0) s[(int64_t)row * (nvec >> 4) + (i >> 4)] = f.scale;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+unsigned device_cus() {
+  int dev = 0, cus = 256;
+  if (hipGetDevice(&dev) == hipSuccess) (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  return (unsigned)cus;
+}
+
+template <bool GLU>
+void launch_gmm(const Gmm& g, hipStream_t s) {
+  const int64_t nn = GLU ? g.Nw / kThinW : (g.Nw + kThinW - 1) / kThinW;
+  const int64_t most = ((int64_t)g.A / kThinRows + g.L) * nn;
+  const unsigned grid = (unsigned)min(most, (int64_t)device_cus() * 8);
+  hipLaunchKernelGGL((k_gmm_thin<GLU>), dim3(grid), dim3(kThinThreads), gmm_table_bytes(g.L), s, g);
+}
+
+constexpr int kMaxK = 1 << 22;   // the rows of a tile are addressed with 32-bit offsets
+
+mdc_status check_gmm(int64_t A, int32_t L, int32_t n, int32_t k) {
+  if (A < 0 || L < 1 || n < 1 || k < 1 || n % 8 != 0 || k % 16 != 0) return MDC_ERR_INVALID;
+  if (L > MDC_MAX_LOCAL_EXPERTS || A > INT32_MAX || (int64_t)n * k > INT32_MAX || k > kMaxK) return MDC_ERR_UNSUPPORTED;
+  if ((A / kThinRows + L + 1) * ((n + kThinW - 1) / kThinW) > INT32_MAX - 65536) return MDC_ERR_UNSUPPORTED;
+  return MDC_OK;
+}
+
+// Workspace: [status block][q1][s1][q2][s2][g].
+struct Ffn8Plan {
+  int64_t A;
+  int H, N, L;
+  size_t off_q1, off_s1, off_q2, off_s2, off_g, bytes;
+};
+
+Ffn8Plan make_ffn8_plan(const mdc_shape* sh, int inter_n) {
+  Ffn8Plan f;
+  f.A = sh->capacity;
+  f.H = sh->hidden;
+  f.N = inter_n;
+  f.L = sh->num_experts / sh->world;
+  const size_t A = (size_t)f.A, H = (size_t)f.H, I = (size_t)f.N / 2;
+  f.off_q1 = MDC_STATUS_BYTES;
+  f.off_s1 = f.off_q1 + round_up(A * H, 256);
+  f.off_q2 = f.off_s1 + round_up(A * (H / kFp8Block) * 4, 256);
+  f.off_s2 = f.off_q2 + round_up(A * I, 256);
+  f.off_g = f.off_s2 + round_up(A * (I / kFp8Block) * 4, 256);
+  f.bytes = f.off_g + round_up(A * I * 4, 256);
+  return f;
+}
+
+mdc_status check_ffn8(const mdc_shape* sh, int inter_n) {
+  mdc_status st = check_shape(sh);
+  if (st != MDC_OK) return st;
+  if (inter_n <= 0) return MDC_ERR_INVALID;
+  if (inter_n % 256 != 0 || sh->hidden % kFp8Block != 0) return MDC_ERR_UNSUPPORTED;
+  const int32_t L = sh->num_experts / sh->world;
+  st = check_gmm(sh->capacity, L, inter_n, sh->hidden);
+  return st != MDC_OK ? st : check_gmm(sh->capacity, L, sh->hidden, inter_n / 2);
+}
+
+mdc_status ffn8_impl(const mdc_shape* shape, int32_t inter_n, const void* expand_x, const void* expand_q,
+                     const float* scales, const int64_t* nums, const void* w1, const float* w1_scale, const void* w2,
+                     const float* w2_scale, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  const mdc_status st = check_ffn8(shape, inter_n);
+  if (st != MDC_OK) return st;
+  const Ffn8Plan f = make_ffn8_plan(shape, inter_n);
+  if (f.A == 0) return MDC_OK;
+  if ((expand_x == nullptr && (expand_q == nullptr || scales == nullptr)) || nums == nullptr || w1 == nullptr ||
+      w1_scale == nullptr || w2 == nullptr || w2_scale == nullptr || y == nullptr || workspace == nullptr)
+    return MDC_ERR_NULLPTR;
+  if (!aligned16(expand_x) || !aligned16(expand_q) || !aligned4(scales) || !aligned8(nums) || !aligned16(w1) ||
+      !aligned4(w1_scale) || !aligned16(w2) || !aligned4(w2_scale) || !aligned16(y) || !aligned16(workspace))
+    return MDC_ERR_INVALID;
+  if (workspace_bytes < f.bytes) return MDC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  mdc_device_status* status = reinterpret_cast<mdc_device_status*>(ws);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const unsigned cus = device_cus();
+  (void)hipGetLastError();
+  const uint8_t* q1 = static_cast<const uint8_t*>(expand_q);
+  if (expand_x != nullptr) {
+    uint2* q = reinterpret_cast<uint2*>(ws + f.off_q1);
+    float* s1 = reinterpret_cast<float*>(ws + f.off_s1);
+    hipLaunchKernelGGL(k_quant_fp8_rows, dim3(cus * 8), dim3(kQuantThreads), 0, s, static_cast<const v4u*>(expand_x),
+                       q, s1, nums, f.L, f.A, f.H / kFp8Block, status);
+    q1 = reinterpret_cast<const uint8_t*>(q);
+    scales = s1;
+  }
+  uint8_t* q2 = reinterpret_cast<uint8_t*>(ws + f.off_q2);
+  float* s2 = reinterpret_cast<float*>(ws + f.off_s2);
+  const Gmm g1{q1, scales, nums, static_cast<const uint8_t*>(w1), w1_scale, nullptr,
+               reinterpret_cast<float*>(ws + f.off_g), (int)f.A, f.L, f.N, f.H, f.H / kFp8Block};
+  launch_gmm<true>(g1, s);
+  hipLaunchKernelGGL(k_quant_fp8_thin, dim3((unsigned)min(f.A, (int64_t)cus * 8)), dim3(kQuantThreads),
+                     gmm_table_bytes(f.L), s, g1, reinterpret_cast<uint2*>(q2), s2, status);
+  const Gmm g2{q2, s2, nums, static_cast<const uint8_t*>(w2), w2_scale, static_cast<uint16_t*>(y), nullptr, (int)f.A,
+               f.L, f.H, f.N / 2, f.N / 2 / kFp8Block};
+  launch_gmm<false>(g2, s);
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+mdc_status mdc_gmm_fp8(int64_t capacity, int32_t experts, int32_t n, int32_t k, const void* a, const float* a_scale,
+                       const int64_t* expert_token_nums, const void* w, const float* w_scale, void* y, void* stream) {
+  const mdc_status st = check_gmm(capacity, experts, n, k);
+  if (st != MDC_OK) return st;
+  if (capacity == 0) return MDC_OK;
+  if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || y == nullptr ||
+      (expert_token_nums == nullptr && experts != 1))
+    return MDC_ERR_NULLPTR;
+  if (!aligned16(a) || !aligned4(a_scale) || !aligned8(expert_token_nums) || !aligned16(w) || !aligned4(w_scale) ||
+      !aligned16(y))
+    return MDC_ERR_INVALID;
+  (void)hipGetLastError();
+  const Gmm g{static_cast<const uint8_t*>(a), a_scale, expert_token_nums, static_cast<const uint8_t*>(w), w_scale,
+              static_cast<uint16_t*>(y), nullptr, (int)capacity, experts, n, k, (k + kFp8Block - 1) / kFp8Block};
+  launch_gmm<false>(g, static_cast<hipStream_t>(stream));
+  return launched();
+}
+
+mdc_status mdc_ffn_fp8_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes) {
+  if (bytes == nullptr) return MDC_ERR_NULLPTR;
+  const mdc_status st = check_ffn8(shape, inter_n);
+  if (st != MDC_OK) return st;
+  *bytes = make_ffn8_plan(shape, inter_n).bytes;
+  return MDC_OK;
+}
+
+mdc_status mdc_ffn_fp8(const mdc_shape* shape, int32_t inter_n, const void* expand_x, const int64_t* expert_token_nums,
+                       const void* w1, const float* w1_scale, const void* w2, const float* w2_scale, void* y,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return ffn8_impl(shape, inter_n, expand_x, nullptr, nullptr, expert_token_nums, w1, w1_scale, w2, w2_scale, y,
+                   workspace, workspace_bytes, stream);
+}
+
+mdc_status mdc_ffn_fp8_quant_input(const mdc_shape* shape, int32_t inter_n, const void* expand_q,
+                                   const float* dynamic_scales, const int64_t* expert_token_nums, const void* w1,
+                                   const float* w1_scale, const void* w2, const float* w2_scale, void* y,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return ffn8_impl(shape, inter_n, nullptr, expand_q, dynamic_scales, expert_token_nums, w1, w1_scale, w2, w2_scale, y,
+                   workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

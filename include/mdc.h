@@ -506,6 +506,210 @@ mdc_status mdc_dispatch_ffn(const mdc_shape* shape,
                             void* ffn_workspace, size_t ffn_workspace_bytes,
                             void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the exchange: gate, residual + RMS norm, and the
+ * fp8 products.  They follow the conventions above: caller-owned device
+ * buffers, work enqueued on `stream` of the current device, argument errors
+ * returned before anything is enqueued, bitwise deterministic results, no
+ * allocation and no synchronisation (every call can be captured into a
+ * graph).  16-bit and 8-bit tensors and their scales are contiguous.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    MDC_DTYPE_BF16 = 0,
+    MDC_DTYPE_FP16 = 1,
+    MDC_DTYPE_FP32 = 2
+} mdc_dtype;
+
+/* ------------------------------------------------------------------------
+ * Gate: the routes and weights that dispatch and combine take, from the
+ * router's logits.
+ *
+ * For each of the W*BS tokens, over its n = E + Z + C ids (routed, zero and
+ * copy experts):
+ *   z    = its logits in fp32.  NaN and -inf turn an id off: it is never
+ *          chosen.  +inf counts as the largest finite value.
+ *   p    = softmax(z) over the ids that are on, or sigmoid(z) id by id
+ *   key  = p + bias (bias NULL: p; a key that is NaN or -inf turns the id
+ *          off too).  The bias steers the choice and has no part in the weight.
+ *   groups > 1: the ids form `groups` equal runs; a run's score is the sum of
+ *          its group_top (1 or 2) largest keys, -inf where it has fewer; only
+ *          the topk_groups runs of largest score (ties: the lower run) stay
+ *          open.
+ *   expert_ids    = the K open ids of largest key in that order, ties to the
+ *          lowest id; -1 where fewer than K are on (the dispatch drops
+ *          such a route and, if it is active, counts it in dropped_ids)
+ *   expert_scales = p of the chosen ids; with renormalise divided by
+ *          their sum (all zero if that is zero); times scale.  0 for id -1.
+ * The choice is the one exact arithmetic makes: with softmax or sigmoid keys
+ * whose fp32 values are too close to tell apart, a token is decided in 64
+ * bits.  Weights are computed in fp32.
+ *
+ *   logits        [W][BS][n], of params->dtype
+ *   bias          [n] fp32 or NULL
+ *   expert_ids    [W][BS][K] int32,  expert_scales [W][BS][K] fp32: written
+ * n <= MDC_MAX_GATE_EXPERTS and groups <= MDC_MAX_GATE_GROUPS (else
+ * MDC_ERR_UNSUPPORTED); groups must divide n, and the open groups must hold K
+ * ids.  Only world, bs, topk and the expert counts of shape are used
+ * (all of it is checked).
+ * ------------------------------------------------------------------------ */
+#define MDC_GATE_SOFTMAX 0
+#define MDC_GATE_SIGMOID 1
+#define MDC_MAX_GATE_EXPERTS 2048
+#define MDC_MAX_GATE_GROUPS 64
+
+typedef struct {
+    int32_t dtype;        /* mdc_dtype of the logits */
+    int32_t score;        /* MDC_GATE_SOFTMAX or MDC_GATE_SIGMOID */
+    int32_t groups;       /* 1: no groups */
+    int32_t topk_groups;  /* 1..groups */
+    int32_t group_top;    /* 1 or 2, at most the ids of a group */
+    int32_t renormalise;  /* 0 or 1 */
+    float scale;          /* finite */
+} mdc_gate_params;
+
+mdc_status mdc_gate(const mdc_shape* shape,
+                    const mdc_gate_params* params,
+                    const void* logits,
+                    const float* bias,
+                    int32_t* expert_ids,
+                    float* expert_scales,
+                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition and RMS norm, with outputs in 16 and in 8 bits: what
+ * stands between one layer's combine (x) and the next gate, dispatch and
+ * expert products.  For each row, in fp32:
+ *   h  = x + residual (residual NULL: x)
+ *   residual_out = h rounded to residual_dtype
+ *   v  = h / sqrt(mean(h^2) + eps) * weight        (of the unrounded h)
+ *   y  = v rounded to dtype
+ *   q, q_scale = v in 8 bits (of the unrounded v):
+ *     MDC_QUANT_INT8: one scale per row, as the quantised dispatch: amax =
+ *       max|v|, q = clamp(rint(v * (127 / amax)), -127, 127), q_scale[row] =
+ *       amax / 127; the form mdc_ffn_quant_input takes
+ *     MDC_QUANT_FP8: e4m3 (OCP), one scale per 128 columns (the last run of
+ *       a row may be shorter): amax = max(max|v|, 2^-110), q = rne_e4m3(448 v
+ *       / amax), q_scale[row][ceil(H / 128)] = amax / 448; the form
+ *       mdc_gmm_fp8 and mdc_ffn_fp8_quant_input take
+ *     Zeros give codes 0 and scale 0.  A row or run that holds NaN or an
+ *     infinity has a scale, and in fp8 codes, that are not finite.
+ *
+ *   x [rows][H] and y of dtype (bf16 or fp16); residual, residual_out of
+ *   residual_dtype, weight [H] of weight_dtype (each dtype or fp32); q [rows][H]
+ * residual may be NULL (then x is normalised as it is; residual_out, if given,
+ * receives x in residual_dtype); residual_out, y and q may each be NULL, not
+ * all of them.  residual_out may be residual or x itself, y may be x
+ * itself (each element is read before it is written, by one thread); other
+ * overlaps are not allowed.  H must be a multiple of 8 (INVALID) and at most
+ * MDC_MAX_NORM_HIDDEN (UNSUPPORTED); the rows' tensors are 16-byte aligned,
+ * q 8-byte.
+ * ------------------------------------------------------------------------ */
+#define MDC_QUANT_NONE 0
+#define MDC_QUANT_INT8 1
+#define MDC_QUANT_FP8 2
+#define MDC_MAX_NORM_HIDDEN 32768
+
+typedef struct {
+    int64_t rows;           /* >= 0, below 2^31 */
+    int32_t hidden;         /* H */
+    int32_t dtype;          /* MDC_DTYPE_BF16 or MDC_DTYPE_FP16 */
+    int32_t residual_dtype; /* dtype or MDC_DTYPE_FP32 */
+    int32_t weight_dtype;   /* dtype or MDC_DTYPE_FP32 */
+    int32_t quant;          /* MDC_QUANT_*; NONE: q and q_scale are NULL */
+    float eps;              /* finite, >= 0 */
+} mdc_norm_params;
+
+mdc_status mdc_add_rms_norm(const mdc_norm_params* params,
+                            const void* x,
+                            const void* residual,
+                            const void* weight,
+                            void* residual_out,
+                            void* y,
+                            void* q,
+                            float* q_scale,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * Grouped product in fp8 (e4m3, OCP) with a scale for each block of 128.
+ *
+ * Rows [0, min(sum(expert_token_nums), A)) of a, grouped by expert in order as
+ * the dispatch lays them out, each times its expert's weights:
+ *   y[r][c] = bf16_rne( sum over k-blocks b of a_scale[r][b] *
+ *             w_scale[e][c / 128][b] * sum over k in block b of
+ *             a[r][k] * w[e][c][k] ),  c < n
+ * Products and sums are fp32; a k-block is 128 columns, the last one K % 128
+ * where that is not zero.  Scales are any fp32 values.
+ *
+ *   a [A][K] e4m3, a_scale [A][ceil(K/128)] fp32, w [L][n][K] e4m3,
+ *   w_scale [L][ceil(n/128)][ceil(K/128)] fp32, y [A][n] bf16 (rows past the
+ *   total are untouched); expert_token_nums [L] int64, or NULL when L == 1:
+ *   all A rows.  Negative counts are read as zero.
+ * a, w and y are 16-byte aligned.  K must be a multiple of 16 and n of 8, both
+ * positive (else MDC_ERR_INVALID); n * K < 2^31, K <= 2^22, L <=
+ * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and the tile count (A / 64 + L + 1) * ceil(n / 32) below 2^31 (else
+ * MDC_ERR_UNSUPPORTED).  No workspace.
+ * ------------------------------------------------------------------------ */
+mdc_status mdc_gmm_fp8(int64_t capacity,
+                       int32_t experts,
+                       int32_t n,
+                       int32_t k,
+                       const void* a,
+                       const float* a_scale,
+                       const int64_t* expert_token_nums,
+                       const void* w,
+                       const float* w_scale,
+                       void* y,
+                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * Grouped expert FFN in fp8: mdc_ffn with e4m3 weights and activations and a
+ * scale for each block of 128, e the row's local expert:
+ *   q1, s1 = x in fp8, one scale per 128 columns (as MDC_QUANT_FP8 above)
+ *   h      = the product of mdc_gmm_fp8 with w1[e], kept in fp32
+ *   g      = silu(h[:, j]) * h[:, j + N/2], j < N/2, in fp32
+ *   q2, s2 = g in fp8 (not rounded to 16 bits before)
+ *   y      = bf16_rne of the product with w2[e]
+ * silu(a) = a / (1 + exp(-a)) with the hardware exp and reciprocal.
+ *
+ *   expand_x [A][H] bf16, expert_token_nums [L] int64, w1 [L][N][H] e4m3,
+ *   w1_scale [L][N/128][H/128] fp32, w2 [L][H][N/2] e4m3, w2_scale
+ *   [L][H/128][N/256] fp32, y [A][H] bf16 (rows past the total are untouched)
+ * inter_n = N must be a positive multiple of 256 and H a multiple of 128; the
+ * bounds of mdc_gmm_fp8 hold for both products.  The workspace (size from
+ * mdc_ffn_fp8_workspace) holds the status block (all zero: nothing in this
+ * call can fail on the data), q1, s1, q2, s2 and g of experts with few rows.
+ * The flags of shape are checked and otherwise ignored.
+ *
+ * mdc_ffn_fp8_quant_input takes rows already in fp8: expand_q [A][H] e4m3 and
+ * dynamic_scales [A][H/128] (mdc_add_rms_norm's q and q_scale).
+ * ------------------------------------------------------------------------ */
+mdc_status mdc_ffn_fp8_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes);
+
+mdc_status mdc_ffn_fp8(const mdc_shape* shape,
+                       int32_t inter_n,
+                       const void* expand_x,
+                       const int64_t* expert_token_nums,
+                       const void* w1,
+                       const float* w1_scale,
+                       const void* w2,
+                       const float* w2_scale,
+                       void* y,
+                       void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+mdc_status mdc_ffn_fp8_quant_input(const mdc_shape* shape,
+                                   int32_t inter_n,
+                                   const void* expand_q,
+                                   const float* dynamic_scales,
+                                   const int64_t* expert_token_nums,
+                                   const void* w1,
+                                   const float* w1_scale,
+                                   const void* w2,
+                                   const float* w2_scale,
+                                   void* y,
+                                   void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
