@@ -22,6 +22,7 @@ namespace {
 // ---------------------------------------------------------------------------
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
 
@@ -41,7 +42,9 @@ struct Gmm {
   const uint8_t* w;        // [L][Nw][K] e4m3
   const float* w_scale;    // [L][ceil(Nw / 128)][nk]
   uint16_t* y;             // [A][Nw] bf16
-  float* g;                // SwiGLU: [A][Nw / 2] fp32
+  float* g;                // SwiGLU of experts with few rows: [thin rows][Nw / 2] fp32 (thin_row)
+  uint8_t* q;              // SwiGLU of the others: [A][Nw / 2] e4m3
+  float* q_scale;          // [A][Nw / 256]
   int A, L, Nw, K, nk;
 };
 
@@ -128,6 +131,13 @@ constexpr int kThinRows = 64;
 constexpr int kThinThreads = 256;
 constexpr int kThinWaves = kThinThreads / 64;
 constexpr int kThinW = 32;   // weight rows of a tile
+
+// Row of the fp32 buffer that holds SwiGLU outputs until they are quantised:
+// the row itself, or one of its expert's own where that needs less memory.
+__host__ __device__ inline int64_t thin_rows(int64_t A, int64_t L) { return A < L * kThinRows ? A : L * kThinRows; }
+__device__ __forceinline__ int64_t thin_row(const Gmm& g, int e, int row0, int row) {
+  return g.A < (int64_t)g.L * kThinRows ? row0 + row : e * kThinRows + row;
+}
 
 template <bool GLU, int MB, int DEPTH>
 __device__ __forceinline__ void thin_tile(const Gmm& g, int e, int row0, int rows, int nt, v4f* red) {
@@ -235,7 +245,7 @@ __device__ __forceinline__ void thin_tile(const Gmm& g, int e, int row0, int row
       for (int r = 0; r < 4; ++r) out[r] = gmm_silu(gate[r]) * up[r];
       const int row = 16 * i + r16;
       if (row < rows)
-        *reinterpret_cast<v4f*>(g.g + (int64_t)(row0 + row) * (Nw / 2) + n0 + 4 * quad) = out;
+        *reinterpret_cast<v4f*>(g.g + thin_row(g, e, row0, row) * (Nw / 2) + n0 + 4 * quad) = out;
     }
   } else {
     for (int i = wave; i < 2 * MB; i += kThinWaves) {
@@ -254,19 +264,337 @@ __global__ __launch_bounds__(kThinThreads, 2) void k_gmm_thin(Gmm g) {
   __shared__ v4f red[kThinWaves * (kThinRows / 16) * 2 * 64];
   __shared__ int64_t wave_total[kThinWaves];
   const GmmTable tab{gmm_table, gmm_table + g.L + 1};
-  gmm_plan<kThinThreads>(g, tab, wave_total, [](int n) { return (n + kThinRows - 1) / kThinRows; });
+  gmm_plan<kThinThreads>(g, tab, wave_total, [](int n) { return n > 0 && n <= kThinRows ? 1 : 0; });
   const int nn = (GLU ? g.Nw / 2 + kThinW / 2 - 1 : g.Nw + kThinW - 1) / (GLU ? kThinW / 2 : kThinW);
   const int T = tab.tiles[g.L] * nn;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
     const int m = t / nn, nt = t - m * nn;
     const int e = gmm_expert(tab, g.L, m);
-    const int first = tab.rows[e];
-    const int row0 = first + (m - tab.tiles[e]) * kThinRows;
-    const int rows = min(tab.rows[e + 1] - row0, kThinRows);
+    const int row0 = tab.rows[e], rows = tab.rows[e + 1] - row0;
     if (rows <= 16) thin_tile<GLU, 1, 4>(g, e, row0, rows, nt, red);
     else if (rows <= 32) thin_tile<GLU, 2, 4>(g, e, row0, rows, nt, red);
     else if (rows <= 48) thin_tile<GLU, 3, 3>(g, e, row0, rows, nt, red);
     else thin_tile<GLU, 4, 3>(g, e, row0, rows, nt, red);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Experts with more rows: tiles of BM rows x 256 weight rows (SwiGLU: 128 gate
+// rows and the 128 up rows that go with them), one workgroup of eight
+// wavefronts per CU walking tiles.  Each k-block of 128 is one stage, loaded
+// global -> LDS directly into one of two stage arrays while the other is
+// multiplied.  Wavefront (wt, wn) holds token blocks 2 i + wt (16 rows each, so
+// that a short tile's blocks are shared) x 64 weight rows.
+//
+// LDS: chunk c (16 bytes) of row r sits at chunk c ^ ((r / 2) & 7) of the row's
+// 128 bytes, so that 16 rows read at one chunk cover all banks.  A direct load
+// writes lane l's 16 bytes at base + 16 l: eight rows per wavefront load, lane
+// l taking row l / 8 and the chunk that belongs in slot l % 8.
+//
+// The scales sa[row][b] sw[.][b] lie behind the rows of the stage array that
+// k-block b uses (two deep): thread (weight half, row) loads, multiplies and
+// stores those of two k-blocks every second stage.  They are not an array of
+// their own because the compiler makes reads of LDS that no direct load writes
+// wait for every direct load in flight.
+// ---------------------------------------------------------------------------
+constexpr int kWideThreads = 512;
+constexpr int kWideW = 256;                      // weight rows of a tile
+constexpr int kWideRows = 256;                   // token rows of a tile, at most
+constexpr int kWideScales = 2 * kWideRows;       // floats: one k-block's scales, [weight half][row]
+constexpr int kWideData = (kWideRows + kWideW) * kFp8Block;
+constexpr int kWideStage = kWideData + 2 * kWideScales * 4;
+
+struct WideSmem {
+  uint8_t* l0;    // kWideStage bytes: even k-blocks (rows, then scales of k-block b at slot b / 2 % 2)
+  uint8_t* l1;    // odd k-blocks
+};
+
+struct WideTile {
+  int e, row0, rows, n0;   // n0: first weight row (SwiGLU: first output column)
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// The k loop: acc[i][j] = token block 2 i + wt times weight block j of the
+// wavefront.  NB: token blocks computed (the others hold no rows).
+template <bool GLU, int BM, int NB>
+__device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, const WideSmem& sm,
+                                           v4f (&acc)[BM / 32][4]) {
+  constexpr int kTokenBytes = BM * kFp8Block;
+  constexpr int kTokenLoads = BM / 64;   // direct loads of token rows per wavefront and stage (8 rows each)
+  constexpr unsigned kOut = 0x80000000u;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wt = wave >> 2, wn = wave & 3;
+  const int K = g.K, nk = g.nk, Nw = g.Nw;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.a + (int64_t)t.row0 * K), (short)0, t.rows * K, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(g.a_scale + (int64_t)t.row0 * nk), (short)0, t.rows * nk * 4, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.w + ((int64_t)t.e * Nw + t.n0) * K), (short)0, (Nw - t.n0) * K, 0x00020000);
+
+  // ---- loads ----
+  unsigned vo[2], chunk[2];   // lane part of a load of eight rows, by the parity of its place
+#pragma unroll
+  for (int par = 0; par < 2; ++par) {
+    chunk[par] = (unsigned)(((lane & 7) ^ ((4 * par + (lane >> 4)) & 7)) << 4);
+    vo[par] = (unsigned)((lane >> 3) * K) + chunk[par];
+  }
+  const unsigned up = GLU && wave >= 4 ? (unsigned)((Nw / 2 - kWideW / 2) * K) : 0u;   // weight rows 128 .. 255
+  auto dma = [&](uint8_t* buf, int b) {   // (no branches here and below: they would split the schedule)
+    unsigned v[2];
+    const unsigned k0 = (unsigned)b * kFp8Block;
+#pragma unroll
+    for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kOut;   // zeros past K
+#pragma unroll
+    for (int j = 0; j < kTokenLoads; ++j) {
+      const int blk = kTokenLoads * wave + j;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(buf + blk * 1024), 16, v[blk & 1],
+                                               k0 + (unsigned)(8 * blk * K), 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int blk = 4 * wave + j;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(buf + kTokenBytes + blk * 1024), 16, v[j & 1],
+                                               k0 + (unsigned)(8 * blk * K) + up, 0, 0);
+    }
+  };
+
+  // ---- scales of k-blocks b, b + 1 (b even): thread (half, row) ----
+  const int wb = (Nw + kFp8Block - 1) / kFp8Block;
+  const int srow = tid & (BM - 1), half = __builtin_amdgcn_readfirstlane(tid / BM) & 1;   // (BM = 128: in pairs)
+  const int wblock = GLU ? (t.n0 + (half ? Nw / 2 : 0)) / kFp8Block : min(t.n0 / kFp8Block + half, wb - 1);
+  const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(g.w_scale + ((int64_t)t.e * wb + wblock) * nk), (short)0, nk * 4, 0x00020000);
+  v2f sa, sw;
+  auto scale_load = [&](int b) {
+    sa = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rs, (unsigned)(srow * nk) * 4u, (unsigned)b * 4u, 0));
+    sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, 0, (unsigned)b * 4u, 0));
+  };
+  auto scale_store = [&](int b) {
+    const int at = kWideData + (((b >> 1) & 1) * kWideScales + half * kWideRows + srow) * 4;
+    *reinterpret_cast<float*>(sm.l0 + at) = b < nk ? sa[0] * sw[0] : 0.f;
+    *reinterpret_cast<float*>(sm.l1 + at) = b + 1 < nk ? sa[1] * sw[1] : 0.f;
+  };
+
+  // ---- fragments ----
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int key = (lane >> 1) & 7;
+  const int f0 = r16 * kFp8Block + ((quad ^ key) << 4), f1 = r16 * kFp8Block + (((4 + quad) ^ key) << 4);
+  auto wrow = [&](int j) {   // first LDS weight row of the wavefront's block j
+    if (GLU) return (j < 2 ? 0 : kWideW / 2 - 32) + 32 * wn + 16 * j;
+    return 64 * wn + 16 * j;
+  };
+  auto wfrag = [&](const uint8_t* buf, int j) {
+    const uint8_t* p = buf + kTokenBytes + wrow(j) * kFp8Block;
+    return join(*reinterpret_cast<const v4i*>(p + f0), *reinterpret_cast<const v4i*>(p + f1));
+  };
+  auto tfrag = [&](const uint8_t* buf, int i) {
+    const uint8_t* p = buf + (32 * i + 16 * wt) * kFp8Block;
+    return join(*reinterpret_cast<const v4i*>(p + f0), *reinterpret_cast<const v4i*>(p + f1));
+  };
+  const int f_sc = kWideData + ((GLU ? 0 : (wn >> 1) * kWideRows) + 16 * wt + r16) * 4;
+  struct Sc {
+    float s[GLU ? 2 : 1];
+  };
+  auto scale = [&](const uint8_t* buf, int b, int i) {
+    const float* p = reinterpret_cast<const float*>(buf + f_sc + ((b >> 1) & 1) * kWideScales * 4) + 32 * i;
+    Sc s;
+#pragma unroll
+    for (int h = 0; h < (GLU ? 2 : 1); ++h) s.s[h] = p[h * kWideRows];
+    return s;
+  };
+  auto add = [&](v4f& c, const v4f& p, float f) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(p[r], f, c[r]);
+  };
+
+  dma(sm.l0, 0);
+  scale_load(0);
+  scale_store(0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the loads into l0 have landed
+  __syncthreads();
+  dma(sm.l1, 1);
+  scale_load(2);
+  v8i w[4], tok = tfrag(sm.l0, 0), tok_next;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = wfrag(sm.l0, j);
+  Sc s_prev{}, s_cur = scale(sm.l0, 0, 0), s_next;
+  v4f p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = v4f{0.f, 0.f, 0.f, 0.f};
+  // Each step issues one matrix instruction and adds the result of the one
+  // three steps before, across token blocks and stages.
+  auto stage = [&](uint8_t* cur, uint8_t* nxt, int b, bool odd) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (i + 1 < NB) {
+        tok_next = tfrag(cur, i + 1);
+        s_next = scale(cur, b, i + 1);
+      } else {
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wavefront's loads into nxt have landed
+        if (odd) scale_store(b + 1);          // (loaded two stages before)
+        __syncthreads();
+        dma(cur, b + 2);
+        if (odd) scale_load(b + 3);
+        tok_next = tfrag(nxt, 0);   // (after the last stage: read, never used)
+        s_next = scale(nxt, b + 1, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = mfma_block(w[j], tok);
+        if (i + 1 == NB) w[j] = wfrag(nxt, j);
+        if (j < 3) add(acc[(i + NB - 1) % NB][j + 1], p[j + 1], s_prev.s[GLU ? (j + 1) >> 1 : 0]);
+        else add(acc[i][0], p[0], s_cur.s[0]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      tok = tok_next;
+      s_prev = s_cur;
+      s_cur = s_next;
+    }
+  };
+  for (int b = 0; b < nk; b += 2) {   // (past an odd last k-block comes one of zeros)
+    stage(sm.l0, sm.l1, b, false);
+    stage(sm.l1, sm.l0, b + 1, true);
+  }
+#pragma unroll
+  for (int j = 1; j < 4; ++j) add(acc[NB - 1][j], p[j], s_prev.s[GLU ? j >> 1 : 0]);
+}
+
+// One tile: the k loop, then the outputs through LDS as whole rows.
+template <bool GLU, int BM>
+__device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const WideSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wt = wave >> 2, wn = wave & 3;
+  const int r16 = lane & 15, quad = lane >> 4;
+  v4f acc[BM / 32][4];
+#pragma unroll
+  for (int i = 0; i < BM / 32; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (t.rows > BM * 3 / 4) wide_kloop<GLU, BM, BM / 32>(g, t, sm, acc);
+  else if (t.rows > BM / 2) wide_kloop<GLU, BM, BM * 3 / 128>(g, t, sm, acc);
+  else if (t.rows > BM / 4) wide_kloop<GLU, BM, BM / 64>(g, t, sm, acc);
+  else wide_kloop<GLU, BM, BM / 128>(g, t, sm, acc);
+  __syncthreads();   // every wavefront has left the stage arrays
+  if (GLU) {
+    // g = silu(gate) * up (columns 32 wn + 16 j + 4 quad + r), its row maxima
+    // over the 128 columns, and the codes
+    uint32_t* top = reinterpret_cast<uint32_t*>(sm.l1);   // [4][kWideRows]
+#pragma unroll
+    for (int i = 0; i < BM / 32; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[i][j][r] = gmm_silu(acc[i][j][r]) * acc[i][j + 2][r];
+          m = max(m, abs_bits(acc[i][j][r]));
+        }
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      if (quad == 0) top[wn * kWideRows + 32 * i + 16 * wt + r16] = m;
+    }
+    __syncthreads();
+    const int nb2 = g.Nw / 2 / kFp8Block;
+#pragma unroll
+    for (int i = 0; i < BM / 32; ++i) {
+      const int row = 32 * i + 16 * wt + r16;
+      uint32_t m = top[row];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) m = max(m, top[w * kWideRows + row]);
+      const Fp8Scaler f(m);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int unit = 2 * wn + j;   // 16 columns
+        *reinterpret_cast<uint32_t*>(sm.l0 + row * kFp8Block + ((unit ^ (row & 7)) << 4) + 4 * quad) =
+            f.codes4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+      }
+      if (wn == 0 && quad == 0 && row < t.rows) g.q_scale[(int64_t)(t.row0 + row) * nb2 + t.n0 / kFp8Block] = f.scale;
+    }
+    __syncthreads();
+    for (int r = tid >> 3; r < t.rows; r += kWideThreads / 8) {
+      const int unit = tid & 7;
+      *reinterpret_cast<v4u*>(g.q + (int64_t)(t.row0 + r) * (g.Nw / 2) + t.n0 + 16 * unit) =
+          *reinterpret_cast<const v4u*>(sm.l0 + r * kFp8Block + ((unit ^ (r & 7)) << 4));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < BM / 32; ++i) {
+      const int row = 32 * i + 16 * wt + r16;
+      uint8_t* line = (row < 128 ? sm.l0 : sm.l1) + (row & 127) * 512;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int unit = 8 * wn + 2 * j + (quad >> 1);   // 8 columns
+        *reinterpret_cast<v4b*>(line + ((unit ^ (row & 31)) << 4) + 8 * (quad & 1)) =
+            __builtin_convertvector(acc[i][j], v4b);
+      }
+    }
+    __syncthreads();
+    const int unit = tid & 31, col = t.n0 + 8 * unit;
+    if (col < g.Nw)
+      for (int r = tid >> 5; r < t.rows; r += kWideThreads / 32)
+        *reinterpret_cast<v4u*>(g.y + (int64_t)(t.row0 + r) * g.Nw + col) =
+            *reinterpret_cast<const v4u*>((r < 128 ? sm.l0 : sm.l1) + (r & 127) * 512 + ((unit ^ (r & 31)) << 4));
+  }
+  __syncthreads();   // the stage arrays are free
+}
+
+// Tile number -> place.  The m-tiles of an expert run in chunks of up to 8,
+// and a chunk's tiles in groups of h m-tiles x 32 / h n-tiles, m fastest, so
+// that the about 32 tiles an XCD runs at a time share rows and weights in its
+// L2.
+__device__ __forceinline__ WideTile wide_place(const Gmm& g, const GmmTable& tab, int t, int nn, int BM, int cols) {
+  const int m = t / nn;
+  const int e = gmm_expert(tab, g.L, m);
+  const int m_first = tab.tiles[e], m_end = tab.tiles[e + 1];
+  const int c0 = m_first + (m - m_first) / 8 * 8;
+  const int h = min(8, m_end - c0);
+  const int r = t - c0 * nn;
+  const int gn = 32 / h, band = h * gn;
+  const int ng = r / band, r2 = r - ng * band;
+  const int q = r2 / h;
+  const int mt = c0 + (r2 - q * h);
+  WideTile w;
+  w.e = e;
+  w.row0 = __builtin_amdgcn_readfirstlane(tab.rows[e] + (mt - m_first) * BM);
+  w.rows = __builtin_amdgcn_readfirstlane(min(tab.rows[e + 1] - w.row0, BM));
+  w.n0 = __builtin_amdgcn_readfirstlane((ng * gn + q) * cols);
+  return w;
+}
+
+template <bool GLU, int BM>
+__device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, const WideSmem& sm) {
+  constexpr int kCols = GLU ? kWideW / 2 : kWideW;
+  const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
+  const int T = tab.tiles[g.L] * nn;
+  const int G = gridDim.x, b = blockIdx.x;
+  // workgroup b runs on XCD b % 8: each XCD walks a run of consecutive tiles
+  for (int t = (b % 8) * (G / 8) + b / 8; t < T; t += G) wide_tile<GLU, BM>(g, wide_place(g, tab, t, nn, BM, kCols), sm);
+}
+
+template <bool GLU>
+__global__ __launch_bounds__(kWideThreads) void k_gmm_wide(Gmm g) {
+  extern __shared__ int gmm_table[];
+  __shared__ __attribute__((aligned(16))) uint8_t l0[kWideStage];
+  __shared__ __attribute__((aligned(16))) uint8_t l1[kWideStage];
+  __shared__ int64_t wave_total[kWideThreads / 64];
+  const WideSmem sm{l0, l1};
+  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
+  gmm_plan<kWideThreads>(g, tab, wave_total, [](int n) { return n > kThinRows ? (n + 255) / 256 : 0; });
+  constexpr int kCols = GLU ? kWideW / 2 : kWideW;
+  const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
+  const int T = tab.tiles[g.L] * nn, G = gridDim.x;
+  if (T == 0) return;
+  // 128-row tiles where 256-row ones leave CUs idle: a 128-row tile takes
+  // about 0.6 of a 256-row one's time and there are at most twice as many
+  if (5 * ((T + G - 1) / G) > 3 * ((2 * T + G - 1) / G)) {
+    gmm_plan<kWideThreads>(g, tab, wave_total, [](int n) { return n > kThinRows ? (n + 127) / 128 : 0; });
+    wide_walk<GLU, 128>(g, tab, sm);
+  } else {
+    wide_walk<GLU, 256>(g, tab, sm);
   }
 }
 
@@ -308,19 +636,18 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_rows(const v4u* __r
 }
 
 // g (fp32) -> q, s.  One workgroup per (expert, row), rows strided.
-__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g, uint2* __restrict__ q, float* __restrict__ s,
-                                                                  mdc_device_status* status) {
+__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g, mdc_device_status* status) {
   extern __shared__ int gmm_table[];
   __shared__ int64_t wave_total[kQuantThreads / 64];
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = mdc_device_status{0, 0, 0, 0};
   const GmmTable tab{gmm_table, gmm_table + g.L + 1};
-  gmm_plan<kQuantThreads>(g, tab, wave_total, [](int n) { return n; });   // here a tile is a row
+  // here a tile is a row
+  gmm_plan<kQuantThreads>(g, tab, wave_total, [](int n) { return n <= kThinRows ? n : 0; });
   const int nvec = g.Nw / 2 / 8;   // a multiple of 16
   for (int m = blockIdx.x; m < tab.tiles[g.L]; m += gridDim.x) {
     const int e = gmm_expert(tab, g.L, m);
-    const int first = tab.rows[e];
-    const int row = first + (m - tab.tiles[e]);
-    const v4f* src = reinterpret_cast<const v4f*>(g.g + (int64_t)row * (g.Nw / 2));
+    const int in = m - tab.tiles[e], row = tab.rows[e] + in;
+    const v4f* src = reinterpret_cast<const v4f*>(g.g + thin_row(g, e, tab.rows[e], in) * (g.Nw / 2));
     for (int i = threadIdx.x; i < (nvec + 63) / 64 * 64; i += kQuantThreads) {
       const v4f z = {0.f, 0.f, 0.f, 0.f};
       const v4f a = i < nvec ? src[2 * i] : z, b = i < nvec ? src[2 * i + 1] : z;
@@ -329,8 +656,9 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g, uint2* 
       for (int r = 0; r < 4; ++r) mx = max(mx, max(abs_bits(a[r]), abs_bits(b[r])));
       const Fp8Scaler f(row16_max(mx));
       if (i < nvec) {
-        q[(int64_t)row * nvec + i] = uint2{f.codes4(a[0], a[1], a[2], a[3]), f.codes4(b[0], b[1], b[2], b[3])};
-        if ((i & 15) == 0) s[(int64_t)row * (nvec >> 4) + (i >> 4)] = f.scale;
+        reinterpret_cast<uint2*>(g.q)[(int64_t)row * nvec + i] =
+            uint2{f.codes4(a[0], a[1], a[2], a[3]), f.codes4(b[0], b[1], b[2], b[3])};
+        if ((i & 15) == 0) g.q_scale[(int64_t)row * (nvec >> 4) + (i >> 4)] = f.scale;
       }
     }
   }
@@ -348,9 +676,13 @@ unsigned device_cus() {
 template <bool GLU>
 void launch_gmm(const Gmm& g, hipStream_t s) {
   const int64_t nn = GLU ? g.Nw / kThinW : (g.Nw + kThinW - 1) / kThinW;
-  const int64_t most = ((int64_t)g.A / kThinRows + g.L) * nn;
-  const unsigned grid = (unsigned)min(most, (int64_t)device_cus() * 8);
-  hipLaunchKernelGGL((k_gmm_thin<GLU>), dim3(grid), dim3(kThinThreads), gmm_table_bytes(g.L), s, g);
+  const unsigned cus = device_cus();
+  // which experts have few rows is known on the device only
+  if (g.A > kThinRows)
+    hipLaunchKernelGGL((k_gmm_wide<GLU>), dim3((cus + 7) / 8 * 8), dim3(kWideThreads), gmm_table_bytes(g.L), s, g);
+  if (g.A <= kThinRows || g.nums != nullptr)
+    hipLaunchKernelGGL((k_gmm_thin<GLU>), dim3((unsigned)min(g.L * nn, (int64_t)cus * 8)), dim3(kThinThreads),
+                       gmm_table_bytes(g.L), s, g);
 }
 
 constexpr int kMaxK = 1 << 22;   // the rows of a tile are addressed with 32-bit offsets
@@ -362,7 +694,7 @@ mdc_status check_gmm(int64_t A, int32_t L, int32_t n, int32_t k) {
   return MDC_OK;
 }
 
-// Workspace: [status block][q1][s1][q2][s2][g].
+// Workspace: [status block][q1][s1][q2][s2][g of experts with few rows].
 struct Ffn8Plan {
   int64_t A;
   int H, N, L;
@@ -381,7 +713,7 @@ Ffn8Plan make_ffn8_plan(const mdc_shape* sh, int inter_n) {
   f.off_q2 = f.off_s1 + round_up(A * (H / kFp8Block) * 4, 256);
   f.off_s2 = f.off_q2 + round_up(A * I, 256);
   f.off_g = f.off_s2 + round_up(A * (I / kFp8Block) * 4, 256);
-  f.bytes = f.off_g + round_up(A * I * 4, 256);
+  f.bytes = f.off_g + round_up((size_t)thin_rows(f.A, f.L) * I * 4, 256);
   return f;
 }
 
@@ -426,12 +758,12 @@ mdc_status ffn8_impl(const mdc_shape* shape, int32_t inter_n, const void* expand
   uint8_t* q2 = reinterpret_cast<uint8_t*>(ws + f.off_q2);
   float* s2 = reinterpret_cast<float*>(ws + f.off_s2);
   const Gmm g1{q1, scales, nums, static_cast<const uint8_t*>(w1), w1_scale, nullptr,
-               reinterpret_cast<float*>(ws + f.off_g), (int)f.A, f.L, f.N, f.H, f.H / kFp8Block};
+               reinterpret_cast<float*>(ws + f.off_g), q2, s2, (int)f.A, f.L, f.N, f.H, f.H / kFp8Block};
   launch_gmm<true>(g1, s);
   hipLaunchKernelGGL(k_quant_fp8_thin, dim3((unsigned)min(f.A, (int64_t)cus * 8)), dim3(kQuantThreads),
-                     gmm_table_bytes(f.L), s, g1, reinterpret_cast<uint2*>(q2), s2, status);
-  const Gmm g2{q2, s2, nums, static_cast<const uint8_t*>(w2), w2_scale, static_cast<uint16_t*>(y), nullptr, (int)f.A,
-               f.L, f.H, f.N / 2, f.N / 2 / kFp8Block};
+                     gmm_table_bytes(f.L), s, g1, status);
+  const Gmm g2{q2, s2, nums, static_cast<const uint8_t*>(w2), w2_scale, static_cast<uint16_t*>(y), nullptr, nullptr, nullptr,
+               (int)f.A, f.L, f.H, f.N / 2, f.N / 2 / kFp8Block};
   launch_gmm<false>(g2, s);
   return launched();
 }
@@ -453,7 +785,7 @@ mdc_status mdc_gmm_fp8(int64_t capacity, int32_t experts, int32_t n, int32_t k, 
     return MDC_ERR_INVALID;
   (void)hipGetLastError();
   const Gmm g{static_cast<const uint8_t*>(a), a_scale, expert_token_nums, static_cast<const uint8_t*>(w), w_scale,
-              static_cast<uint16_t*>(y), nullptr, (int)capacity, experts, n, k, (k + kFp8Block - 1) / kFp8Block};
+              static_cast<uint16_t*>(y), nullptr, nullptr, nullptr, (int)capacity, experts, n, k, (k + kFp8Block - 1) / kFp8Block};
   launch_gmm<false>(g, static_cast<hipStream_t>(stream));
   return launched();
 }
