@@ -25,6 +25,8 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(4))) float scalar_f;   // read by scalar loads
 
 __device__ __forceinline__ v4f mfma_block(v8i w, v8i t) {
   // formats 0, 0: both operands e4m3; no hardware scales
@@ -42,27 +44,36 @@ struct Gmm {
   const uint8_t* w;        // [L][Nw][K] e4m3
   const float* w_scale;    // [L][ceil(Nw / 128)][nk]
   uint16_t* y;             // [A][Nw] bf16
-  float* g;                // SwiGLU of experts with few rows: [thin rows][Nw / 2] fp32 (thin_row)
-  uint8_t* q;              // SwiGLU of the others: [A][Nw / 2] e4m3
+  float* g;                // SwiGLU with split: [A][Nw / 2] fp32
+  uint8_t* q;              // SwiGLU: [A][Nw / 2] e4m3
   float* q_scale;          // [A][Nw / 256]
+  mdc_device_status* status;   // cleared, or NULL
   int A, L, Nw, K, nk;
+  int split;               // SwiGLU: thin experts' outputs go through g
 };
 
 // ---------------------------------------------------------------------------
 // Rows and tiles of the experts.  Every workgroup works out the plan from the
-// counts by itself, in LDS: rows[e], tiles[e] = first row and first m-tile of
-// expert e, e <= L.
+// counts by itself, in LDS.  Experts with at most kThinRows rows, one block of
+// the matrix instruction, are "thin": what counts there is to stream the
+// weights.  The others are "wide".
 // ---------------------------------------------------------------------------
-struct GmmTable {
-  int* rows;    // [L + 1]
-  int* tiles;   // [L + 1]
-};
-constexpr size_t gmm_table_bytes(int L) { return 2 * sizeof(int) * ((size_t)L + 1); }
+constexpr int kGmmThreads = 512;
+constexpr int kGmmWaves = kGmmThreads / 64;
+constexpr int kThinRows = 16;
 
-// Inclusive sum over the workgroup's threads; wave_total holds one value per
-// wavefront and one more.
+struct GmmTable {
+  int* rows;        // [L + 1] first row of expert e
+  int* tiles;       // [L + 1] first m-tile of expert e (tiles of wide experts)
+  uint16_t* thin;   // [L] the thin experts with rows
+  int n_thin;
+};
+constexpr size_t gmm_table_bytes(int L) { return 2 * sizeof(int) * ((size_t)L + 1) + sizeof(uint16_t) * (size_t)L; }
+
+// Inclusive sum over the workgroup's threads, and the sum of all of them.
+// wave_total holds a value per wavefront.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_total, int64_t& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -71,41 +82,54 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_total) {
   }
   if (lane == 63) wave_total[wave] = v;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) v += wave_total[w];
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    const int64_t n = wave_total[w];
+    if (w < wave) v += n;
+    all += n;
+  }
   __syncthreads();
   return v;
 }
 
-// mtiles(n): m-tiles of an expert with n rows.
-template <int THREADS, typename F>
-__device__ __forceinline__ void gmm_plan(const Gmm& g, GmmTable t, int64_t* wave_total, F mtiles) {
-  int64_t carry = 0;
-  int tcarry = 0;
+// Rows of expert e as counted (negative: none).
+__device__ __forceinline__ int64_t gmm_count(const int64_t* nums, int e, int64_t A) {
+  return nums == nullptr ? A : min(max(nums[e], (int64_t)0), A);
+}
+
+// rows[e] of every expert, clipped at A.
+template <int THREADS>
+__device__ __forceinline__ void gmm_rows(const Gmm& g, int* rows, int64_t* wave_total) {
+  int64_t carry = 0, all;
   for (int e0 = 0; e0 < g.L; e0 += THREADS) {
     const int e = e0 + threadIdx.x;
-    int64_t n = 0;
-    if (e < g.L) n = g.nums == nullptr ? g.A : min(max(g.nums[e], (int64_t)0), (int64_t)g.A);
-    const int64_t end = carry + block_scan<THREADS>(n, wave_total);
-    const int hi = (int)min(end, (int64_t)g.A), lo = (int)min(end - n, (int64_t)g.A);
-    const int m = mtiles(hi - lo);
-    const int tend = tcarry + (int)block_scan<THREADS>(m, wave_total);
-    if (e < g.L) {
-      t.rows[e + 1] = hi;
-      t.tiles[e + 1] = tend;
-    }
-    if (e0 + THREADS < g.L) {   // the last thread's ends start the next run
-      if (threadIdx.x == THREADS - 1) {
-        wave_total[0] = end;
-        wave_total[1] = tend;
-      }
-      __syncthreads();
-      carry = wave_total[0];
-      tcarry = (int)wave_total[1];
-      __syncthreads();
-    }
+    const int64_t end = carry + block_scan<THREADS>(e < g.L ? gmm_count(g.nums, e, g.A) : 0, wave_total, all);
+    if (e < g.L) rows[e + 1] = (int)min(end, (int64_t)g.A);
+    carry += all;
   }
-  if (threadIdx.x == 0) t.rows[0] = t.tiles[0] = 0;
+  if (threadIdx.x == 0) rows[0] = 0;
   __syncthreads();
+}
+
+// The thin experts, and tiles[e] with m-tiles of `rows` rows.  Returns the
+// number of m-tiles.
+__device__ __forceinline__ int gmm_tiles(const Gmm& g, GmmTable& t, int rows, int64_t* wave_total) {
+  int64_t carry = 0, all;   // m-tiles so far, and thin experts above 2^32
+  for (int e0 = 0; e0 < g.L; e0 += kGmmThreads) {
+    const int e = e0 + threadIdx.x;
+    const int n = e < g.L ? t.rows[e + 1] - t.rows[e] : 0;
+    const bool thin = n > 0 && n <= kThinRows;
+    const int64_t mine = thin ? (int64_t)1 << 32 : n > 0 ? (n + rows - 1) / rows : 0;
+    const int64_t end = carry + block_scan<kGmmThreads>(mine, wave_total, all);
+    if (e < g.L) t.tiles[e + 1] = (int)(uint32_t)end;
+    if (thin) t.thin[(int)(end >> 32) - 1] = (uint16_t)e;
+    carry += all;
+  }
+  if (threadIdx.x == 0) t.tiles[0] = 0;
+  __syncthreads();
+  t.n_thin = __builtin_amdgcn_readfirstlane((int)(carry >> 32));
+  return __builtin_amdgcn_readfirstlane((int)(uint32_t)carry);
 }
 
 // Expert that m-tile m belongs to: the number of experts whose tiles end at or
@@ -121,161 +145,248 @@ __device__ __forceinline__ int gmm_expert(const GmmTable& t, int L, int m) {
 }
 
 // ---------------------------------------------------------------------------
-// Experts with few rows: what counts is to stream the weights.  A workgroup
-// takes up to 64 rows of an expert and 32 weight rows (SwiGLU: 16 gate rows and
-// the 16 up rows that go with them); its four wavefronts split the k-blocks
-// into four runs and join their sums through LDS.  Weights and rows go from
-// memory straight to registers, DEPTH k-blocks ahead.
+// Thin experts.  A tile is one expert's rows times 16 rs output columns (SwiGLU:
+// of gate and of up): wavefront (rb, kh) takes 16 weight rows of it over the
+// kh-th of ks runs of k-blocks, rs ks = 8, and the runs' sums are joined through
+// LDS.  A workgroup takes a run of consecutive tiles.
+//
+// The weights, which are all that memory has to bring, go global -> LDS
+// directly, eight rows x 128 bytes per instruction, into a ring of each
+// wavefront's own, kThinRing bytes ahead and on into the next tile.  (Loads in
+// the matrix instruction's layout, 16 rows x 64 bytes, cost the address unit 27
+// ns per KB instead of 7 and kept a decode step's weights at 4.0 TB/s.)  The
+// expert's rows stay in registers from tile to tile, kThinRun k-blocks of them.
+//
+// The compiler would make every LDS access wait for every direct load in
+// flight, so the accesses here are written out with their waits: a ring slot is
+// read when at most the loads of the slots behind it are out.  Other memory
+// operations in between only make that wait longer.
+//
+// SwiGLU's outputs are quantised in blocks of 128 columns: a workgroup takes
+// whole blocks and collects them in LDS (Gmm.split: it takes tiles, and their
+// outputs go to memory in fp32, where k_quant_fp8_thin quantises them).
 // ---------------------------------------------------------------------------
-constexpr int kThinRows = 64;
-constexpr int kThinThreads = 256;
-constexpr int kThinWaves = kThinThreads / 64;
-constexpr int kThinW = 32;   // weight rows of a tile
+constexpr unsigned kPastEnd = 0x80000000u;   // an offset past every buffer: loads there read zero
+constexpr int kThinRing = 12288;             // bytes of a wavefront's ring
+constexpr int kThinRun = 8;                  // k-blocks of rows in registers
+constexpr int kLineG = kFp8Block + 4;        // floats of a row of SwiGLU outputs in LDS
 
-// Row of the fp32 buffer that holds SwiGLU outputs until they are quantised:
-// the row itself, or one of its expert's own where that needs less memory.
-__host__ __device__ inline int64_t thin_rows(int64_t A, int64_t L) { return A < L * kThinRows ? A : L * kThinRows; }
-__device__ __forceinline__ int64_t thin_row(const Gmm& g, int e, int row0, int row) {
-  return g.A < (int64_t)g.L * kThinRows ? row0 + row : e * kThinRows + row;
+__device__ __forceinline__ unsigned lds_at(const void* p) { return (unsigned)(size_t)(lds_void*)p; }
+__device__ __forceinline__ void lds_put(unsigned at, v4f v) {
+  asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
 }
+__device__ __forceinline__ v8i lds_get2(unsigned a, unsigned b) {
+  v4i x, y;
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x), "=&v"(y)
+               : "v"(a), "v"(b)
+               : "memory");
+  return join(x, y);
+}
+// a barrier that leaves loads in flight
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <bool GLU, int MB, int DEPTH>
-__device__ __forceinline__ void thin_tile(const Gmm& g, int e, int row0, int rows, int nt, v4f* red) {
+struct ThinSmem {
+  unsigned ring;   // this wavefront's, kThinRing bytes
+  unsigned red;    // [8 wavefronts][1 or 2 blocks][64] v4f
+  unsigned g;      // [kThinRows][kLineG] fp32
+};
+
+template <bool GLU>
+__device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int ks, const ThinSmem& sm) {
+  constexpr int WB = GLU ? 2 : 1;
+  constexpr int kSlot = WB * 2048, kSlots = kThinRing / kSlot;
+  constexpr int kLoads = 2 * WB;   // direct loads of a slot
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
-  const int K = g.K, nk = g.nk, Nw = g.Nw;
-  const int n0 = nt * (GLU ? kThinW / 2 : kThinW);
-  constexpr unsigned kOut = 0x80000000u;   // past every buffer: reads zero
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<float*>(g.a_scale + (int64_t)row0 * nk), (short)0, rows * nk * 4, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.w + (int64_t)e * Nw * K), (short)0, Nw * K, 0x00020000);
+  const int K = g.K, nk = g.nk, Nw = g.Nw, cols = GLU ? Nw / 2 : Nw;
   const int wb = (Nw + kFp8Block - 1) / kFp8Block;
-  const float* ws0 = g.w_scale + ((int64_t)e * wb + n0 / kFp8Block) * nk;
-  const float* ws1 = GLU ? g.w_scale + ((int64_t)e * wb + (Nw / 2 + n0) / kFp8Block) * nk : ws0;
-  // lane offsets of the weight rows and token rows, without k
-  unsigned wo[2], to[MB], so[MB];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int row = (GLU ? n0 + j * (Nw / 2) : n0 + 16 * j) + r16;
-    wo[j] = row < Nw ? (unsigned)row * (unsigned)K : kOut;
-  }
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    to[i] = (unsigned)((16 * i + r16) * K);
-    so[i] = (unsigned)((16 * i + r16) * nk) * 4u;
-  }
-  struct Step {
-    v4i w[2][2], t[MB][2];
-    float sa[MB], sw[2];
+  const int rs = kGmmWaves / ks, rb = wave / ks, kh = wave - rb * ks;
+  const int per = (nk + ks - 1) / ks, kb0 = kh * per;
+  const bool blocks = GLU && !g.split;               // whole 128-column blocks per workgroup
+  const int width = 16 * rs, tiles_per = (cols + width - 1) / width;
+  // this workgroup's tiles: [t0, t1) of n_thin * tiles_per, whole blocks of ks tiles if they are wanted
+  const int grain = blocks ? ks : 1;
+  const int64_t T = (int64_t)tab.n_thin * tiles_per / grain;
+  const int t0 = (int)(T * blockIdx.x / gridDim.x) * grain, t1 = (int)(T * (blockIdx.x + 1) / gridDim.x) * grain;
+  if (t0 == t1) return;
+
+  // ---- weights: tile by tile, step by step ----
+  auto weights = [&](int i) {
+    const int e = __builtin_amdgcn_readfirstlane((int)tab.thin[i]);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.w + (int64_t)e * Nw * K), (short)0, Nw * K,
+                                             0x00020000);
   };
-  auto load = [&](Step& s, int b) {
-    const unsigned k0 = (unsigned)b * kFp8Block + 16u * quad, k1 = k0 + 64u;
-    const bool in0 = k0 < (unsigned)K, in1 = k1 < (unsigned)K;
+  struct {
+    int i, n, step, left;   // place of the expert in the list, first column, step, tiles to come
+  } c = {t0 / tiles_per, (t0 % tiles_per) * width, 0, t1 - t0};
+  __amdgpu_buffer_rsrc_t rw = weights(c.i);
+  unsigned slot = 0;   // of the next load
+  const int lrow = lane >> 3;
+  auto fetch = [&]() {
+    const bool in = c.left > 0;
+    const unsigned k0 = in ? (unsigned)min(kb0 + c.step, nk) * kFp8Block : (unsigned)nk * kFp8Block;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, in0 ? wo[j] + k0 : kOut, 0, 0);
-      s.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, in1 ? wo[j] + k1 : kOut, 0, 0);
+    for (int j = 0; j < WB; ++j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {   // rows 8 h + lane / 8; the chunk whose place lane % 8 is
+        const unsigned chunk = (unsigned)((lane & 7) ^ ((4 * h + (lrow >> 1)) & 7)) << 4;
+        const int row = c.n + 16 * rb + 8 * h + lrow;
+        const bool ok = k0 + chunk < (unsigned)K && row < cols;
+        const unsigned at = ok ? (unsigned)(row + j * (Nw / 2)) * (unsigned)K + k0 + chunk : kPastEnd;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(sm.ring + slot + j * 2048 + h * 1024), 16, at,
+                                                 0, 0, 0);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      s.t[i][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, in0 ? to[i] + k0 : kOut, 0, 0);
-      s.t[i][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, in1 ? to[i] + k1 : kOut, 0, 0);
-      s.sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[i] + (unsigned)b * 4u, 0, 0));
-    }
-    s.sw[0] = ws0[b];
-    s.sw[1] = GLU ? ws1[b] : s.sw[0];
-  };
-  v4f acc[MB][2];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) acc[i][0] = acc[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](const Step& s) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const v8i t = join(s.t[i][0], s.t[i][1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const v4f p = mfma_block(join(s.w[j][0], s.w[j][1]), t);
-        const float sc = s.sa[i] * s.sw[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc, acc[i][j][r]);
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    if (++c.step == per) {
+      c.step = 0;
+      --c.left;
+      c.n += width;
+      if (c.n >= cols) {
+        c.n = 0;
+        if (c.left > 0) rw = weights(++c.i);
       }
     }
   };
-  const int per = (nk + kThinWaves - 1) / kThinWaves;
-  const int beg = min(nk, wave * per), end = min(nk, beg + per);
-  Step ring[DEPTH];
-  if (beg < end) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(ring[d], min(beg + d, end - 1));
-    int b = beg;
-    for (; b + DEPTH <= end; b += DEPTH)
+  for (int d = 0; d < kSlots; ++d) fetch();
+
+  const int key = (r16 >> 1) & 7;
+  const unsigned f0 = sm.ring + r16 * kFp8Block + ((quad ^ key) << 4);
+  const unsigned f1 = sm.ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
+  unsigned read = 0;
+  v8i tok[kThinRun];
+  float sa[kThinRun], sw[WB][kThinRun], sw_next[WB][kThinRun];
+  // weight scales of a tile's run, by scalar loads: they pass by the direct loads' count
+  auto scales = [&](float (&s)[WB][kThinRun], int e, int n, int s0) {
+    const scalar_f* p = (const scalar_f*)(g.w_scale + ((int64_t)e * wb + min((n + 16 * rb) / kFp8Block, wb - 1)) * nk);
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        compute(ring[d]);
-        load(ring[d], min(b + d + DEPTH, end - 1));   // (past the run: its last block again, unused)
+    for (int j = 0; j < WB; ++j)
+#pragma unroll
+      for (int d = 0; d < kThinRun; ++d) s[j][d] = p[(int64_t)j * (wb / 2) * nk + min(kb0 + s0 + d, nk - 1)];
+  };
+  int i = t0 / tiles_per, n0 = (t0 % tiles_per) * width, have = -1, row0 = 0, rows = 0;
+  int e_next = __builtin_amdgcn_readfirstlane((int)tab.thin[i]), e = e_next;
+  scales(sw_next, e, n0, 0);
+  for (int t = t0; t < t1; ++t) {
+    if (i != have) {
+      e = e_next;
+      row0 = __builtin_amdgcn_readfirstlane(tab.rows[e]);
+      rows = __builtin_amdgcn_readfirstlane(tab.rows[e + 1] - row0);
+    }
+#pragma unroll
+    for (int j = 0; j < WB; ++j)
+#pragma unroll
+      for (int d = 0; d < kThinRun; ++d) sw[j][d] = sw_next[j][d];
+    if (t + 1 < t1) {
+      const bool on = n0 + width < cols;   // the next tile is of the same expert
+      if (!on) e_next = __builtin_amdgcn_readfirstlane((int)tab.thin[i + 1]);
+      scales(sw_next, e_next, on ? n0 + width : 0, 0);
+    }
+    v4f acc[WB];
+#pragma unroll
+    for (int j = 0; j < WB; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < per; s0 += kThinRun) {
+      if (s0 != 0) scales(sw, e, n0, s0);
+      if (i != have || per > kThinRun) {
+        // the rows' k-blocks of this run, in the matrix instruction's layout
+        const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float*>(g.a_scale + (int64_t)row0 * nk), (short)0, rows * nk * 4, 0x00020000);
+#pragma unroll
+        for (int d = 0; d < kThinRun; ++d) {
+          const int b = s0 + d < per ? kb0 + s0 + d : nk;
+          const unsigned k0 = (unsigned)b * kFp8Block + 16u * quad, k1 = k0 + 64u, at = (unsigned)(r16 * K);
+          tok[d] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
+                        __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
+          sa[d] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                rq, b < nk ? (unsigned)(r16 * nk + b) * 4u : kPastEnd, 0, 0));
+        }
       }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (b + d < end) compute(ring[d]);
+      for (int d = 0; d < kThinRun; ++d) {
+        if (s0 + d < per) {
+          // vmcnt: at most the loads of the other slots are out
+          __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * kLoads));
+          v8i w[WB];
+#pragma unroll
+          for (int j = 0; j < WB; ++j) w[j] = lds_get2(f0 + read + j * 2048, f1 + read + j * 2048);
+          read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
+          fetch();
+#pragma unroll
+          for (int j = 0; j < WB; ++j) {
+            const v4f p = mfma_block(w[j], tok[d]);
+            const float f = sa[d] * (kb0 + s0 + d < nk ? sw[j][d] : 0.f);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], f, acc[j][r]);
+          }
+        }
+      }
+      have = i;
+    }
+    // join the runs of k-blocks: wavefront ob < rs sums those of block ob
+#pragma unroll
+    for (int j = 0; j < WB; ++j) lds_put(sm.red + ((wave * WB + j) * 64 + lane) * 16, acc[j]);
+    lds_barrier();
+    if (wave < rs) {
+      v4f sum[WB];
+#pragma unroll
+      for (int j = 0; j < WB; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < ks; ++k) {
+        const unsigned at = sm.red + ((wave * ks + k) * WB * 64 + lane) * 16;
+        const v8i p = lds_get2(at, at + (WB - 1) * 1024);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sum[0][r] += __int_as_float(p[r]);
+          if (GLU) sum[WB - 1][r] += __int_as_float(p[4 + r]);
+        }
+      }
+      const int col = n0 + 16 * wave + 4 * quad;
+      if (GLU) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[0][r] = gmm_silu(sum[0][r]) * sum[WB - 1][r];
+        if (blocks) lds_put(sm.g + (r16 * kLineG + col % kFp8Block) * 4, sum[0]);
+        else if (r16 < rows) *reinterpret_cast<v4f*>(g.g + (int64_t)(row0 + r16) * cols + col) = sum[0];
+      } else if (r16 < rows && col < Nw) {
+        *reinterpret_cast<v4b*>(g.y + (int64_t)(row0 + r16) * Nw + col) = __builtin_convertvector(sum[0], v4b);
+      }
+    }
+    lds_barrier();   // the sums have been read, SwiGLU's outputs are there
+    if (blocks && (n0 + width) % kFp8Block == 0 && wave < kThinRows / 4) {
+      // row r = thread / 16, 8 columns per thread (overwritten only behind the next tile's first barrier)
+      const int r = threadIdx.x >> 4, u = threadIdx.x & 15;
+      const unsigned at = sm.g + (r * kLineG + 8 * u) * 4;
+      const v8i v = lds_get2(at, at + 16);
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, (uint32_t)v[k] & 0x7FFFFFFFu);
+      const Fp8Scaler f(row16_max(m));
+      if (r < rows) {
+        const int64_t q = (int64_t)(row0 + r) * (cols / kFp8Block) + n0 / kFp8Block;
+        auto at8 = [&](int k) { return __int_as_float(v[k]); };
+        reinterpret_cast<uint2*>(g.q)[q * 16 + u] =
+            uint2{f.codes4(at8(0), at8(1), at8(2), at8(3)), f.codes4(at8(4), at8(5), at8(6), at8(7))};
+        if (u == 0) g.q_scale[q] = f.scale;
+      }
+    }
+    n0 += width;
+    if (n0 >= cols) {
+      n0 = 0;
+      ++i;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) red[(wave * MB * 2 + i * 2 + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  auto total = [&](int block) {
-    v4f s = red[block * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < kThinWaves; ++w) {
-      const v4f p = red[(w * MB * 2 + block) * 64 + lane];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s[r] += p[r];
-    }
-    return s;
-  };
-  if (GLU) {
-    for (int i = wave; i < MB; i += kThinWaves) {
-      const v4f gate = total(2 * i), up = total(2 * i + 1);
-      v4f out;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) out[r] = gmm_silu(gate[r]) * up[r];
-      const int row = 16 * i + r16;
-      if (row < rows)
-        *reinterpret_cast<v4f*>(g.g + thin_row(g, e, row0, row) * (Nw / 2) + n0 + 4 * quad) = out;
-    }
-  } else {
-    for (int i = wave; i < 2 * MB; i += kThinWaves) {
-      const v4f s = total(i);
-      const int row = 16 * (i >> 1) + r16, col = n0 + 16 * (i & 1) + 4 * quad;
-      if (row < rows && col < Nw)
-        *reinterpret_cast<v4b*>(g.y + (int64_t)(row0 + row) * Nw + col) = __builtin_convertvector(s, v4b);
-    }
-  }
-  __syncthreads();   // red is free again
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
 }
 
-template <bool GLU>
-__global__ __launch_bounds__(kThinThreads, 2) void k_gmm_thin(Gmm g) {
-  extern __shared__ int gmm_table[];
-  __shared__ v4f red[kThinWaves * (kThinRows / 16) * 2 * 64];
-  __shared__ int64_t wave_total[kThinWaves];
-  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
-  gmm_plan<kThinThreads>(g, tab, wave_total, [](int n) { return n > 0 && n <= kThinRows ? 1 : 0; });
-  const int nn = (GLU ? g.Nw / 2 + kThinW / 2 - 1 : g.Nw + kThinW - 1) / (GLU ? kThinW / 2 : kThinW);
-  const int T = tab.tiles[g.L] * nn;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const int m = t / nn, nt = t - m * nn;
-    const int e = gmm_expert(tab, g.L, m);
-    const int row0 = tab.rows[e], rows = tab.rows[e + 1] - row0;
-    if (rows <= 16) thin_tile<GLU, 1, 4>(g, e, row0, rows, nt, red);
-    else if (rows <= 32) thin_tile<GLU, 2, 4>(g, e, row0, rows, nt, red);
-    else if (rows <= 48) thin_tile<GLU, 3, 3>(g, e, row0, rows, nt, red);
-    else thin_tile<GLU, 4, 3>(g, e, row0, rows, nt, red);
-  }
+// ks: at least 6 k-blocks per wavefront, and as many tiles as workgroups.
+__device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, bool blocks) {
+  int ks = g.nk >= 48 ? 8 : g.nk >= 24 ? 4 : g.nk >= 12 ? 2 : 1;
+  if (!blocks)
+    while (ks < kGmmWaves && experts * ((cols + 128 / ks - 1) / (128 / ks)) < (int)gridDim.x) ks *= 2;
+  return ks;
 }
 
 // ---------------------------------------------------------------------------
@@ -297,7 +408,6 @@ __global__ __launch_bounds__(kThinThreads, 2) void k_gmm_thin(Gmm g) {
 // their own because the compiler makes reads of LDS that no direct load writes
 // wait for every direct load in flight.
 // ---------------------------------------------------------------------------
-constexpr int kWideThreads = 512;
 constexpr int kWideW = 256;                      // weight rows of a tile
 constexpr int kWideRows = 256;                   // token rows of a tile, at most
 constexpr int kWideScales = 2 * kWideRows;       // floats: one k-block's scales, [weight half][row]
@@ -313,8 +423,6 @@ struct WideTile {
   int e, row0, rows, n0;   // n0: first weight row (SwiGLU: first output column)
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-
 // The k loop: acc[i][j] = token block 2 i + wt times weight block j of the
 // wavefront.  NB: token blocks computed (the others hold no rows).
 template <bool GLU, int BM, int NB>
@@ -322,7 +430,6 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
                                            v4f (&acc)[BM / 32][4]) {
   constexpr int kTokenBytes = BM * kFp8Block;
   constexpr int kTokenLoads = BM / 64;   // direct loads of token rows per wavefront and stage (8 rows each)
-  constexpr unsigned kOut = 0x80000000u;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave >> 2, wn = wave & 3;
@@ -346,7 +453,7 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     unsigned v[2];
     const unsigned k0 = (unsigned)b * kFp8Block;
 #pragma unroll
-    for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kOut;   // zeros past K
+    for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kPastEnd;   // zeros past K
 #pragma unroll
     for (int j = 0; j < kTokenLoads; ++j) {
       const int blk = kTokenLoads * wave + j;
@@ -515,7 +622,7 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
       if (wn == 0 && quad == 0 && row < t.rows) g.q_scale[(int64_t)(t.row0 + row) * nb2 + t.n0 / kFp8Block] = f.scale;
     }
     __syncthreads();
-    for (int r = tid >> 3; r < t.rows; r += kWideThreads / 8) {
+    for (int r = tid >> 3; r < t.rows; r += kGmmThreads / 8) {
       const int unit = tid & 7;
       *reinterpret_cast<v4u*>(g.q + (int64_t)(t.row0 + r) * (g.Nw / 2) + t.n0 + 16 * unit) =
           *reinterpret_cast<const v4u*>(sm.l0 + r * kFp8Block + ((unit ^ (r & 7)) << 4));
@@ -535,7 +642,7 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
     __syncthreads();
     const int unit = tid & 31, col = t.n0 + 8 * unit;
     if (col < g.Nw)
-      for (int r = tid >> 5; r < t.rows; r += kWideThreads / 32)
+      for (int r = tid >> 5; r < t.rows; r += kGmmThreads / 32)
         *reinterpret_cast<v4u*>(g.y + (int64_t)(t.row0 + r) * g.Nw + col) =
             *reinterpret_cast<const v4u*>((r < 128 ? sm.l0 : sm.l1) + (r & 127) * 512 + ((unit ^ (r & 31)) << 4));
   }
@@ -575,26 +682,40 @@ __device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, con
   for (int t = (b % 8) * (G / 8) + b / 8; t < T; t += G) wide_tile<GLU, BM>(g, wide_place(g, tab, t, nn, BM, kCols), sm);
 }
 
+// One workgroup per CU: the wide experts' tiles, then the thin experts' groups.
 template <bool GLU>
-__global__ __launch_bounds__(kWideThreads) void k_gmm_wide(Gmm g) {
+__global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   extern __shared__ int gmm_table[];
   __shared__ __attribute__((aligned(16))) uint8_t l0[kWideStage];
   __shared__ __attribute__((aligned(16))) uint8_t l1[kWideStage];
-  __shared__ int64_t wave_total[kWideThreads / 64];
-  const WideSmem sm{l0, l1};
-  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
-  gmm_plan<kWideThreads>(g, tab, wave_total, [](int n) { return n > kThinRows ? (n + 255) / 256 : 0; });
+  __shared__ int64_t wave_total[kGmmWaves];
+  GmmTable tab{gmm_table, gmm_table + g.L + 1, reinterpret_cast<uint16_t*>(gmm_table + 2 * (g.L + 1)), 0};
+  if (g.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *g.status = mdc_device_status{0, 0, 0, 0};
+  gmm_rows<kGmmThreads>(g, tab.rows, wave_total);
   constexpr int kCols = GLU ? kWideW / 2 : kWideW;
   const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
-  const int T = tab.tiles[g.L] * nn, G = gridDim.x;
-  if (T == 0) return;
-  // 128-row tiles where 256-row ones leave CUs idle: a 128-row tile takes
-  // about 0.6 of a 256-row one's time and there are at most twice as many
-  if (5 * ((T + G - 1) / G) > 3 * ((2 * T + G - 1) / G)) {
-    gmm_plan<kWideThreads>(g, tab, wave_total, [](int n) { return n > kThinRows ? (n + 127) / 128 : 0; });
-    wide_walk<GLU, 128>(g, tab, sm);
-  } else {
-    wide_walk<GLU, 256>(g, tab, sm);
+  const int G = gridDim.x;
+  const int T = gmm_tiles(g, tab, 256, wave_total) * nn;
+  if (T != 0) {
+    const WideSmem sm{l0, l1};
+    // 128-row tiles where 256-row ones leave CUs idle: a 128-row tile takes
+    // about 0.6 of a 256-row one's time and there are at most twice as many
+    if (5 * ((T + G - 1) / G) > 3 * ((2 * T + G - 1) / G)) {
+      gmm_tiles(g, tab, 128, wave_total);
+      wide_walk<GLU, 128>(g, tab, sm);
+    } else {
+      wide_walk<GLU, 256>(g, tab, sm);
+    }
+  }
+  if (tab.n_thin != 0) {
+    __syncthreads();   // l0 and l1 are free
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // four wavefronts' rings in each array, then the sums in one and SwiGLU's outputs in the other
+    const ThinSmem sm{lds_at(wave < 4 ? l0 : l1) + (wave & 3) * kThinRing, lds_at(l0) + 4 * kThinRing,
+                      lds_at(l1) + 4 * kThinRing};
+    static_assert(4 * kThinRing + kGmmWaves * 2 * 1024 <= kWideStage, "rings and sums fit in a stage array");
+    static_assert(4 * kThinRing + kThinRows * kLineG * 4 <= kWideStage, "rings and outputs fit in a stage array");
+    thin_walk<GLU>(g, tab, thin_split(g, tab.n_thin, GLU ? g.Nw / 2 : g.Nw, GLU && !g.split), sm);
   }
 }
 
@@ -613,12 +734,11 @@ __device__ __forceinline__ int64_t rows_in_use(const int64_t* nums, int L, int64
   return min(total, A);
 }
 
-// x [rows][128 nb] bf16 -> q, s.  Clears the workspace's status block.
+// x [rows][128 nb] bf16 -> q, s.
 __global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_rows(const v4u* __restrict__ x, uint2* __restrict__ q,
                                                                   float* __restrict__ s,
                                                                   const int64_t* __restrict__ nums, int L, int64_t A,
-                                                                  int nb, mdc_device_status* status) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = mdc_device_status{0, 0, 0, 0};
+                                                                  int nb) {
   const int64_t n = rows_in_use(nums, L, A) * nb * 16;   // vectors of 8
   for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < (n + 63) / 64 * 64;
        i += (int64_t)gridDim.x * kQuantThreads) {
@@ -635,19 +755,19 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_rows(const v4u* __r
   }
 }
 
-// g (fp32) -> q, s.  One workgroup per (expert, row), rows strided.
-__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g, mdc_device_status* status) {
+// g (fp32) -> q, s of the thin experts' rows.  One workgroup per (expert, row),
+// strided.
+__global__ __launch_bounds__(kQuantThreads) void k_quant_fp8_thin(Gmm g) {
   extern __shared__ int gmm_table[];
   __shared__ int64_t wave_total[kQuantThreads / 64];
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = mdc_device_status{0, 0, 0, 0};
-  const GmmTable tab{gmm_table, gmm_table + g.L + 1};
-  // here a tile is a row
-  gmm_plan<kQuantThreads>(g, tab, wave_total, [](int n) { return n <= kThinRows ? n : 0; });
+  int* rows = gmm_table;
+  gmm_rows<kQuantThreads>(g, rows, wave_total);
   const int nvec = g.Nw / 2 / 8;   // a multiple of 16
-  for (int m = blockIdx.x; m < tab.tiles[g.L]; m += gridDim.x) {
-    const int e = gmm_expert(tab, g.L, m);
-    const int in = m - tab.tiles[e], row = tab.rows[e] + in;
-    const v4f* src = reinterpret_cast<const v4f*>(g.g + thin_row(g, e, tab.rows[e], in) * (g.Nw / 2));
+  for (int m = blockIdx.x; m < g.L * kThinRows; m += gridDim.x) {
+    const int e = m / kThinRows, in = m - e * kThinRows;
+    const int count = rows[e + 1] - rows[e], row = rows[e] + in;
+    if (count > kThinRows || in >= count) continue;
+    const v4f* src = reinterpret_cast<const v4f*>(g.g + (int64_t)row * (g.Nw / 2));
     for (int i = threadIdx.x; i < (nvec + 63) / 64 * 64; i += kQuantThreads) {
       const v4f z = {0.f, 0.f, 0.f, 0.f};
       const v4f a = i < nvec ? src[2 * i] : z, b = i < nvec ? src[2 * i + 1] : z;
@@ -673,16 +793,18 @@ unsigned device_cus() {
   return (unsigned)cus;
 }
 
+// Whether thin experts' SwiGLU outputs go through memory in fp32 and a launch
+// that quantises them: where the 128-column blocks are too few for the CUs, and
+// the capacity says that thin experts are what there is (which experts are thin
+// is known on the device only).
+constexpr int kSplitBlocks = 192;
+bool gmm_split(int64_t A, int64_t L, int64_t cols) {
+  return L * (cols / kFp8Block) < kSplitBlocks && A <= L * kThinRows;
+}
+
 template <bool GLU>
 void launch_gmm(const Gmm& g, hipStream_t s) {
-  const int64_t nn = GLU ? g.Nw / kThinW : (g.Nw + kThinW - 1) / kThinW;
-  const unsigned cus = device_cus();
-  // which experts have few rows is known on the device only
-  if (g.A > kThinRows)
-    hipLaunchKernelGGL((k_gmm_wide<GLU>), dim3((cus + 7) / 8 * 8), dim3(kWideThreads), gmm_table_bytes(g.L), s, g);
-  if (g.A <= kThinRows || g.nums != nullptr)
-    hipLaunchKernelGGL((k_gmm_thin<GLU>), dim3((unsigned)min(g.L * nn, (int64_t)cus * 8)), dim3(kThinThreads),
-                       gmm_table_bytes(g.L), s, g);
+  hipLaunchKernelGGL((k_gmm<GLU>), dim3((device_cus() + 7) / 8 * 8), dim3(kGmmThreads), gmm_table_bytes(g.L), s, g);
 }
 
 constexpr int kMaxK = 1 << 22;   // the rows of a tile are addressed with 32-bit offsets
@@ -690,11 +812,11 @@ constexpr int kMaxK = 1 << 22;   // the rows of a tile are addressed with 32-bit
 mdc_status check_gmm(int64_t A, int32_t L, int32_t n, int32_t k) {
   if (A < 0 || L < 1 || n < 1 || k < 1 || n % 8 != 0 || k % 16 != 0) return MDC_ERR_INVALID;
   if (L > MDC_MAX_LOCAL_EXPERTS || A > INT32_MAX || (int64_t)n * k > INT32_MAX || k > kMaxK) return MDC_ERR_UNSUPPORTED;
-  if ((A / kThinRows + L + 1) * ((n + kThinW - 1) / kThinW) > INT32_MAX - 65536) return MDC_ERR_UNSUPPORTED;
+  if ((A / kThinRows + L + 1) * ((n + 15) / 16) > INT32_MAX - 65536) return MDC_ERR_UNSUPPORTED;
   return MDC_OK;
 }
 
-// Workspace: [status block][q1][s1][q2][s2][g of experts with few rows].
+// Workspace: [status block][q1][s1][q2][s2][g, where thin experts split k].
 struct Ffn8Plan {
   int64_t A;
   int H, N, L;
@@ -713,7 +835,7 @@ Ffn8Plan make_ffn8_plan(const mdc_shape* sh, int inter_n) {
   f.off_q2 = f.off_s1 + round_up(A * (H / kFp8Block) * 4, 256);
   f.off_s2 = f.off_q2 + round_up(A * I, 256);
   f.off_g = f.off_s2 + round_up(A * (I / kFp8Block) * 4, 256);
-  f.bytes = f.off_g + round_up((size_t)thin_rows(f.A, f.L) * I * 4, 256);
+  f.bytes = f.off_g + (gmm_split(f.A, f.L, I) ? round_up(A * I * 4, 256) : 0);
   return f;
 }
 
@@ -751,19 +873,21 @@ mdc_status ffn8_impl(const mdc_shape* shape, int32_t inter_n, const void* expand
     uint2* q = reinterpret_cast<uint2*>(ws + f.off_q1);
     float* s1 = reinterpret_cast<float*>(ws + f.off_s1);
     hipLaunchKernelGGL(k_quant_fp8_rows, dim3(cus * 8), dim3(kQuantThreads), 0, s, static_cast<const v4u*>(expand_x),
-                       q, s1, nums, f.L, f.A, f.H / kFp8Block, status);
+                       q, s1, nums, f.L, f.A, f.H / kFp8Block);
     q1 = reinterpret_cast<const uint8_t*>(q);
     scales = s1;
   }
   uint8_t* q2 = reinterpret_cast<uint8_t*>(ws + f.off_q2);
   float* s2 = reinterpret_cast<float*>(ws + f.off_s2);
   const Gmm g1{q1, scales, nums, static_cast<const uint8_t*>(w1), w1_scale, nullptr,
-               reinterpret_cast<float*>(ws + f.off_g), q2, s2, (int)f.A, f.L, f.N, f.H, f.H / kFp8Block};
+               reinterpret_cast<float*>(ws + f.off_g), q2, s2, status, (int)f.A, f.L, f.N, f.H, f.H / kFp8Block,
+               gmm_split(f.A, f.L, f.N / 2)};
   launch_gmm<true>(g1, s);
-  hipLaunchKernelGGL(k_quant_fp8_thin, dim3((unsigned)min(f.A, (int64_t)cus * 8)), dim3(kQuantThreads),
-                     gmm_table_bytes(f.L), s, g1, status);
+  if (g1.split)
+    hipLaunchKernelGGL(k_quant_fp8_thin, dim3((unsigned)min((int64_t)f.L * kThinRows, (int64_t)cus * 8)),
+                       dim3(kQuantThreads), ((size_t)f.L + 1) * sizeof(int), s, g1);
   const Gmm g2{q2, s2, nums, static_cast<const uint8_t*>(w2), w2_scale, static_cast<uint16_t*>(y), nullptr, nullptr, nullptr,
-               (int)f.A, f.L, f.H, f.N / 2, f.N / 2 / kFp8Block};
+               nullptr, (int)f.A, f.L, f.H, f.N / 2, f.N / 2 / kFp8Block, 0};
   launch_gmm<false>(g2, s);
   return launched();
 }
@@ -785,7 +909,8 @@ mdc_status mdc_gmm_fp8(int64_t capacity, int32_t experts, int32_t n, int32_t k, 
     return MDC_ERR_INVALID;
   (void)hipGetLastError();
   const Gmm g{static_cast<const uint8_t*>(a), a_scale, expert_token_nums, static_cast<const uint8_t*>(w), w_scale,
-              static_cast<uint16_t*>(y), nullptr, nullptr, nullptr, (int)capacity, experts, n, k, (k + kFp8Block - 1) / kFp8Block};
+              static_cast<uint16_t*>(y), nullptr, nullptr, nullptr, nullptr, (int)capacity, experts, n, k,
+              (k + kFp8Block - 1) / kFp8Block, 0};
   launch_gmm<false>(g, static_cast<hipStream_t>(stream));
   return launched();
 }

@@ -646,7 +646,7 @@ mdc_status mdc_add_rms_norm(const mdc_norm_params* params,
  *   all A rows.  Negative counts are read as zero.
  * a, w and y are 16-byte aligned.  K must be a multiple of 16 and n of 8, both
  * positive (else MDC_ERR_INVALID); n * K < 2^31, K <= 2^22, L <=
- * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and the tile count (A / 64 + L + 1) * ceil(n / 32) below 2^31 (else
+ * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and the tile count (A / 64 + L + 1) * ceil(n / 16) below 2^31 (else
  * MDC_ERR_UNSUPPORTED).  No workspace.
  * ------------------------------------------------------------------------ */
 mdc_status mdc_gmm_fp8(int64_t capacity,
