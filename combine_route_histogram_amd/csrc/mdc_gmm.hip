@@ -54,13 +54,14 @@ struct Gmm {
 
 // ---------------------------------------------------------------------------
 // Rows and tiles of the experts.  Every workgroup works out the plan from the
-// counts by itself, in LDS.  Experts with at most kThinRows rows, one block of
+// counts by itself, in LDS.  Experts with at most kThinRows rows, two blocks of
 // the matrix instruction, are "thin": what counts there is to stream the
 // weights.  The others are "wide".
 // ---------------------------------------------------------------------------
 constexpr int kGmmThreads = 512;
 constexpr int kGmmWaves = kGmmThreads / 64;
-constexpr int kThinRows = 16;
+constexpr int kThinBlocks = 2;
+constexpr int kThinRows = 16 * kThinBlocks;
 
 struct GmmTable {
   int* rows;        // [L + 1] first row of expert e
@@ -169,6 +170,7 @@ __device__ __forceinline__ int gmm_expert(const GmmTable& t, int L, int m) {
 constexpr unsigned kPastEnd = 0x80000000u;   // an offset past every buffer: loads there read zero
 constexpr int kThinRing = 12288;             // bytes of a wavefront's ring
 constexpr int kThinRun = 8;                  // k-blocks of rows in registers
+constexpr int kWideCost = 2;                 // a wide tile's time in those of 128 columns of thin work
 constexpr int kLineG = kFp8Block + 4;        // floats of a row of SwiGLU outputs in LDS
 
 __device__ __forceinline__ unsigned lds_at(const void* p) { return (unsigned)(size_t)(lds_void*)p; }
@@ -192,9 +194,24 @@ struct ThinSmem {
   unsigned g;      // [kThinRows][kLineG] fp32
 };
 
+// This workgroup's place in the walks: workgroup b runs on XCD b % 8, and each
+// XCD takes a run of places.
+__device__ __forceinline__ int wide_line() { return (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8; }
+
+// First of T equal pieces of thin work for the workgroup at place `line`, after
+// `wide` wide tiles were dealt to places 0, 1, ... in turn: a place with a wide
+// tile more gets less, a wide tile counted as `cost` pieces.
+__device__ __forceinline__ int64_t thin_share(int64_t T, int wide, int cost, int line) {
+  const int G = gridDim.x, more = wide % G;   // places [0, more) have a tile more
+  // x pieces for those, x + cost for the others: more x + (G - more) (x + cost) = T, x >= 0
+  const int64_t rest = T - (int64_t)(G - more) * cost;
+  if (rest <= 0) return line <= more ? 0 : T * (line - more) / (G - more);   // (more < G)
+  return line <= more ? rest * line / G : rest * line / G + (int64_t)(line - more) * cost;
+}
+
 template <bool GLU>
-__device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int ks, const ThinSmem& sm) {
-  constexpr int WB = GLU ? 2 : 1;
+__device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int wide, int ks, const ThinSmem& sm) {
+  constexpr int WB = GLU ? 2 : 1, MB = kThinBlocks;
   constexpr int kSlot = WB * 2048, kSlots = kThinRing / kSlot;
   constexpr int kLoads = 2 * WB;   // direct loads of a slot
   const int lane = threadIdx.x & 63;
@@ -209,7 +226,9 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
   // this workgroup's tiles: [t0, t1) of n_thin * tiles_per, whole blocks of ks tiles if they are wanted
   const int grain = blocks ? ks : 1;
   const int64_t T = (int64_t)tab.n_thin * tiles_per / grain;
-  const int t0 = (int)(T * blockIdx.x / gridDim.x) * grain, t1 = (int)(T * (blockIdx.x + 1) / gridDim.x) * grain;
+  const int cost = max(1, kWideCost * 8 / (rs * grain));
+  const int t0 = (int)thin_share(T, wide, cost, wide_line()) * grain;
+  const int t1 = (int)thin_share(T, wide, cost, wide_line() + 1) * grain;
   if (t0 == t1) return;
 
   // ---- weights: tile by tile, step by step ----
@@ -257,8 +276,8 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
   const unsigned f0 = sm.ring + r16 * kFp8Block + ((quad ^ key) << 4);
   const unsigned f1 = sm.ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
   unsigned read = 0;
-  v8i tok[kThinRun];
-  float sa[kThinRun], sw[WB][kThinRun], sw_next[WB][kThinRun];
+  v8i tok[kThinRun][MB];
+  float sa[kThinRun][MB], sw[WB][kThinRun], sw_next[WB][kThinRun];
   // weight scales of a tile's run, by scalar loads: they pass by the direct loads' count
   auto scales = [&](float (&s)[WB][kThinRun], int e, int n, int s0) {
     const scalar_f* p = (const scalar_f*)(g.w_scale + ((int64_t)e * wb + min((n + 16 * rb) / kFp8Block, wb - 1)) * nk);
@@ -285,9 +304,11 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
       if (!on) e_next = __builtin_amdgcn_readfirstlane((int)tab.thin[i + 1]);
       scales(sw_next, e_next, on ? n0 + width : 0, 0);
     }
-    v4f acc[WB];
+    v4f acc[MB][WB];
 #pragma unroll
-    for (int j = 0; j < WB; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int j = 0; j < WB; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
     for (int s0 = 0; s0 < per; s0 += kThinRun) {
       if (s0 != 0) scales(sw, e, n0, s0);
       if (i != have || per > kThinRun) {
@@ -299,11 +320,16 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
 #pragma unroll
         for (int d = 0; d < kThinRun; ++d) {
           const int b = s0 + d < per ? kb0 + s0 + d : nk;
-          const unsigned k0 = (unsigned)b * kFp8Block + 16u * quad, k1 = k0 + 64u, at = (unsigned)(r16 * K);
-          tok[d] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
-                        __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
-          sa[d] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                rq, b < nk ? (unsigned)(r16 * nk + b) * 4u : kPastEnd, 0, 0));
+          const unsigned k0 = (unsigned)b * kFp8Block + 16u * quad, k1 = k0 + 64u;
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            const int row = 16 * m + r16;
+            const unsigned at = (unsigned)(row * K);
+            tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
+                             __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
+            sa[d][m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                     rq, b < nk ? (unsigned)(row * nk + b) * 4u : kPastEnd, 0, 0));
+          }
         }
       }
 #pragma unroll
@@ -318,10 +344,13 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
           fetch();
 #pragma unroll
           for (int j = 0; j < WB; ++j) {
-            const v4f p = mfma_block(w[j], tok[d]);
-            const float f = sa[d] * (kb0 + s0 + d < nk ? sw[j][d] : 0.f);
+            const float f = kb0 + s0 + d < nk ? sw[j][d] : 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(p[r], f, acc[j][r]);
+            for (int m = 0; m < MB; ++m) {
+              const v4f p = mfma_block(w[j], tok[d][m]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[m][j][r] = __builtin_fmaf(p[r], sa[d][m] * f, acc[m][j][r]);
+            }
           }
         }
       }
@@ -329,33 +358,37 @@ __device__ __forceinline__ void thin_walk(const Gmm& g, const GmmTable& tab, int
     }
     // join the runs of k-blocks: wavefront ob < rs sums those of block ob
 #pragma unroll
-    for (int j = 0; j < WB; ++j) lds_put(sm.red + ((wave * WB + j) * 64 + lane) * 16, acc[j]);
-    lds_barrier();
-    if (wave < rs) {
-      v4f sum[WB];
+    for (int m = 0; m < MB; ++m) {
 #pragma unroll
-      for (int j = 0; j < WB; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < ks; ++k) {
-        const unsigned at = sm.red + ((wave * ks + k) * WB * 64 + lane) * 16;
-        const v8i p = lds_get2(at, at + (WB - 1) * 1024);
+      for (int j = 0; j < WB; ++j) lds_put(sm.red + ((wave * WB + j) * 64 + lane) * 16, acc[m][j]);
+      lds_barrier();
+      if (wave < rs) {
+        v4f sum[WB];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sum[0][r] += __int_as_float(p[r]);
-          if (GLU) sum[WB - 1][r] += __int_as_float(p[4 + r]);
+        for (int j = 0; j < WB; ++j) sum[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < ks; ++k) {
+          const unsigned at = sm.red + ((wave * ks + k) * WB * 64 + lane) * 16;
+          const v8i p = lds_get2(at, at + (WB - 1) * 1024);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sum[0][r] += __int_as_float(p[r]);
+            if (GLU) sum[WB - 1][r] += __int_as_float(p[4 + r]);
+          }
+        }
+        const int row = 16 * m + r16, col = n0 + 16 * wave + 4 * quad;
+        if (GLU) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[0][r] = gmm_silu(sum[0][r]) * sum[WB - 1][r];
+          if (blocks) lds_put(sm.g + (row * kLineG + col % kFp8Block) * 4, sum[0]);
+          else if (row < rows) *reinterpret_cast<v4f*>(g.g + (int64_t)(row0 + row) * cols + col) = sum[0];
+        } else if (row < rows && col < Nw) {
+          *reinterpret_cast<v4b*>(g.y + (int64_t)(row0 + row) * Nw + col) = __builtin_convertvector(sum[0], v4b);
         }
       }
-      const int col = n0 + 16 * wave + 4 * quad;
-      if (GLU) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[0][r] = gmm_silu(sum[0][r]) * sum[WB - 1][r];
-        if (blocks) lds_put(sm.g + (r16 * kLineG + col % kFp8Block) * 4, sum[0]);
-        else if (r16 < rows) *reinterpret_cast<v4f*>(g.g + (int64_t)(row0 + r16) * cols + col) = sum[0];
-      } else if (r16 < rows && col < Nw) {
-        *reinterpret_cast<v4b*>(g.y + (int64_t)(row0 + r16) * Nw + col) = __builtin_convertvector(sum[0], v4b);
-      }
+      lds_barrier();   // the sums have been read, SwiGLU's outputs are there
     }
-    lds_barrier();   // the sums have been read, SwiGLU's outputs are there
-    if (blocks && (n0 + width) % kFp8Block == 0 && wave < kThinRows / 4) {
+    if (blocks && (n0 + width) % kFp8Block == 0) {
+      static_assert(kThinRows * 16 == kGmmThreads, "a thread for 8 of the outputs");
       // row r = thread / 16, 8 columns per thread (overwritten only behind the next tile's first barrier)
       const int r = threadIdx.x >> 4, u = threadIdx.x & 15;
       const unsigned at = sm.g + (r * kLineG + 8 * u) * 4;
@@ -677,9 +710,7 @@ __device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, con
   constexpr int kCols = GLU ? kWideW / 2 : kWideW;
   const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
   const int T = tab.tiles[g.L] * nn;
-  const int G = gridDim.x, b = blockIdx.x;
-  // workgroup b runs on XCD b % 8: each XCD walks a run of consecutive tiles
-  for (int t = (b % 8) * (G / 8) + b / 8; t < T; t += G) wide_tile<GLU, BM>(g, wide_place(g, tab, t, nn, BM, kCols), sm);
+  for (int t = wide_line(); t < T; t += gridDim.x) wide_tile<GLU, BM>(g, wide_place(g, tab, t, nn, BM, kCols), sm);
 }
 
 // One workgroup per CU: the wide experts' tiles, then the thin experts' groups.
@@ -696,12 +727,13 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
   const int G = gridDim.x;
   const int T = gmm_tiles(g, tab, 256, wave_total) * nn;
+  int wide = T;
   if (T != 0) {
     const WideSmem sm{l0, l1};
     // 128-row tiles where 256-row ones leave CUs idle: a 128-row tile takes
     // about 0.6 of a 256-row one's time and there are at most twice as many
     if (5 * ((T + G - 1) / G) > 3 * ((2 * T + G - 1) / G)) {
-      gmm_tiles(g, tab, 128, wave_total);
+      wide = gmm_tiles(g, tab, 128, wave_total) * nn;
       wide_walk<GLU, 128>(g, tab, sm);
     } else {
       wide_walk<GLU, 256>(g, tab, sm);
@@ -710,12 +742,12 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   if (tab.n_thin != 0) {
     __syncthreads();   // l0 and l1 are free
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // four wavefronts' rings in each array, then the sums in one and SwiGLU's outputs in the other
-    const ThinSmem sm{lds_at(wave < 4 ? l0 : l1) + (wave & 3) * kThinRing, lds_at(l0) + 4 * kThinRing,
-                      lds_at(l1) + 4 * kThinRing};
-    static_assert(4 * kThinRing + kGmmWaves * 2 * 1024 <= kWideStage, "rings and sums fit in a stage array");
+    // four wavefronts' rings in each array, then SwiGLU's outputs in one and the sums in the other
     static_assert(4 * kThinRing + kThinRows * kLineG * 4 <= kWideStage, "rings and outputs fit in a stage array");
-    thin_walk<GLU>(g, tab, thin_split(g, tab.n_thin, GLU ? g.Nw / 2 : g.Nw, GLU && !g.split), sm);
+    static_assert(4 * kThinRing + kGmmWaves * 2 * 1024 <= kWideStage, "rings and sums fit in a stage array");
+    const ThinSmem sm{lds_at(wave < 4 ? l0 : l1) + (wave & 3) * kThinRing, lds_at(l1) + 4 * kThinRing,
+                      lds_at(l0) + 4 * kThinRing};
+    thin_walk<GLU>(g, tab, wide, thin_split(g, tab.n_thin, GLU ? g.Nw / 2 : g.Nw, GLU && !g.split), sm);
   }
 }
 
@@ -797,9 +829,9 @@ unsigned device_cus() {
 // that quantises them: where the 128-column blocks are too few for the CUs, and
 // the capacity says that thin experts are what there is (which experts are thin
 // is known on the device only).
-constexpr int kSplitBlocks = 192;
+constexpr int kSplitBlocks = 192, kSplitRows = 128;
 bool gmm_split(int64_t A, int64_t L, int64_t cols) {
-  return L * (cols / kFp8Block) < kSplitBlocks && A <= L * kThinRows;
+  return L * (cols / kFp8Block) < kSplitBlocks && A <= L * kSplitRows;
 }
 
 template <bool GLU>
