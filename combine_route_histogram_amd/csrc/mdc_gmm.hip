@@ -482,35 +482,45 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     vo[par] = (unsigned)((lane >> 3) * K) + chunk[par];
   }
   const unsigned up = GLU && wave >= 4 ? (unsigned)((Nw / 2 - kWideW / 2) * K) : 0u;   // weight rows 128 .. 255
-  auto dma = [&](uint8_t* buf, int b) {   // (no branches here and below: they would split the schedule)
+  // Direct loads of k-block b, of kLoads in kParts parts.  (No branches here
+  // and below: they would split the schedule.)
+  constexpr int kLoads = kTokenLoads + 4;
+  constexpr int kParts = NB / 2 + 1, kPart = (kLoads + kParts - 1) / kParts;
+  auto dma = [&](uint8_t* buf, int b, int part) {
     unsigned v[2];
     const unsigned k0 = (unsigned)b * kFp8Block;
 #pragma unroll
     for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kPastEnd;   // zeros past K
 #pragma unroll
-    for (int j = 0; j < kTokenLoads; ++j) {
-      const int blk = kTokenLoads * wave + j;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(buf + blk * 1024), 16, v[blk & 1],
-                                               k0 + (unsigned)(8 * blk * K), 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int blk = 4 * wave + j;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(buf + kTokenBytes + blk * 1024), 16, v[j & 1],
-                                               k0 + (unsigned)(8 * blk * K) + up, 0, 0);
+    for (int q = part * kPart; q < min(kLoads, (part + 1) * kPart); ++q) {
+      if (q < 4) {
+        const int blk = 4 * wave + q;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(buf + kTokenBytes + blk * 1024), 16, v[q & 1],
+                                                 k0 + (unsigned)(8 * blk * K) + up, 0, 0);
+      } else {
+        const int blk = kTokenLoads * wave + q - 4;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(buf + blk * 1024), 16, v[blk & 1],
+                                                 k0 + (unsigned)(8 * blk * K), 0, 0);
+      }
     }
   };
+  auto dma_all = [&](uint8_t* buf, int b) {
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) dma(buf, b, part);
+  };
 
-  // ---- scales of k-blocks b, b + 1 (b even): thread (half, row) ----
+  // ---- scales of k-blocks b, b + 1 (b even): thread (row, half), so that a
+  // wavefront's loads touch 32 rows (64 would take the address unit twice as long) ----
   const int wb = (Nw + kFp8Block - 1) / kFp8Block;
-  const int srow = tid & (BM - 1), half = __builtin_amdgcn_readfirstlane(tid / BM) & 1;   // (BM = 128: in pairs)
-  const int wblock = GLU ? (t.n0 + (half ? Nw / 2 : 0)) / kFp8Block : min(t.n0 / kFp8Block + half, wb - 1);
+  const int srow = (tid >> 1) & (BM - 1), half = tid & 1;   // (BM = 128: two threads each)
+  const int wblock = t.n0 / kFp8Block;
+  const unsigned wnext = (unsigned)((GLU ? wb / 2 : min(1, wb - 1 - wblock)) * nk) * 4u;   // from the first half's scales
   const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<float*>(g.w_scale + ((int64_t)t.e * wb + wblock) * nk), (short)0, nk * 4, 0x00020000);
+      const_cast<float*>(g.w_scale + ((int64_t)t.e * wb + wblock) * nk), (short)0, (int)wnext + nk * 4, 0x00020000);
   v2f sa, sw;
   auto scale_load = [&](int b) {
     sa = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rs, (unsigned)(srow * nk) * 4u, (unsigned)b * 4u, 0));
-    sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, 0, (unsigned)b * 4u, 0));
+    sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, half ? wnext : 0u, (unsigned)b * 4u, 0));
   };
   auto scale_store = [&](int b) {
     const int at = kWideData + (((b >> 1) & 1) * kWideScales + half * kWideRows + srow) * 4;
@@ -550,12 +560,12 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(p[r], f, c[r]);
   };
 
-  dma(sm.l0, 0);
+  dma_all(sm.l0, 0);
   scale_load(0);
   scale_store(0);
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the loads into l0 have landed
   __syncthreads();
-  dma(sm.l1, 1);
+  dma(sm.l1, 1, 0);
   scale_load(2);
   v8i w[4], tok = tfrag(sm.l0, 0), tok_next;
 #pragma unroll
@@ -569,6 +579,7 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
   auto stage = [&](uint8_t* cur, uint8_t* nxt, int b, bool odd) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
+      if (i + 1 < kParts) dma(nxt, b + 1, i + 1);   // (all at once they would hold up the products)
       if (i + 1 < NB) {
         tok_next = tfrag(cur, i + 1);
         s_next = scale(cur, b, i + 1);
@@ -576,7 +587,7 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
         __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wavefront's loads into nxt have landed
         if (odd) scale_store(b + 1);          // (loaded two stages before)
         __syncthreads();
-        dma(cur, b + 2);
+        dma(cur, b + 2, 0);
         if (odd) scale_load(b + 3);
         tok_next = tfrag(nxt, 0);   // (after the last stage: read, never used)
         s_next = scale(nxt, b + 1, 0);
@@ -600,6 +611,7 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
   }
 #pragma unroll
   for (int j = 1; j < 4; ++j) add(acc[NB - 1][j], p[j], s_prev.s[GLU ? j >> 1 : 0]);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the last stage's loads (of zeros) have landed too
 }
 
 // One tile: the k loop, then the outputs through LDS as whole rows.
