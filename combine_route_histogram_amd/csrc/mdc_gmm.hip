@@ -426,7 +426,7 @@ __device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, b
 // Experts with more rows: tiles of BM rows x 256 weight rows (SwiGLU: 128 gate
 // rows and the 128 up rows that go with them), one workgroup of eight
 // wavefronts per CU walking tiles.  Each k-block of 128 is one stage, loaded
-// global -> LDS directly into one of two stage arrays while the other is
+// global -> LDS directly into a ring of S stages while earlier ones are
 // multiplied.  Wavefront (wt, wn) holds token blocks 2 i + wt (16 rows each, so
 // that a short tile's blocks are shared) x 64 weight rows.
 //
@@ -435,22 +435,20 @@ __device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, b
 // writes lane l's 16 bytes at base + 16 l: eight rows per wavefront load, lane
 // l taking row l / 8 and the chunk that belongs in slot l % 8.
 //
-// The scales sa[row][b] sw[.][b] lie behind the rows of the stage array that
-// k-block b uses (two deep): thread (weight half, row) loads, multiplies and
-// stores those of two k-blocks every second stage.  They are not an array of
-// their own because the compiler makes reads of LDS that no direct load writes
-// wait for every direct load in flight.
+// The scales sa[row][b] sw[.][b] of four k-blocks lie behind the ring: thread
+// (row, weight half) loads, multiplies and stores those of two k-blocks every
+// second stage.
+//
+// The direct loads take their LDS addresses as numbers, and the waits for them
+// are written out (a stage's before the barrier that opens it): told the array,
+// the compiler would make every LDS read wait for every direct load.
 // ---------------------------------------------------------------------------
-constexpr int kWideW = 256;                      // weight rows of a tile
-constexpr int kWideRows = 256;                   // token rows of a tile, at most
-constexpr int kWideScales = 2 * kWideRows;       // floats: one k-block's scales, [weight half][row]
-constexpr int kWideData = (kWideRows + kWideW) * kFp8Block;
-constexpr int kWideStage = kWideData + 2 * kWideScales * 4;
-
-struct WideSmem {
-  uint8_t* l0;    // kWideStage bytes: even k-blocks (rows, then scales of k-block b at slot b / 2 % 2)
-  uint8_t* l1;    // odd k-blocks
-};
+constexpr int kWideW = 256;   // weight rows of a tile
+constexpr int wide_stage(int BM) { return (BM + kWideW) * kFp8Block; }
+constexpr int wide_bytes(int BM, int S) { return S * wide_stage(BM) + 4 * 2 * BM * 4; }
+// 128-row tiles take three stages where the experts' table leaves that much LDS.
+constexpr int kLdsDeep = wide_bytes(128, 3), kLdsFlat = wide_bytes(256, 2);
+static_assert(kLdsFlat >= wide_bytes(64, 3) && kLdsFlat >= wide_bytes(128, 2) && kLdsDeep >= kLdsFlat, "LDS of the tiles");
 
 struct WideTile {
   int e, row0, rows, n0;   // n0: first weight row (SwiGLU: first output column)
@@ -458,9 +456,9 @@ struct WideTile {
 
 // The k loop: acc[i][j] = token block 2 i + wt times weight block j of the
 // wavefront.  NB: token blocks computed (the others hold no rows).
-template <bool GLU, int BM, int NB>
-__device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, const WideSmem& sm,
-                                           v4f (&acc)[BM / 32][4]) {
+template <bool GLU, int BM, int S, int NB>
+__device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint8_t* smem, v4f (&acc)[BM / 32][4]) {
+  constexpr int kStage = wide_stage(BM), kRing = S * kStage;
   constexpr int kTokenBytes = BM * kFp8Block;
   constexpr int kTokenLoads = BM / 64;   // direct loads of token rows per wavefront and stage (8 rows each)
   const int tid = threadIdx.x, lane = tid & 63;
@@ -486,7 +484,8 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
   // and below: they would split the schedule.)
   constexpr int kLoads = kTokenLoads + 4;
   constexpr int kParts = NB / 2 + 1, kPart = (kLoads + kParts - 1) / kParts;
-  auto dma = [&](uint8_t* buf, int b, int part) {
+  const unsigned lds = lds_at(smem);
+  auto dma = [&](int at, int b, int part) {   // at: the stage's place in the ring
     unsigned v[2];
     const unsigned k0 = (unsigned)b * kFp8Block;
 #pragma unroll
@@ -495,20 +494,15 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     for (int q = part * kPart; q < min(kLoads, (part + 1) * kPart); ++q) {
       if (q < 4) {
         const int blk = 4 * wave + q;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(buf + kTokenBytes + blk * 1024), 16, v[q & 1],
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(lds + at + kTokenBytes + blk * 1024), 16, v[q & 1],
                                                  k0 + (unsigned)(8 * blk * K) + up, 0, 0);
       } else {
         const int blk = kTokenLoads * wave + q - 4;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(buf + blk * 1024), 16, v[blk & 1],
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(lds + at + blk * 1024), 16, v[blk & 1],
                                                  k0 + (unsigned)(8 * blk * K), 0, 0);
       }
     }
   };
-  auto dma_all = [&](uint8_t* buf, int b) {
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) dma(buf, b, part);
-  };
-
   // ---- scales of k-blocks b, b + 1 (b even): thread (row, half), so that a
   // wavefront's loads touch 32 rows (64 would take the address unit twice as long) ----
   const int wb = (Nw + kFp8Block - 1) / kFp8Block;
@@ -522,10 +516,11 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     sa = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rs, (unsigned)(srow * nk) * 4u, (unsigned)b * 4u, 0));
     sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, half ? wnext : 0u, (unsigned)b * 4u, 0));
   };
+  float* const sc = reinterpret_cast<float*>(smem + kRing);   // [4][2 weight halves][BM], k-block b at b % 4
   auto scale_store = [&](int b) {
-    const int at = kWideData + (((b >> 1) & 1) * kWideScales + half * kWideRows + srow) * 4;
-    *reinterpret_cast<float*>(sm.l0 + at) = b < nk ? sa[0] * sw[0] : 0.f;
-    *reinterpret_cast<float*>(sm.l1 + at) = b + 1 < nk ? sa[1] * sw[1] : 0.f;
+    float* p = sc + (b & 3) * 2 * BM + half * BM + srow;
+    p[0] = b < nk ? sa[0] * sw[0] : 0.f;
+    p[2 * BM] = b + 1 < nk ? sa[1] * sw[1] : 0.f;
   };
 
   // ---- fragments ----
@@ -536,23 +531,23 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     if (GLU) return (j < 2 ? 0 : kWideW / 2 - 32) + 32 * wn + 16 * j;
     return 64 * wn + 16 * j;
   };
-  auto wfrag = [&](const uint8_t* buf, int j) {
-    const uint8_t* p = buf + kTokenBytes + wrow(j) * kFp8Block;
+  auto wfrag = [&](int at, int j) {
+    const uint8_t* p = smem + at + kTokenBytes + wrow(j) * kFp8Block;
     return join(*reinterpret_cast<const v4i*>(p + f0), *reinterpret_cast<const v4i*>(p + f1));
   };
-  auto tfrag = [&](const uint8_t* buf, int i) {
-    const uint8_t* p = buf + (32 * i + 16 * wt) * kFp8Block;
+  auto tfrag = [&](int at, int i) {
+    const uint8_t* p = smem + at + (32 * i + 16 * wt) * kFp8Block;
     return join(*reinterpret_cast<const v4i*>(p + f0), *reinterpret_cast<const v4i*>(p + f1));
   };
-  const int f_sc = kWideData + ((GLU ? 0 : (wn >> 1) * kWideRows) + 16 * wt + r16) * 4;
+  const float* const my_sc = sc + (GLU ? 0 : (wn >> 1) * BM) + 16 * wt + r16;
   struct Sc {
     float s[GLU ? 2 : 1];
   };
-  auto scale = [&](const uint8_t* buf, int b, int i) {
-    const float* p = reinterpret_cast<const float*>(buf + f_sc + ((b >> 1) & 1) * kWideScales * 4) + 32 * i;
+  auto scale = [&](int b, int i) {
+    const float* p = my_sc + (b & 3) * 2 * BM + 32 * i;
     Sc s;
 #pragma unroll
-    for (int h = 0; h < (GLU ? 2 : 1); ++h) s.s[h] = p[h * kWideRows];
+    for (int h = 0; h < (GLU ? 2 : 1); ++h) s.s[h] = p[h * BM];
     return s;
   };
   auto add = [&](v4f& c, const v4f& p, float f) {
@@ -560,37 +555,43 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
     for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(p[r], f, c[r]);
   };
 
-  dma_all(sm.l0, 0);
+  // Stages 0 .. S - 2 are loaded ahead, and the first part of stage S - 1.
+  constexpr int kAhead = 0x0F70 | (((S - 2) * kLoads) & 15) | ((((S - 2) * kLoads) >> 4) << 14);   // vmcnt of S - 2 stages
   scale_load(0);
-  scale_store(0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the loads into l0 have landed
-  __syncthreads();
-  dma(sm.l1, 1, 0);
-  scale_load(2);
-  v8i w[4], tok = tfrag(sm.l0, 0), tok_next;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = wfrag(sm.l0, j);
-  Sc s_prev{}, s_cur = scale(sm.l0, 0, 0), s_next;
+  for (int d = 0; d < S - 1; ++d)
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) dma(d * kStage, d, part);
+  scale_store(0);
+  __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of stage 0 have landed
+  lds_barrier();
+  dma((S - 1) * kStage, S - 1, 0);
+  scale_load(2);
+  v8i w[4], tok = tfrag(0, 0), tok_next;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = wfrag(0, j);
+  Sc s_prev{}, s_cur = scale(0, 0), s_next;
   v4f p[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) p[j] = v4f{0.f, 0.f, 0.f, 0.f};
   // Each step issues one matrix instruction and adds the result of the one
   // three steps before, across token blocks and stages.
-  auto stage = [&](uint8_t* cur, uint8_t* nxt, int b, bool odd) {
+  int cur = 0, nxt = kStage, last = (S - 1) * kStage;   // places of k-blocks b, b + 1, b + S - 1
+  auto stage = [&](int b, bool odd) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      if (i + 1 < kParts) dma(nxt, b + 1, i + 1);   // (all at once they would hold up the products)
+      if (i + 1 < kParts) dma(last, b + S - 1, i + 1);   // (all at once they would hold up the products)
       if (i + 1 < NB) {
         tok_next = tfrag(cur, i + 1);
-        s_next = scale(cur, b, i + 1);
+        s_next = scale(b, i + 1);
       } else {
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wavefront's loads into nxt have landed
+        __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of k-block b + 1 have landed
         if (odd) scale_store(b + 1);          // (loaded two stages before)
-        __syncthreads();
-        dma(cur, b + 2, 0);
+        lds_barrier();
+        dma(cur, b + S, 0);
         if (odd) scale_load(b + 3);
         tok_next = tfrag(nxt, 0);   // (after the last stage: read, never used)
-        s_next = scale(nxt, b + 1, 0);
+        s_next = scale(b + 1, 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -604,19 +605,22 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, cons
       s_prev = s_cur;
       s_cur = s_next;
     }
+    last = cur;
+    cur = nxt;
+    nxt = nxt + kStage == kRing ? 0 : nxt + kStage;
   };
   for (int b = 0; b < nk; b += 2) {   // (past an odd last k-block comes one of zeros)
-    stage(sm.l0, sm.l1, b, false);
-    stage(sm.l1, sm.l0, b + 1, true);
+    stage(b, false);
+    stage(b + 1, true);
   }
 #pragma unroll
   for (int j = 1; j < 4; ++j) add(acc[NB - 1][j], p[j], s_prev.s[GLU ? j >> 1 : 0]);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the last stage's loads (of zeros) have landed too
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the loads past the last stage (of zeros) have landed too
 }
 
 // One tile: the k loop, then the outputs through LDS as whole rows.
-template <bool GLU, int BM>
-__device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const WideSmem& sm) {
+template <bool GLU, int BM, int S>
+__device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, uint8_t* smem) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave >> 2, wn = wave & 3;
@@ -626,15 +630,15 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
   for (int i = 0; i < BM / 32; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (t.rows > BM * 3 / 4) wide_kloop<GLU, BM, BM / 32>(g, t, sm, acc);
-  else if (t.rows > BM / 2) wide_kloop<GLU, BM, BM * 3 / 128>(g, t, sm, acc);
-  else if (t.rows > BM / 4) wide_kloop<GLU, BM, BM / 64>(g, t, sm, acc);
-  else wide_kloop<GLU, BM, BM / 128>(g, t, sm, acc);
-  __syncthreads();   // every wavefront has left the stage arrays
+  if (t.rows > BM * 3 / 4 || BM <= 64) wide_kloop<GLU, BM, S, BM / 32>(g, t, smem, acc);
+  else if (t.rows > BM / 2) wide_kloop<GLU, BM, S, (BM * 3 / 4 + 31) / 32>(g, t, smem, acc);
+  else if (t.rows > BM / 4) wide_kloop<GLU, BM, S, BM / 64>(g, t, smem, acc);
+  else wide_kloop<GLU, BM, S, (BM + 127) / 128>(g, t, smem, acc);
+  __syncthreads();   // every wavefront has left the ring
   if (GLU) {
     // g = silu(gate) * up (columns 32 wn + 16 j + 4 quad + r), its row maxima
     // over the 128 columns, and the codes
-    uint32_t* top = reinterpret_cast<uint32_t*>(sm.l1);   // [4][kWideRows]
+    uint32_t* top = reinterpret_cast<uint32_t*>(smem + BM * kFp8Block);   // [4][BM]
 #pragma unroll
     for (int i = 0; i < BM / 32; ++i) {
       uint32_t m = 0;
@@ -647,7 +651,7 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
         }
       m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
       m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      if (quad == 0) top[wn * kWideRows + 32 * i + 16 * wt + r16] = m;
+      if (quad == 0) top[wn * BM + 32 * i + 16 * wt + r16] = m;
     }
     __syncthreads();
     const int nb2 = g.Nw / 2 / kFp8Block;
@@ -656,12 +660,12 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
       const int row = 32 * i + 16 * wt + r16;
       uint32_t m = top[row];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) m = max(m, top[w * kWideRows + row]);
+      for (int w = 1; w < 4; ++w) m = max(m, top[w * BM + row]);
       const Fp8Scaler f(m);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int unit = 2 * wn + j;   // 16 columns
-        *reinterpret_cast<uint32_t*>(sm.l0 + row * kFp8Block + ((unit ^ (row & 7)) << 4) + 4 * quad) =
+        *reinterpret_cast<uint32_t*>(smem + row * kFp8Block + ((unit ^ (row & 7)) << 4) + 4 * quad) =
             f.codes4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
       }
       if (wn == 0 && quad == 0 && row < t.rows) g.q_scale[(int64_t)(t.row0 + row) * nb2 + t.n0 / kFp8Block] = f.scale;
@@ -670,13 +674,13 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
     for (int r = tid >> 3; r < t.rows; r += kGmmThreads / 8) {
       const int unit = tid & 7;
       *reinterpret_cast<v4u*>(g.q + (int64_t)(t.row0 + r) * (g.Nw / 2) + t.n0 + 16 * unit) =
-          *reinterpret_cast<const v4u*>(sm.l0 + r * kFp8Block + ((unit ^ (r & 7)) << 4));
+          *reinterpret_cast<const v4u*>(smem + r * kFp8Block + ((unit ^ (r & 7)) << 4));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < BM / 32; ++i) {
       const int row = 32 * i + 16 * wt + r16;
-      uint8_t* line = (row < 128 ? sm.l0 : sm.l1) + (row & 127) * 512;
+      uint8_t* line = smem + row * 512;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int unit = 8 * wn + 2 * j + (quad >> 1);   // 8 columns
@@ -689,9 +693,9 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, const
     if (col < g.Nw)
       for (int r = tid >> 5; r < t.rows; r += kGmmThreads / 32)
         *reinterpret_cast<v4u*>(g.y + (int64_t)(t.row0 + r) * g.Nw + col) =
-            *reinterpret_cast<const v4u*>((r < 128 ? sm.l0 : sm.l1) + (r & 127) * 512 + ((unit ^ (r & 31)) << 4));
+            *reinterpret_cast<const v4u*>(smem + r * 512 + ((unit ^ (r & 31)) << 4));
   }
-  __syncthreads();   // the stage arrays are free
+  __syncthreads();   // the ring is free
 }
 
 // Tile number -> place.  The m-tiles of an expert run in chunks of up to 8,
@@ -717,20 +721,27 @@ __device__ __forceinline__ WideTile wide_place(const Gmm& g, const GmmTable& tab
   return w;
 }
 
-template <bool GLU, int BM>
-__device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, const WideSmem& sm) {
+template <bool GLU, int BM, int S>
+__device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, uint8_t* smem) {
   constexpr int kCols = GLU ? kWideW / 2 : kWideW;
   const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
   const int T = tab.tiles[g.L] * nn;
-  for (int t = wide_line(); t < T; t += gridDim.x) wide_tile<GLU, BM>(g, wide_place(g, tab, t, nn, BM, kCols), sm);
+  for (int t = wide_line(); t < T; t += gridDim.x)
+    wide_tile<GLU, BM, S>(g, wide_place(g, tab, t, nn, BM, kCols), smem);
 }
 
-// One workgroup per CU: the wide experts' tiles, then the thin experts' groups.
-template <bool GLU>
+#ifndef FORCE
+#define FORCE 0
+#endif
+constexpr int kForce = FORCE;
+constexpr int kCost256 = 20, kCost128 = 11, kCost64 = 6;   // time of a tile of that many rows
+
+// One workgroup per CU: the wide experts' tiles, then the thin experts'.
+// DEEP: the LDS holds three stages of 128-row tiles.
+template <bool GLU, bool DEEP>
 __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   extern __shared__ int gmm_table[];
-  __shared__ __attribute__((aligned(16))) uint8_t l0[kWideStage];
-  __shared__ __attribute__((aligned(16))) uint8_t l1[kWideStage];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[DEEP ? kLdsDeep : kLdsFlat];
   __shared__ int64_t wave_total[kGmmWaves];
   GmmTable tab{gmm_table, gmm_table + g.L + 1, reinterpret_cast<uint16_t*>(gmm_table + 2 * (g.L + 1)), 0};
   if (g.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *g.status = mdc_device_status{0, 0, 0, 0};
@@ -738,27 +749,34 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   constexpr int kCols = GLU ? kWideW / 2 : kWideW;
   const int nn = ((GLU ? g.Nw / 2 : g.Nw) + kCols - 1) / kCols;
   const int G = gridDim.x;
-  const int T = gmm_tiles(g, tab, 256, wave_total) * nn;
-  int wide = T;
-  if (T != 0) {
-    const WideSmem sm{l0, l1};
-    // 128-row tiles where 256-row ones leave CUs idle: a 128-row tile takes
-    // about 0.6 of a 256-row one's time and there are at most twice as many
-    if (5 * ((T + G - 1) / G) > 3 * ((2 * T + G - 1) / G)) {
-      wide = gmm_tiles(g, tab, 128, wave_total) * nn;
-      wide_walk<GLU, 128>(g, tab, sm);
-    } else {
-      wide_walk<GLU, 256>(g, tab, sm);
+  int wide = gmm_tiles(g, tab, 256, wave_total) * nn;
+  if (wide != 0) {
+    // Tiles of 256, 128 or 64 rows, by the rounds that each takes and what a
+    // round costs.
+    int best = kForce ? kForce : 256, cost = kCost256 * ((wide + G - 1) / G);
+    int tiles = wide;
+#pragma unroll
+    for (int rows = 128; rows >= 64; rows >>= 1) {
+      const int n = gmm_tiles(g, tab, rows, wave_total) * nn;
+      const int c = (rows == 128 ? kCost128 : kCost64) * ((n + G - 1) / G);
+      if (!kForce && c < cost) {
+        best = rows;
+        cost = c;
+      }
+      tiles = n;
     }
+    wide = best == 64 ? tiles : gmm_tiles(g, tab, best, wave_total) * nn;
+    if (best == 64) wide_walk<GLU, 64, 3>(g, tab, smem);
+    else if (best == 128) wide_walk<GLU, 128, DEEP ? 3 : 2>(g, tab, smem);
+    else wide_walk<GLU, 256, 2>(g, tab, smem);
   }
   if (tab.n_thin != 0) {
-    __syncthreads();   // l0 and l1 are free
+    __syncthreads();   // smem is free
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // four wavefronts' rings in each array, then SwiGLU's outputs in one and the sums in the other
-    static_assert(4 * kThinRing + kThinRows * kLineG * 4 <= kWideStage, "rings and outputs fit in a stage array");
-    static_assert(4 * kThinRing + kGmmWaves * 2 * 1024 <= kWideStage, "rings and sums fit in a stage array");
-    const ThinSmem sm{lds_at(wave < 4 ? l0 : l1) + (wave & 3) * kThinRing, lds_at(l1) + 4 * kThinRing,
-                      lds_at(l0) + 4 * kThinRing};
+    constexpr int kRings = kGmmWaves * kThinRing;
+    static_assert(kRings + kGmmWaves * 2 * 1024 + kThinRows * kLineG * 4 <= kLdsFlat, "LDS of the thin tiles");
+    const ThinSmem sm{lds_at(smem) + wave * kThinRing, lds_at(smem) + kRings,
+                      lds_at(smem) + kRings + kGmmWaves * 2 * 1024};
     thin_walk<GLU>(g, tab, wide, thin_split(g, tab.n_thin, GLU ? g.Nw / 2 : g.Nw, GLU && !g.split), sm);
   }
 }
@@ -846,9 +864,14 @@ bool gmm_split(int64_t A, int64_t L, int64_t cols) {
   return L * (cols / kFp8Block) < kSplitBlocks && A <= L * kSplitRows;
 }
 
+constexpr size_t kLdsSize = 160 << 10;   // of a CU
+
 template <bool GLU>
 void launch_gmm(const Gmm& g, hipStream_t s) {
-  hipLaunchKernelGGL((k_gmm<GLU>), dim3((device_cus() + 7) / 8 * 8), dim3(kGmmThreads), gmm_table_bytes(g.L), s, g);
+  const dim3 grid((device_cus() + 7) / 8 * 8), block(kGmmThreads);
+  const size_t table = gmm_table_bytes(g.L);
+  if (table + kLdsDeep + 128 <= kLdsSize) hipLaunchKernelGGL((k_gmm<GLU, true>), grid, block, table, s, g);
+  else hipLaunchKernelGGL((k_gmm<GLU, false>), grid, block, table, s, g);
 }
 
 constexpr int kMaxK = 1 << 22;   // the rows of a tile are addressed with 32-bit offsets
