@@ -730,11 +730,10 @@ __device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, uin
     wide_tile<GLU, BM, S>(g, wide_place(g, tab, t, nn, BM, kCols), smem);
 }
 
-#ifndef FORCE
-#define FORCE 0
-#endif
-constexpr int kForce = FORCE;
-constexpr int kCost256 = 20, kCost128 = 11, kCost64 = 6;   // time of a tile of that many rows
+// What a k-block of a tile of 256, 128 and 64 rows takes, in tenths of a
+// microsecond (4096 x 4096 x 7168, 2048 and 1024 rows of it: 256 workgroups with
+// one tile each, 105, 65 and 48 us).
+constexpr int kCost256 = 19, kCost128 = 12, kCost64 = 8;
 
 // One workgroup per CU: the wide experts' tiles, then the thin experts'.
 // DEEP: the LDS holds three stages of 128-row tiles.
@@ -751,21 +750,20 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   const int G = gridDim.x;
   int wide = gmm_tiles(g, tab, 256, wave_total) * nn;
   if (wide != 0) {
-    // Tiles of 256, 128 or 64 rows, by the rounds that each takes and what a
-    // round costs.
-    int best = kForce ? kForce : 256, cost = kCost256 * ((wide + G - 1) / G);
-    int tiles = wide;
+    // Tiles of 256, 128 or 64 rows, whichever rounds of tiles take less time:
+    // large ones do more products per byte and stage, small ones fill the CUs.
+    int best = 256, cost = kCost256 * ((wide + G - 1) / G);
 #pragma unroll
     for (int rows = 128; rows >= 64; rows >>= 1) {
       const int n = gmm_tiles(g, tab, rows, wave_total) * nn;
       const int c = (rows == 128 ? kCost128 : kCost64) * ((n + G - 1) / G);
-      if (!kForce && c < cost) {
+      wide = n;
+      if (c < cost) {
         best = rows;
         cost = c;
       }
-      tiles = n;
     }
-    wide = best == 64 ? tiles : gmm_tiles(g, tab, best, wave_total) * nn;
+    if (best != 64) wide = gmm_tiles(g, tab, best, wave_total) * nn;
     if (best == 64) wide_walk<GLU, 64, 3>(g, tab, smem);
     else if (best == 128) wide_walk<GLU, 128, DEEP ? 3 : 2>(g, tab, smem);
     else wide_walk<GLU, 256, 2>(g, tab, smem);
