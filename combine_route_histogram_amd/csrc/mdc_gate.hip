@@ -9,17 +9,21 @@ namespace {
 // ---------------------------------------------------------------------------
 // One token is handled by LPT lanes of a wavefront (16: four tokens per
 // wavefront, or 64), lane l holding the scores of experts l*VPL .. +VPL in
-// registers.  K rounds of "largest key, lowest index" pick the experts: a
-// maximum and an index minimum over the LPT lanes with DPP moves.
+// registers.  K rounds of "largest key" pick the experts: a maximum in the lane
+// and over the lanes with DPP moves.
 //
 // Keys are the scores as ordered integers (order_key): integer maxima need no
 // NaN rules, and INT_MIN marks an expert that is off or already taken.
 //
-// The choice is the one that exact scores give.  Keys made of probabilities
-// are rounded, so the fp32 rounds run once more than K and compare neighbours:
-// when two keys closer than their error bound might be in the wrong order (and
-// are not equal by equal inputs), the wavefront repeats its tokens with 64-bit
-// scores.  Without a bias and groups the key is the logit itself, exact.
+// The choice is the one that exact scores give.  Three ways of picking, each
+// run where the one before found two neighbours in its order too close for it:
+//   packed  the key's upper bits with the expert's number below them, so that a
+//           round is one maximum: 16-bit logits without bias and groups fit
+//           exactly, other keys lose their lowest 8 to 11 bits;
+//   fp32    the whole fp32 key, and the lowest index among equal ones.  A logit
+//           is exact; a probability is off by some rounding;
+//   fp64    the same on 64-bit scores.
+// The rounds run once more than K to see the neighbour behind the last choice.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 
@@ -32,11 +36,53 @@ struct GateArgs {
   int groups, topk_groups, group_top;
   int sigmoid, renormalise;
   float scale;
+  int vec;              // rows of logits (and the bias) can be read in 16-byte pieces of VPL experts
 };
 
 __device__ __forceinline__ float gate_load(const float* p) { return *p; }
 __device__ __forceinline__ float gate_load(const _Float16* p) { return (float)*p; }
 __device__ __forceinline__ float gate_load(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// The VPL logits of a lane, from expert `base`; -inf past the last expert.
+typedef float v4f __attribute__((ext_vector_type(4)));
+template <int VPL>
+__device__ __forceinline__ void gate_row(const float* p, int base, const GateArgs& a, float (&z)[VPL]) {
+  if constexpr (VPL % 4 == 0) {
+    if (a.vec) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += 4) {
+        v4f v = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+        if (base < a.E) v = *reinterpret_cast<const v4f*>(p + base + j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[j + k] = v[k];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) z[j] = base + j < a.E ? p[base + j] : -__builtin_inff();
+}
+template <int VPL, typename T>
+__device__ __forceinline__ void gate_row(const T* p, int base, const GateArgs& a, float (&z)[VPL]) {
+  if constexpr (VPL % 8 == 0) {
+    if (a.vec) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += 8) {
+        v4u v = {0u, 0u, 0u, 0u};
+        if (base < a.E) v = *reinterpret_cast<const v4u*>(p + base + j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint16_t h = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+          const float f = gate_load(reinterpret_cast<const T*>(&h));
+          z[j + k] = base < a.E ? f : -__builtin_inff();
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) z[j] = base + j < a.E ? gate_load(p + base + j) : -__builtin_inff();
+}
 
 // NaN -> -inf (the expert is off), +inf -> the largest finite value.
 __device__ __forceinline__ float gate_clean(float z) {
@@ -123,134 +169,231 @@ inline int lds_slots(int lpt, int vpl) { return lpt * vpl + (lpt * vpl >> 5); }
 
 // What a token's lanes know after the rounds.
 struct GatePick {
-  int id, next_id;   // lane l < K: expert of choice l, and of choice l + 1 (-1: none)
-  bool near;         // the order of two keys is within their rounding
+  int id;      // lane l < K: expert of choice l (-1: none)
+  bool near;   // choices l and l + 1 may be in the wrong order
 };
 
-// Chooses the K experts of this lane's token from its cleaned logits.  near is
-// only looked for in fp32.
+template <typename Key>
+struct GateMax {
+  __device__ __forceinline__ Key operator()(Key x, Key y) const { return max(x, y); }
+};
+struct GateMin {
+  __device__ __forceinline__ int32_t operator()(int32_t x, int32_t y) const { return min(x, y); }
+};
+
+// Rounds on keys whose lowest bits give way to the expert's number (the lower
+// number the larger key, so that equal keys go to the lowest).  gap: what two
+// whole keys may differ by and still be in the wrong order; 0: the bits given up
+// are zero, the order is exact.
+template <int LPT, int VPL>
+__device__ __forceinline__ GatePick gate_rounds_packed(const int32_t (&key)[VPL], int K, int lane, float gap) {
+  constexpr int kBits = LPT * VPL <= 256 ? 8 : 11;
+  constexpr int32_t kNumber = (1 << kBits) - 1;
+  int32_t k[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    k[j] = key[j] == INT32_MIN ? INT32_MIN : (key[j] & ~kNumber) | (kNumber - (lane * VPL + j));
+  GatePick r{-1, false};
+  const int rounds = gap > 0.f ? K + 1 : K;
+  int32_t prev = INT32_MIN;
+  for (int t = 0; t < rounds; ++t) {
+    int32_t best = k[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) best = max(best, k[j]);
+    best = lanes_reduce<LPT>(best, GateMax<int32_t>());
+    if (__all(best == INT32_MIN)) break;   // (of this wavefront's tokens)
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) k[j] = k[j] == best ? INT32_MIN : k[j];
+    const int id = best == INT32_MIN ? -1 : kNumber - (best & kNumber);
+    if (lane == t) r.id = id;
+    if (lane == t - 1) {
+      // least distance of two keys with these upper bits (NaN behind +inf, which is near)
+      r.near = id >= 0 && gap > 0.f && !(key_value(prev & ~kNumber) - key_value(best | kNumber) > gap);
+    }
+    prev = best;
+  }
+  return r;
+}
+
+// Rounds on whole keys.
+template <int LPT, int VPL, typename Key>
+__device__ __forceinline__ GatePick gate_rounds(Key (&key)[VPL], Key off, int K, int lane, float gap) {
+  constexpr bool kExact = sizeof(Key) == 8;
+  const int base = lane * VPL;
+  GatePick r{-1, false};
+  const int rounds = !kExact && gap > 0.f ? K + 1 : K;
+  Key prev = off;
+  for (int t = 0; t < rounds; ++t) {
+    Key best = key[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+    best = lanes_reduce<LPT>(best, GateMax<Key>());
+    if (__all(best == off)) break;   // (of this wavefront's tokens)
+    int32_t id = INT32_MAX;
+#pragma unroll
+    for (int j = VPL - 1; j >= 0; --j) id = key[j] == best ? base + j : id;
+    id = lanes_reduce<LPT>(id, GateMin());
+    if (best == off) id = -1;
+    const int mine = id - base;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = mine == j ? off : key[j];
+    if (lane == t) r.id = id;
+    if (!kExact && lane == t - 1) {
+      r.near = id >= 0 && gap > 0.f && !(key_value((int32_t)prev) - key_value((int32_t)best) > gap);
+    }
+    prev = best;
+  }
+  return r;
+}
+
+// Keys of this lane's experts from its cleaned logits.  tol (fp32): bound on
+// what a key may be off by.
 template <int LPT, int VPL, typename Real>
-__device__ __forceinline__ GatePick gate_pick(const GateArgs& a, const float (&z)[VPL], int lane, float zmax,
-                                              typename GateKey<Real>::type* lds) {
+__device__ __forceinline__ void gate_keys(const GateArgs& a, const float (&z)[VPL], int lane, float zmax,
+                                          typename GateKey<Real>::type (&key)[VPL], float& tol) {
   typedef typename GateKey<Real>::type Key;
   constexpr Key kOff = GateKey<Real>::kOff;
   constexpr bool kExact = sizeof(Real) == 8;
   const int base = lane * VPL;
-  const bool by_logit = a.bias == nullptr && a.groups == 1;
-  Key key[VPL];
-  float tol = 0.f;   // bound on what two keys' difference may be off by (fp32)
-  if (by_logit) {
+  tol = 0.f;
+  if (a.bias == nullptr && a.groups == 1) {   // the order of the logits
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = z[j] > -__builtin_inff() ? (Key)order_key((Real)z[j]) : kOff;
+    return;
+  }
+  Real p[VPL];
+  if (a.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) p[j] = gate_inv((Real)1 + gate_exp(-(Real)z[j]));
+    // exp, sum and reciprocal: s (1 - s) |z| 2^-23 + 2 ulp of s, below 2^-22 each
+    tol = 0x1p-21f;
   } else {
-    Real p[VPL];
-    if (a.sigmoid) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) p[j] = gate_inv((Real)1 + gate_exp(-(Real)z[j]));
-      // exp, sum and reciprocal: s (1 - s) |z| 2^-23 + 2 ulp of s, below 2^-22 each
-      tol = 0x1p-20f;
-    } else {
-      Real sum = 0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        p[j] = z[j] > -__builtin_inff() ? gate_exp((Real)z[j] - (Real)zmax) : (Real)0;
-        sum += p[j];
-      }
-      sum = lanes_sum<LPT>(sum);
-      const Real inv = gate_inv(sum);   // (no expert live: infinite, and no key uses it)
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) p[j] *= inv;
-      // the sum's relative error (VPL + 6 additions) and the exponentials'
-      // reach every key in proportion to its probability, at most 1 / sum
-      tol = 0x1p-17f * (float)inv;
-    }
-    float kmax = 0.f;
+    Real sum = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      const Real k = a.bias == nullptr ? p[j] : p[j] + (Real)(base + j < a.E ? a.bias[base + j] : 0.f);
-      const bool on = z[j] > -__builtin_inff() && k > -(Real)__builtin_inff();
-      key[j] = on ? order_key(k) : kOff;
-      if (!kExact && on) kmax = fmaxf(kmax, fabsf((float)k));
+      p[j] = z[j] > -__builtin_inff() ? gate_exp((Real)z[j] - (Real)zmax) : (Real)0;
+      sum += p[j];
     }
-    if (!kExact) tol += 0x1p-22f * lanes_max<LPT>(fminf(kmax, 3.402823466e38f));   // the additions of the bias
+    sum = lanes_sum<LPT>(sum);
+    const Real inv = gate_inv(sum);   // (no expert live: infinite, and no key uses it)
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) p[j] *= inv;
+    // the sum's relative error (VPL + 6 additions) and the exponentials'
+    // reach every key in proportion to its probability, at most 1 / sum
+    tol = 0x1p-17f * (float)inv;
   }
-  GatePick r{-1, -1, false};
-  if (a.groups > 1) {
-    // lane g scans group g's keys in LDS for its group_top largest
-    const int size = a.E / a.groups;
+  float kmax = 0.f;
+  float b[VPL];
+  if (a.bias != nullptr) gate_row<VPL>(a.bias, base, a, b);
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const Real k = a.bias == nullptr ? p[j] : p[j] + (Real)b[j];
+    const bool on = z[j] > -__builtin_inff() && k > -(Real)__builtin_inff();
+    key[j] = on ? order_key(k) : kOff;
+    if (!kExact && on) kmax = fmaxf(kmax, fabsf((float)k));
+  }
+  if (!kExact) tol += 0x1p-22f * lanes_max<LPT>(fminf(kmax, 3.402823466e38f));   // the additions of the bias
+}
+
+// Turns off the keys of closed groups.  Returns whether the border between open
+// and closed groups is within the scores' rounding (fp32).
+template <int LPT, int VPL, typename Real>
+__device__ __forceinline__ bool gate_close_groups(const GateArgs& a, int lane, float tol,
+                                                  typename GateKey<Real>::type (&key)[VPL],
+                                                  typename GateKey<Real>::type* lds) {
+  typedef typename GateKey<Real>::type Key;
+  constexpr Key kOff = GateKey<Real>::kOff;
+  constexpr bool kExact = sizeof(Real) == 8;
+  const int base = lane * VPL;
+  const int size = a.E / a.groups;
+  const int per = size / VPL;   // lanes of a group, where it is made of whole lanes
+  const bool whole = size % VPL == 0 && (per & (per - 1)) == 0 && per <= 16;
+  // the group's two largest keys: in every lane of the group, or (LDS) of group g in lane g
+  Key first = kOff, second = kOff;
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      second = max(second, min(first, key[j]));
+      first = max(first, key[j]);
+    }
+    for (int o = 1; o < per; o <<= 1) {
+      const Key f = __shfl_xor(first, o, 64), s = __shfl_xor(second, o, 64);
+      second = max(max(second, s), min(first, f));
+      first = max(first, f);
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) lds[lds_slot(base + j)] = key[j];
-    __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    Key first = kOff, second = kOff;
-    const bool mine = lane < a.groups;
-    if (mine) {
+    if (lane < a.groups) {
       for (int i = 0; i < size; ++i) {
         const Key k = lds[lds_slot(lane * size + i)];
         second = max(second, min(first, k));
         first = max(first, k);
       }
     }
-    auto value = [](Key k) -> Real {
-      if (k == kOff) return -(Real)__builtin_inff();
-      if constexpr (kExact) {
-        return __longlong_as_double(k ^ ((k >> 63) & 0x7FFFFFFFFFFFFFFFll));
-      } else {
-        return key_value(k);
-      }
-    };
-    const Real score = a.group_top == 2 ? value(first) + value(second) : value(first);
-    const Key gkey = !mine ? kOff : score > -(Real)__builtin_inff() ? order_key(score) : (Key)(kOff + 1);
-    // rank of each group among the others
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const Key other = __shfl(gkey, (threadIdx.x & 63 & ~(LPT - 1)) + g, 64);
-      rank += other > gkey || (other == gkey && g < lane);
-    }
-    const bool open = mine && rank < a.topk_groups;
-    if (!kExact && a.topk_groups < a.groups) {
-      auto least = [](int32_t x, int32_t y) { return min(x, y); };
-      auto most = [](int32_t x, int32_t y) { return max(x, y); };
-      const int32_t lo = lanes_reduce<LPT>(open ? (int32_t)gkey : INT32_MAX, least);
-      const int32_t hi = lanes_reduce<LPT>(mine && !open ? (int32_t)gkey : INT32_MIN, most);
-      r.near = hi > kOff + 1 && !(key_value(lo) - key_value(hi) > 3.f * tol);   // a sum of two keys
-    }
-    const uint64_t opened = __ballot(open) >> (threadIdx.x & 63 & ~(LPT - 1));
-    const float per = 1.0f / (float)size;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  auto value = [](Key k) -> Real {
+    if (k == kOff) return -(Real)__builtin_inff();
+    if constexpr (kExact) return __longlong_as_double(k ^ ((k >> 63) & 0x7FFFFFFFFFFFFFFFll));
+    else return key_value(k);
+  };
+  const Real score = a.group_top == 2 ? value(first) + value(second) : value(first);
+  const int group = whole ? lane / per : lane, step = whole ? per : 1;
+  const bool mine = group < a.groups;
+  const Key gkey = !mine ? kOff : score > -(Real)__builtin_inff() ? order_key(score) : (Key)(kOff + 1);
+  int rank = 0;   // of this group among the others
+  const int lane0 = threadIdx.x & 63 & ~(LPT - 1);
+  for (int g = 0; g < a.groups; ++g) {
+    const Key other = __shfl(gkey, lane0 + g * step, 64);
+    rank += other > gkey || (other == gkey && g < group);
+  }
+  const bool open = mine && rank < a.topk_groups;
+  bool near = false;
+  if (!kExact && a.topk_groups < a.groups) {
+    const int32_t lo = lanes_reduce<LPT>(open ? (int32_t)gkey : INT32_MAX, GateMin());
+    const int32_t hi = lanes_reduce<LPT>(mine && !open ? (int32_t)gkey : INT32_MIN, GateMax<int32_t>());
+    near = hi > (int32_t)kOff + 1 && !(key_value(lo) - key_value(hi) > 4.f * tol);   // sums of two keys
+  }
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = open ? key[j] : kOff;
+  } else {
+    const uint64_t opened = __ballot(open) >> lane0;
+    const float inv = 1.0f / (float)size;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       // (e + 0.5) / size is at least 0.5 / size from a whole number: exact for e < 2048
-      const int g = (int)(((float)(base + j) + 0.5f) * per);
+      const int g = (int)(((float)(base + j) + 0.5f) * inv);
       if (!((opened >> (g & 63)) & 1)) key[j] = kOff;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  const int rounds = by_logit || kExact ? a.K : a.K + 1;
-  Key prev = kOff;
-  for (int k = 0; k < rounds; ++k) {
-    Key best = key[0];
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
-    best = lanes_reduce<LPT>(best, [](Key x, Key y) { return max(x, y); });
-    if (__all(best == kOff)) break;   // (of this wavefront's tokens)
-    int32_t id = INT32_MAX;
-#pragma unroll
-    for (int j = VPL - 1; j >= 0; --j) id = key[j] == best ? base + j : id;
-    id = lanes_reduce<LPT>(id, [](int32_t x, int32_t y) { return min(x, y); });
-    if (best == kOff) id = -1;
-    const int mine = id - base;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = mine == j ? kOff : key[j];
-    if (lane == k) r.id = id;
-    if (!kExact && !by_logit) {
-      if (lane == k - 1) {
-        r.next_id = id;
-        r.near |= id >= 0 && !(key_value((int32_t)prev) - key_value((int32_t)best) > 2.f * tol);
-      }
-      prev = best;
-    }
+  return near;
+}
+
+// Chooses the K experts of this lane's token.  EXACT16: the logits have 16 bits.
+template <int LPT, int VPL, bool EXACT16>
+__device__ __forceinline__ GatePick gate_pick(const GateArgs& a, const float (&z)[VPL], int lane, float zmax,
+                                              int64_t* lds) {
+  int32_t key[VPL];
+  float tol;
+  gate_keys<LPT, VPL, float>(a, z, lane, zmax, key, tol);
+  bool border = false;
+  if (a.groups > 1) border = gate_close_groups<LPT, VPL, float>(a, lane, tol, key, reinterpret_cast<int32_t*>(lds));
+  const bool by_logit = a.bias == nullptr && a.groups == 1;
+  const bool sixteen = by_logit && EXACT16;   // (fp16's 11 significant bits leave 13 of fp32's free, bf16's 16)
+  GatePick r = gate_rounds_packed<LPT, VPL>(key, a.K, lane, sixteen ? 0.f : by_logit ? 0x1p-149f : 2.f * tol);
+  if (!__any(border)) {
+    if (!__any(r.near)) return r;
+    r = gate_rounds<LPT, VPL, int32_t>(key, INT32_MIN, a.K, lane, 2.f * tol);   // (logits: tol is zero, no doubt left)
+    if (!__any(r.near)) return r;
   }
-  return r;
+  int64_t key64[VPL];
+  float none;
+  gate_keys<LPT, VPL, double>(a, z, lane, zmax, key64, none);
+  if (a.groups > 1) (void)gate_close_groups<LPT, VPL, double>(a, lane, 0.f, key64, lds);
+  return gate_rounds<LPT, VPL, int64_t>(key64, GateKey<double>::kOff, a.K, lane, 0.f);
 }
 
 template <typename T, int LPT, int VPL>
@@ -264,8 +407,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.E;
   const int base = lane * VPL;
   float z[VPL];
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) z[j] = base + j < a.E ? gate_load(row + base + j) : -__builtin_inff();
+  gate_row<VPL>(row, base, a, z);
   float zmax = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
@@ -274,13 +416,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   }
   if (!a.sigmoid) zmax = lanes_max<LPT>(zmax);
   int64_t* lds = gate_lds + (int64_t)slot * (LPT * VPL + (LPT * VPL >> 5));
-  GatePick r = gate_pick<LPT, VPL, float>(a, z, lane, zmax, reinterpret_cast<int32_t*>(lds));
-  if (r.near && r.id >= 0 && r.next_id >= 0 && a.groups == 1) {
-    // equal inputs have equal keys: their order by index is right
-    r.near = !(gate_load(row + r.id) == gate_load(row + r.next_id) &&
-               (a.bias == nullptr || a.bias[r.id] == a.bias[r.next_id]));
-  }
-  if (__any(r.near)) r = gate_pick<LPT, VPL, double>(a, z, lane, zmax, lds);
+  const GatePick r = gate_pick<LPT, VPL, sizeof(T) == 2>(a, z, lane, zmax, lds);
 
   // Weights from the logits of the chosen experts, choice k in lane k.
   const bool have = lane < a.K && r.id >= 0;
@@ -315,7 +451,8 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
 // Host side
 // ---------------------------------------------------------------------------
 template <typename T, int LPT, int VPL>
-void launch_gate(const GateArgs& a, hipStream_t s) {
+void launch_gate(GateArgs a, hipStream_t s) {
+  a.vec = a.E % VPL == 0 && a.E * sizeof(T) % 16 == 0 && aligned16(a.logits) && aligned16(a.bias);
   constexpr int kTokens = kGateThreads / LPT;
   const size_t lds = a.groups > 1 ? (size_t)kTokens * lds_slots(LPT, VPL) * sizeof(int64_t) : 0;
   hipLaunchKernelGGL((k_gate<T, LPT, VPL>), dim3((a.T + kTokens - 1) / kTokens), dim3(kGateThreads), lds, s, a);
@@ -365,7 +502,7 @@ mdc_status mdc_gate(const mdc_shape* shape, const mdc_gate_params* params, const
       !aligned4(expert_scales))
     return MDC_ERR_INVALID;
   const GateArgs a{logits, bias, expert_ids, expert_scales, (int)T, (int)E, shape->topk, p.groups, p.topk_groups,
-                   p.group_top, p.score == MDC_GATE_SIGMOID, p.renormalise, p.scale};
+                   p.group_top, p.score == MDC_GATE_SIGMOID, p.renormalise, p.scale, 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (p.dtype == MDC_DTYPE_BF16) launch_gate_typed<uint16_t>(a, s);
