@@ -15,15 +15,15 @@ namespace {
 // Keys are the scores as ordered integers (order_key): integer maxima need no
 // NaN rules, and INT_MIN marks an expert that is off or already taken.
 //
-// The choice is the one that exact scores give.  Three ways of picking, each
-// run where the one before found two neighbours in its order too close for it:
-//   packed  the key's upper bits with the expert's number below them, so that a
-//           round is one maximum: 16-bit logits without bias and groups fit
-//           exactly, other keys lose their lowest 8 to 11 bits;
-//   fp32    the whole fp32 key, and the lowest index among equal ones.  A logit
-//           is exact; a probability is off by some rounding;
-//   fp64    the same on 64-bit scores.
-// The rounds run once more than K to see the neighbour behind the last choice.
+// The choice is the one that 64-bit scores give.  A key in the rounds has the
+// expert's number in its lowest bits, so that a round is one maximum: 16-bit
+// logits without bias and groups fit exactly, other keys lose their lowest 8 to
+// 11 bits, and probabilities are off by some rounding besides.  Rounds run once
+// more than K to see the neighbour behind the last choice; where two neighbours
+// are too close for such keys, a few more choices are taken and put in order by
+// their scores in 64 bits, one choice a lane (gate_order); and only where that
+// cannot settle it (a long run of close keys, or close groups) are all of the
+// token's keys made again in 64 bits.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 
@@ -167,12 +167,6 @@ __device__ __forceinline__ double gate_inv(double v) { return 1.0 / v; }
 __device__ __forceinline__ int lds_slot(int e) { return e + (e >> 5); }
 inline int lds_slots(int lpt, int vpl) { return lpt * vpl + (lpt * vpl >> 5); }
 
-// What a token's lanes know after the rounds.
-struct GatePick {
-  int id;      // lane l < K: expert of choice l (-1: none)
-  bool near;   // choices l and l + 1 may be in the wrong order
-};
-
 template <typename Key>
 struct GateMax {
   __device__ __forceinline__ Key operator()(Key x, Key y) const { return max(x, y); }
@@ -180,71 +174,6 @@ struct GateMax {
 struct GateMin {
   __device__ __forceinline__ int32_t operator()(int32_t x, int32_t y) const { return min(x, y); }
 };
-
-// Rounds on keys whose lowest bits give way to the expert's number (the lower
-// number the larger key, so that equal keys go to the lowest).  gap: what two
-// whole keys may differ by and still be in the wrong order; 0: the bits given up
-// are zero, the order is exact.
-template <int LPT, int VPL>
-__device__ __forceinline__ GatePick gate_rounds_packed(const int32_t (&key)[VPL], int K, int lane, float gap) {
-  constexpr int kBits = LPT * VPL <= 256 ? 8 : 11;
-  constexpr int32_t kNumber = (1 << kBits) - 1;
-  int32_t k[VPL];
-#pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    k[j] = key[j] == INT32_MIN ? INT32_MIN : (key[j] & ~kNumber) | (kNumber - (lane * VPL + j));
-  GatePick r{-1, false};
-  const int rounds = gap > 0.f ? K + 1 : K;
-  int32_t prev = INT32_MIN;
-  for (int t = 0; t < rounds; ++t) {
-    int32_t best = k[0];
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) best = max(best, k[j]);
-    best = lanes_reduce<LPT>(best, GateMax<int32_t>());
-    if (__all(best == INT32_MIN)) break;   // (of this wavefront's tokens)
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) k[j] = k[j] == best ? INT32_MIN : k[j];
-    const int id = best == INT32_MIN ? -1 : kNumber - (best & kNumber);
-    if (lane == t) r.id = id;
-    if (lane == t - 1) {
-      // least distance of two keys with these upper bits (NaN behind +inf, which is near)
-      r.near = id >= 0 && gap > 0.f && !(key_value(prev & ~kNumber) - key_value(best | kNumber) > gap);
-    }
-    prev = best;
-  }
-  return r;
-}
-
-// Rounds on whole keys.
-template <int LPT, int VPL, typename Key>
-__device__ __forceinline__ GatePick gate_rounds(Key (&key)[VPL], Key off, int K, int lane, float gap) {
-  constexpr bool kExact = sizeof(Key) == 8;
-  const int base = lane * VPL;
-  GatePick r{-1, false};
-  const int rounds = !kExact && gap > 0.f ? K + 1 : K;
-  Key prev = off;
-  for (int t = 0; t < rounds; ++t) {
-    Key best = key[0];
-#pragma unroll
-    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
-    best = lanes_reduce<LPT>(best, GateMax<Key>());
-    if (__all(best == off)) break;   // (of this wavefront's tokens)
-    int32_t id = INT32_MAX;
-#pragma unroll
-    for (int j = VPL - 1; j >= 0; --j) id = key[j] == best ? base + j : id;
-    id = lanes_reduce<LPT>(id, GateMin());
-    if (best == off) id = -1;
-    const int mine = id - base;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = mine == j ? off : key[j];
-    if (lane == t) r.id = id;
-    if (!kExact && lane == t - 1) {
-      r.near = id >= 0 && gap > 0.f && !(key_value((int32_t)prev) - key_value((int32_t)best) > gap);
-    }
-    prev = best;
-  }
-  return r;
-}
 
 // Keys of this lane's experts from its cleaned logits.  tol (fp32): bound on
 // what a key may be off by.
@@ -265,8 +194,10 @@ __device__ __forceinline__ void gate_keys(const GateArgs& a, const float (&z)[VP
   if (a.sigmoid) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) p[j] = gate_inv((Real)1 + gate_exp(-(Real)z[j]));
-    // exp, sum and reciprocal: s (1 - s) |z| 2^-23 + 2 ulp of s, below 2^-22 each
-    tol = 0x1p-21f;
+    // in 2^-24: the exponent's product 1.5 |z| s (1 - s) <= 0.34, the
+    // exponential's ulp 2 s (1 - s) <= 0.5, the sum's rounding and the
+    // reciprocal's ulp one each
+    tol = 0x1p-22f;
   } else {
     Real sum = 0;
 #pragma unroll
@@ -292,7 +223,13 @@ __device__ __forceinline__ void gate_keys(const GateArgs& a, const float (&z)[VP
     key[j] = on ? order_key(k) : kOff;
     if (!kExact && on) kmax = fmaxf(kmax, fabsf((float)k));
   }
-  if (!kExact) tol += 0x1p-22f * lanes_max<LPT>(fminf(kmax, 3.402823466e38f));   // the additions of the bias
+  if (!kExact) tol += 0x1p-24f * lanes_max<LPT>(fminf(kmax, 3.402823466e38f));   // the addition of the bias
+}
+
+// Whether groups of `size` experts are 1, 2, 4 .. 16 whole lanes of vpl experts.
+__host__ __device__ inline bool gate_whole_lanes(int size, int vpl) {
+  const int per = size / vpl;
+  return size % vpl == 0 && (per & (per - 1)) == 0 && per <= 16;
 }
 
 // Turns off the keys of closed groups.  Returns whether the border between open
@@ -307,7 +244,7 @@ __device__ __forceinline__ bool gate_close_groups(const GateArgs& a, int lane, f
   const int base = lane * VPL;
   const int size = a.E / a.groups;
   const int per = size / VPL;   // lanes of a group, where it is made of whole lanes
-  const bool whole = size % VPL == 0 && (per & (per - 1)) == 0 && per <= 16;
+  const bool whole = gate_whole_lanes(size, VPL);
   // the group's two largest keys: in every lane of the group, or (LDS) of group g in lane g
   Key first = kOff, second = kOff;
   if (whole) {
@@ -354,7 +291,7 @@ __device__ __forceinline__ bool gate_close_groups(const GateArgs& a, int lane, f
   if (!kExact && a.topk_groups < a.groups) {
     const int32_t lo = lanes_reduce<LPT>(open ? (int32_t)gkey : INT32_MAX, GateMin());
     const int32_t hi = lanes_reduce<LPT>(mine && !open ? (int32_t)gkey : INT32_MIN, GateMax<int32_t>());
-    near = hi > (int32_t)kOff + 1 && !(key_value(lo) - key_value(hi) > 4.f * tol);   // sums of two keys
+    near = hi > (int32_t)kOff + 1 && !(key_value(lo) - key_value(hi) > 8.f * tol);   // two sums of two keys, rounded
   }
   if (whole) {
 #pragma unroll
@@ -372,28 +309,167 @@ __device__ __forceinline__ bool gate_close_groups(const GateArgs& a, int lane, f
   return near;
 }
 
-// Chooses the K experts of this lane's token.  EXACT16: the logits have 16 bits.
-template <int LPT, int VPL, bool EXACT16>
-__device__ __forceinline__ GatePick gate_pick(const GateArgs& a, const float (&z)[VPL], int lane, float zmax,
-                                              int64_t* lds) {
+// Rounds on keys whose lowest bits give way to the expert's number (the lower
+// number the larger key, so that equal keys go to the lowest): the id of choice
+// l in lane l.  gap: what two whole keys may differ by and still be in the wrong
+// order; 0: the bits given up are zero and the order is exact.  Where the first
+// K are not certain, `count` choices are returned (else K), near: choices l and
+// l + 1 of them may be in the wrong order.
+template <int LPT, int VPL>
+__device__ __forceinline__ int gate_rounds(const int32_t (&key)[VPL], int K, int lane, float gap, int& count,
+                                           bool& near) {
+  constexpr int kBits = LPT * VPL <= 256 ? 8 : 11;
+  constexpr int32_t kNumber = (1 << kBits) - 1;
+  int32_t k[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    k[j] = key[j] == INT32_MIN ? INT32_MIN : (key[j] & ~kNumber) | (kNumber - (lane * VPL + j));
+  // Runs of up to four keys, largest first: a round looks at the heads and
+  // moves up the run whose head it took.
+  constexpr int kRun = VPL < 4 ? VPL : 4;
+  auto order = [&](int i, int j) {
+    const int32_t hi = max(k[i], k[j]);
+    k[j] = min(k[i], k[j]);
+    k[i] = hi;
+  };
+#pragma unroll
+  for (int j = 0; j < VPL; j += kRun) {
+    if constexpr (kRun > 1) order(j, j + 1);
+    if constexpr (kRun > 2) {
+      order(j + 2, j + 3);
+      order(j, j + 2);
+      order(j + 1, j + 3);
+      order(j + 1, j + 2);
+    }
+  }
+  int32_t mine = INT32_MIN, best = INT32_MIN;
+  // Least distance of two keys with these upper bits (NaN behind +inf, which is near).
+  auto is_near = [&](int n) {
+    const int32_t below = __shfl_down(mine, 1, 64);
+    const int32_t next = lane == n - 1 ? best : below;
+    return lane < n && next != INT32_MIN && !(key_value(mine & ~kNumber) - key_value(next | kNumber) > gap);
+  };
+  near = false;
+  int rounds = gap > 0.f ? K + 1 : K;
+  const int more = count;
+  count = K;
+  for (int t = 0; t < rounds; ++t) {
+    best = k[0];
+#pragma unroll
+    for (int j = kRun; j < VPL; j += kRun) best = max(best, k[j]);
+    best = lanes_reduce<LPT>(best, GateMax<int32_t>());
+#pragma unroll
+    for (int j = 0; j < VPL; j += kRun) {
+      const bool hit = k[j] == best;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) k[j + i] = !hit ? k[j + i] : i + 1 < kRun ? k[j + i + 1] : INT32_MIN;
+    }
+    if (t >= K) {
+      near = is_near(t);
+      if (t == K && __any(near)) {
+        count = more;
+        rounds = more + 1;
+      }
+    }
+    mine = lane == t ? best : mine;
+  }
+  return mine != INT32_MIN ? kNumber - (mine & kNumber) : -1;
+}
+
+// Rounds on 64-bit keys.
+template <int LPT, int VPL>
+__device__ __forceinline__ int gate_rounds(int64_t (&key)[VPL], int K, int lane) {
+  constexpr int64_t kOff = GateKey<double>::kOff;
+  const int base = lane * VPL;
+  int chosen = -1;
+  for (int t = 0; t < K; ++t) {
+    int64_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+    best = lanes_reduce<LPT>(best, GateMax<int64_t>());
+    int32_t id = INT32_MAX;
+#pragma unroll
+    for (int j = VPL - 1; j >= 0; --j) id = key[j] == best ? base + j : id;
+    id = lanes_reduce<LPT>(id, GateMin());
+    if (best == kOff) id = -1;
+    const int mine = id - base;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = mine == j ? kOff : key[j];
+    if (lane == t) chosen = id;
+  }
+  return chosen;
+}
+
+// Puts the first K of `count` choices (id, in lane l choice l) in the order of
+// their scores in 64 bits.  A choice that is not near the one behind it is above
+// all behind it.  False: all from choice K - 1 on are near, so that experts
+// behind the last one would have to be looked at too.
+template <int LPT, int VPL, typename T>
+__device__ __forceinline__ bool gate_order(const GateArgs& a, const T* row, int lane, float zmax, int count, bool near,
+                                           int& id) {
+  const int lane0 = threadIdx.x & 63 & ~(LPT - 1);
+  const uint64_t ends = __ballot(!near && lane >= a.K - 1 && lane < count) >> lane0;
+  if (!__all((ends & (~0ull >> (64 - LPT))) != 0)) return false;
+  const bool by_logit = a.bias == nullptr && a.groups == 1;
+  double sum = 0;
+  if (!a.sigmoid && !by_logit) {
+#pragma unroll 2
+    for (int j = 0; j < VPL; ++j) {
+      const int e = min(lane * VPL + j, a.E - 1);
+      const float z = gate_clean(gate_load(row + e));
+      const double p = gate_exp((double)z - (double)zmax);
+      sum += lane * VPL + j < a.E && z > -__builtin_inff() ? p : 0.0;
+    }
+    sum = lanes_sum<LPT>(sum);
+  }
+  double key = -__builtin_inf();
+  if (lane < count && id >= 0) {
+    const double z = gate_clean(gate_load(row + id));
+    key = z;
+    if (!by_logit) {
+      key = a.sigmoid ? gate_inv(1.0 + gate_exp(-z)) : gate_exp(z - (double)zmax) * gate_inv(sum);
+      if (a.bias != nullptr) key += (double)a.bias[id];
+    }
+  }
+  int rank = 0;
+  for (int i = 0; i < count; ++i) {
+    const double other = __shfl(key, lane0 + i, 64);
+    const int from = __shfl(id, lane0 + i, 64);
+    rank += other > key || (other == key && from < id);
+  }
+  int ordered = -1;
+  for (int i = 0; i < count; ++i) {
+    const int there = __shfl(rank, lane0 + i, 64), from = __shfl(id, lane0 + i, 64);
+    ordered = there == lane ? from : ordered;
+  }
+  id = ordered;
+  return true;
+}
+
+// The experts of this lane's token: choice l in lane l < K, -1 for none.
+template <int LPT, int VPL, typename T>
+__device__ __forceinline__ int gate_pick(const GateArgs& a, const T* row, const float (&z)[VPL], int lane, float zmax,
+                                         int64_t* lds) {
   int32_t key[VPL];
   float tol;
   gate_keys<LPT, VPL, float>(a, z, lane, zmax, key, tol);
   bool border = false;
   if (a.groups > 1) border = gate_close_groups<LPT, VPL, float>(a, lane, tol, key, reinterpret_cast<int32_t*>(lds));
-  const bool by_logit = a.bias == nullptr && a.groups == 1;
-  const bool sixteen = by_logit && EXACT16;   // (fp16's 11 significant bits leave 13 of fp32's free, bf16's 16)
-  GatePick r = gate_rounds_packed<LPT, VPL>(key, a.K, lane, sixteen ? 0.f : by_logit ? 0x1p-149f : 2.f * tol);
   if (!__any(border)) {
-    if (!__any(r.near)) return r;
-    r = gate_rounds<LPT, VPL, int32_t>(key, INT32_MIN, a.K, lane, 2.f * tol);   // (logits: tol is zero, no doubt left)
-    if (!__any(r.near)) return r;
+    const bool by_logit = a.bias == nullptr && a.groups == 1;
+    // (fp16's 11 significant bits leave 13 of fp32's free, bf16's 16; fp32 logits are equal or a step apart)
+    const float gap = !by_logit ? 2.f * tol : sizeof(T) == 2 ? 0.f : 0x1p-149f;
+    int count = min(a.K + 4, LPT);
+    bool near;
+    int id = gate_rounds<LPT, VPL>(key, a.K, lane, gap, count, near);
+    if (!__any(near && lane < a.K)) return id;
+    if (gate_order<LPT, VPL>(a, row, lane, zmax, count, near, id)) return id;
   }
   int64_t key64[VPL];
   float none;
   gate_keys<LPT, VPL, double>(a, z, lane, zmax, key64, none);
   if (a.groups > 1) (void)gate_close_groups<LPT, VPL, double>(a, lane, 0.f, key64, lds);
-  return gate_rounds<LPT, VPL, int64_t>(key64, GateKey<double>::kOff, a.K, lane, 0.f);
+  return gate_rounds<LPT, VPL>(key64, a.K, lane);
 }
 
 template <typename T, int LPT, int VPL>
@@ -416,11 +492,11 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   }
   if (!a.sigmoid) zmax = lanes_max<LPT>(zmax);
   int64_t* lds = gate_lds + (int64_t)slot * (LPT * VPL + (LPT * VPL >> 5));
-  const GatePick r = gate_pick<LPT, VPL, sizeof(T) == 2>(a, z, lane, zmax, lds);
+  const int id = gate_pick<LPT, VPL>(a, row, z, lane, zmax, lds);
 
   // Weights from the logits of the chosen experts, choice k in lane k.
-  const bool have = lane < a.K && r.id >= 0;
-  const float zc = have ? gate_clean(gate_load(row + r.id)) : -__builtin_inff();
+  const bool have = lane < a.K && id >= 0;
+  const float zc = have ? gate_clean(gate_load(row + id)) : -__builtin_inff();
   float w = 0.f;
   if (a.sigmoid) {
     w = have ? 1.0f / (1.0f + expf(-zc)) : 0.f;
@@ -442,7 +518,7 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
     w = have ? expf(zc - zmax) / sum : 0.f;
   }
   if (lane < a.K && token < a.T) {
-    a.ids[(int64_t)token * a.K + lane] = r.id;
+    a.ids[(int64_t)token * a.K + lane] = id;
     a.weights[(int64_t)token * a.K + lane] = w * a.scale;
   }
 }
@@ -454,7 +530,7 @@ template <typename T, int LPT, int VPL>
 void launch_gate(GateArgs a, hipStream_t s) {
   a.vec = a.E % VPL == 0 && a.E * sizeof(T) % 16 == 0 && aligned16(a.logits) && aligned16(a.bias);
   constexpr int kTokens = kGateThreads / LPT;
-  const size_t lds = a.groups > 1 ? (size_t)kTokens * lds_slots(LPT, VPL) * sizeof(int64_t) : 0;
+  const size_t lds = a.groups > 1 && !gate_whole_lanes(a.E / a.groups, VPL) ? (size_t)kTokens * lds_slots(LPT, VPL) * sizeof(int64_t) : 0;
   hipLaunchKernelGGL((k_gate<T, LPT, VPL>), dim3((a.T + kTokens - 1) / kTokens), dim3(kGateThreads), lds, s, a);
 }
 
