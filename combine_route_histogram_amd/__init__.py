@@ -501,6 +501,13 @@ def prepare_dispatch_ffn(shape: Shape, inter_n: int, x, expand_q, dynamic_scales
 
 # ---- gate, norm and fp8 products: these also check that their tensors are on one GPU, and run there ----
 
+# The handle of a device's current stream and the current device as plain
+# integers: building torch's Stream object takes longer than the smallest of
+# these kernels.  Where torch has no such query the public ones serve.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 _DTYPES = {torch.bfloat16: MDC_DTYPE_BF16, torch.float16: MDC_DTYPE_FP16, torch.float32: MDC_DTYPE_FP32}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _SCORES = {"softmax": MDC_GATE_SOFTMAX, "sigmoid": MDC_GATE_SIGMOID}
@@ -515,7 +522,7 @@ class DevicePrepared(Prepared):
         self._device = device
 
     def _launch(self) -> int:
-        if self._device is None or torch.cuda.current_device() == self._device:
+        if self._device is None or _raw_device() == self._device:
             return self._fn(*self._args)
         with torch.cuda.device(self._device):
             return self._fn(*self._args)
@@ -544,7 +551,7 @@ def _one_device(*tensors) -> Optional[int]:
 
 def _device_stream(stream, device: Optional[int]) -> Optional[int]:
     if stream is None and device is not None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device)
     return _stream(stream)
 
 
