@@ -423,7 +423,7 @@ __device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, b
 }
 
 // ---------------------------------------------------------------------------
-// Experts with more rows: tiles of BM rows x 256 weight rows (SwiGLU: 128 gate
+// Experts with more rows: tiles of BM = 32 to 256 rows x 256 weight rows (SwiGLU: 128 gate
 // rows and the 128 up rows that go with them), one workgroup of eight
 // wavefronts per CU walking tiles.  Each k-block of 128 is one stage, loaded
 // global -> LDS directly into a ring of S stages while earlier ones are
@@ -435,9 +435,12 @@ __device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, b
 // writes lane l's 16 bytes at base + 16 l: eight rows per wavefront load, lane
 // l taking row l / 8 and the chunk that belongs in slot l % 8.
 //
-// The scales sa[row][b] sw[.][b] of four k-blocks lie behind the ring: thread
-// (row, weight half) loads, multiplies and stores those of two k-blocks every
-// second stage.
+// The scales sa[row][b] sw[.][b] of two periods of k-blocks lie behind the
+// ring: thread (row, weight half, group) loads, multiplies and stores those of
+// two k-blocks a period.  Tiles of 64 and 32 rows have threads for 8 and 16
+// k-blocks (a load of 32 rows takes the address unit 27 ns; taken by every
+// wavefront at every second k-block they cost a stage of 32 rows 0.1 of its 0.75
+// us).
 //
 // The direct loads take their LDS addresses as numbers, and the waits for them
 // are written out (a stage's before the barrier that opens it): told the array,
@@ -445,10 +448,12 @@ __device__ __forceinline__ int thin_split(const Gmm& g, int experts, int cols, b
 // ---------------------------------------------------------------------------
 constexpr int kWideW = 256;   // weight rows of a tile
 constexpr int wide_stage(int BM) { return (BM + kWideW) * kFp8Block; }
-constexpr int wide_bytes(int BM, int S) { return S * wide_stage(BM) + 4 * 2 * BM * 4; }
+constexpr int kWideScales = 8192;   // bytes of scales behind the ring
+constexpr int wide_bytes(int BM, int S) { return S * wide_stage(BM) + kWideScales; }
 // 128-row tiles take three stages where the experts' table leaves that much LDS.
 constexpr int kLdsDeep = wide_bytes(128, 3), kLdsFlat = wide_bytes(256, 2);
-static_assert(kLdsFlat >= wide_bytes(64, 3) && kLdsFlat >= wide_bytes(128, 2) && kLdsDeep >= kLdsFlat, "LDS of the tiles");
+static_assert(kLdsFlat >= wide_bytes(32, 3) && kLdsFlat >= wide_bytes(64, 3) && kLdsFlat >= wide_bytes(128, 2) &&
+                  kLdsDeep >= wide_bytes(32, 4) && kLdsDeep >= kLdsFlat, "LDS of the tiles");
 
 struct WideTile {
   int e, row0, rows, n0;   // n0: first weight row (SwiGLU: first output column)
@@ -460,7 +465,7 @@ template <bool GLU, int BM, int S, int NB>
 __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint8_t* smem, v4f (&acc)[BM / 32][4]) {
   constexpr int kStage = wide_stage(BM), kRing = S * kStage;
   constexpr int kTokenBytes = BM * kFp8Block;
-  constexpr int kTokenLoads = BM / 64;   // direct loads of token rows per wavefront and stage (8 rows each)
+  constexpr int kTokenLoads = (BM + 63) / 64;   // direct loads of token rows per wavefront and stage (8 rows each)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave >> 2, wn = wave & 3;
@@ -483,7 +488,8 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint
   // Direct loads of k-block b, of kLoads in kParts parts.  (No branches here
   // and below: they would split the schedule.)
   constexpr int kLoads = kTokenLoads + 4;
-  constexpr int kParts = NB / 2 + 1, kPart = (kLoads + kParts - 1) / kParts;
+  constexpr bool kFine = NB <= 2;   // a part behind each matrix instruction
+  constexpr int kParts = kFine ? 4 * NB : NB / 2 + 1, kPart = (kLoads + kParts - 1) / kParts;
   const unsigned lds = lds_at(smem);
   auto dma = [&](int at, int b, int part) {   // at: the stage's place in the ring
     unsigned v[2];
@@ -497,30 +503,35 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(lds + at + kTokenBytes + blk * 1024), 16, v[q & 1],
                                                  k0 + (unsigned)(8 * blk * K) + up, 0, 0);
       } else {
-        const int blk = kTokenLoads * wave + q - 4;
+        const int blk = (kTokenLoads * wave + q - 4) & (BM / 8 - 1);   // (BM = 32: two wavefronts load the same)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(lds + at + blk * 1024), 16, v[blk & 1],
                                                  k0 + (unsigned)(8 * blk * K), 0, 0);
       }
     }
   };
-  // ---- scales of k-blocks b, b + 1 (b even): thread (row, half), so that a
-  // wavefront's loads touch 32 rows (64 would take the address unit twice as long) ----
+  // ---- scales of the kPeriod k-blocks from b, a multiple of kPeriod: two of
+  // them for thread (row, weight half, group) ----
+  // (The larger tiles take the two next k-blocks every second stage, 128 rows
+  // twice: a condition in their loop makes the compiler spill.)
+  constexpr int kGroups = BM < 128 ? kGmmThreads / (2 * BM) : 1, kPeriod = 2 * kGroups;
+  static_assert(2 * kPeriod * 2 * BM * (int)sizeof(float) <= kWideScales, "two periods of scales");
   const int wb = (Nw + kFp8Block - 1) / kFp8Block;
-  const int srow = (tid >> 1) & (BM - 1), half = tid & 1;   // (BM = 128: two threads each)
+  const int sgroup = tid % kGroups, half = tid / kGroups & 1, srow = tid / (2 * kGroups) & (BM - 1);
   const int wblock = t.n0 / kFp8Block;
   const unsigned wnext = (unsigned)((GLU ? wb / 2 : min(1, wb - 1 - wblock)) * nk) * 4u;   // from the first half's scales
   const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<float*>(g.w_scale + ((int64_t)t.e * wb + wblock) * nk), (short)0, (int)wnext + nk * 4, 0x00020000);
   v2f sa, sw;
   auto scale_load = [&](int b) {
-    sa = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rs, (unsigned)(srow * nk) * 4u, (unsigned)b * 4u, 0));
-    sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, half ? wnext : 0u, (unsigned)b * 4u, 0));
+    sa = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rs, (unsigned)(srow * nk + 2 * sgroup) * 4u, (unsigned)b * 4u, 0));
+    sw = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rv, (half ? wnext : 0u) + 8u * (unsigned)sgroup, (unsigned)b * 4u, 0));
   };
-  float* const sc = reinterpret_cast<float*>(smem + kRing);   // [4][2 weight halves][BM], k-block b at b % 4
+  float* const sc = reinterpret_cast<float*>(smem + kRing);   // [2 kPeriod][2 weight halves][BM], k-block b at b % (2 kPeriod)
   auto scale_store = [&](int b) {
-    float* p = sc + (b & 3) * 2 * BM + half * BM + srow;
-    p[0] = b < nk ? sa[0] * sw[0] : 0.f;
-    p[2 * BM] = b + 1 < nk ? sa[1] * sw[1] : 0.f;
+    const int mine = b + 2 * sgroup;
+    float* p = sc + (mine & (2 * kPeriod - 1)) * 2 * BM + half * BM + srow;
+    p[0] = mine < nk ? sa[0] * sw[0] : 0.f;
+    p[2 * BM] = mine + 1 < nk ? sa[1] * sw[1] : 0.f;
   };
 
   // ---- fragments ----
@@ -544,7 +555,7 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint
     float s[GLU ? 2 : 1];
   };
   auto scale = [&](int b, int i) {
-    const float* p = my_sc + (b & 3) * 2 * BM + 32 * i;
+    const float* p = my_sc + (b & (2 * kPeriod - 1)) * 2 * BM + 32 * i;
     Sc s;
 #pragma unroll
     for (int h = 0; h < (GLU ? 2 : 1); ++h) s.s[h] = p[h * BM];
@@ -565,8 +576,9 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint
   scale_store(0);
   __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of stage 0 have landed
   lds_barrier();
-  dma((S - 1) * kStage, S - 1, 0);
-  scale_load(2);
+#pragma unroll
+  for (int part = 0; part < (kFine ? 4 : 1); ++part) dma((S - 1) * kStage, S - 1, part);
+  scale_load(kPeriod);
   v8i w[4], tok = tfrag(0, 0), tok_next;
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = wfrag(0, j);
@@ -580,22 +592,26 @@ __device__ __forceinline__ void wide_kloop(const Gmm& g, const WideTile& t, uint
   auto stage = [&](int b, bool odd) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      if (i + 1 < kParts) dma(last, b + S - 1, i + 1);   // (all at once they would hold up the products)
+      if (!kFine && i + 1 < kParts) dma(last, b + S - 1, i + 1);   // (all at once they would hold up the products)
       if (i + 1 < NB) {
         tok_next = tfrag(cur, i + 1);
         s_next = scale(b, i + 1);
       } else {
         __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of k-block b + 1 have landed
-        if (odd) scale_store(b + 1);          // (loaded two stages before)
+        if (odd && (b + 1) % kPeriod == 0) scale_store(b + 1);   // (loaded a period before)
         lds_barrier();
-        dma(cur, b + S, 0);
-        if (odd) scale_load(b + 3);
+        if (!kFine) dma(cur, b + S, 0);
+        if (odd && (b + 1) % kPeriod == 0) scale_load(b + 1 + kPeriod);
         tok_next = tfrag(nxt, 0);   // (after the last stage: read, never used)
         s_next = scale(b + 1, 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         p[j] = mfma_block(w[j], tok);
+        if (kFine) {
+          if (i + 1 == NB) dma(cur, b + S, j);
+          else dma(last, b + S - 1, 4 * (i + 1) + j);
+        }
         if (i + 1 == NB) w[j] = wfrag(nxt, j);
         if (j < 3) add(acc[(i + NB - 1) % NB][j + 1], p[j + 1], s_prev.s[GLU ? (j + 1) >> 1 : 0]);
         else add(acc[i][0], p[0], s_cur.s[0]);
@@ -630,7 +646,8 @@ __device__ __forceinline__ void wide_tile(const Gmm& g, const WideTile& t, uint8
   for (int i = 0; i < BM / 32; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (t.rows > BM * 3 / 4 || BM <= 64) wide_kloop<GLU, BM, S, BM / 32>(g, t, smem, acc);
+  if constexpr (BM <= 64) wide_kloop<GLU, BM, S, BM / 32>(g, t, smem, acc);
+  else if (t.rows > BM * 3 / 4) wide_kloop<GLU, BM, S, BM / 32>(g, t, smem, acc);
   else if (t.rows > BM / 2) wide_kloop<GLU, BM, S, (BM * 3 / 4 + 31) / 32>(g, t, smem, acc);
   else if (t.rows > BM / 4) wide_kloop<GLU, BM, S, BM / 64>(g, t, smem, acc);
   else wide_kloop<GLU, BM, S, (BM + 127) / 128>(g, t, smem, acc);
@@ -730,10 +747,14 @@ __device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, uin
     wide_tile<GLU, BM, S>(g, wide_place(g, tab, t, nn, BM, kCols), smem);
 }
 
-// What a k-block of a tile of 256, 128 and 64 rows takes, in tenths of a
-// microsecond (4096 x 4096 x 7168, 2048 and 1024 rows of it: 256 workgroups with
-// one tile each, 105, 65 and 48 us).
-constexpr int kCost256 = 19, kCost128 = 12, kCost64 = 8;
+// What a k-block of a tile of 256, 128, 64 and 32 rows takes, in tenths of a
+// microsecond (4096, 2048, 1024 and 512 rows x 4096 x 7168, so that 256
+// workgroups have one tile each: 118, 73, 48 and 39 us).  Both sides of the
+// choice: those 512 rows take 45 us in tiles of 64 rows and 65 us in tiles of
+// 128; 512 x 7168 x 2048 takes 21 us in 224 tiles of 64 rows and 27 us in two
+// rounds of 32-row tiles; 2048 x 7168 x 2048 41 us in tiles of 256 rows, 47 us
+// in two rounds of 128 and 56 us in four of 64.
+constexpr int kCost256 = 20, kCost128 = 12, kCost64 = 8, kCost32 = 6;
 
 // One workgroup per CU: the wide experts' tiles, then the thin experts'.
 // DEEP: the LDS holds three stages of 128-row tiles.
@@ -754,17 +775,18 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
     // large ones do more products per byte and stage, small ones fill the CUs.
     int best = 256, cost = kCost256 * ((wide + G - 1) / G);
 #pragma unroll
-    for (int rows = 128; rows >= 64; rows >>= 1) {
+    for (int rows = 128; rows >= 32; rows >>= 1) {
       const int n = gmm_tiles(g, tab, rows, wave_total) * nn;
-      const int c = (rows == 128 ? kCost128 : kCost64) * ((n + G - 1) / G);
+      const int c = (rows == 128 ? kCost128 : rows == 64 ? kCost64 : kCost32) * ((n + G - 1) / G);
       wide = n;
       if (c < cost) {
         best = rows;
         cost = c;
       }
     }
-    if (best != 64) wide = gmm_tiles(g, tab, best, wave_total) * nn;
-    if (best == 64) wide_walk<GLU, 64, 3>(g, tab, smem);
+    if (best != 32) wide = gmm_tiles(g, tab, best, wave_total) * nn;
+    if (best == 32) wide_walk<GLU, 32, DEEP ? 4 : 3>(g, tab, smem);
+    else if (best == 64) wide_walk<GLU, 64, 3>(g, tab, smem);
     else if (best == 128) wide_walk<GLU, 128, DEEP ? 3 : 2>(g, tab, smem);
     else wide_walk<GLU, 256, 2>(g, tab, smem);
   }
