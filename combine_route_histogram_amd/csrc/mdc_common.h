@@ -104,6 +104,14 @@ mdc_status check_shape(const mdc_shape* sh) {
   return MDC_OK;
 }
 
+// A grid of n workgroups in two dimensions: a launch takes fewer than 2^32
+// threads along one.  The kernel's number is grid_block(), which may be >= n.
+constexpr unsigned kGridRow = 1u << 20;
+inline dim3 grid_of(int64_t n) {
+  return n <= kGridRow ? dim3((unsigned)n) : dim3(kGridRow, (unsigned)((n + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ int64_t grid_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 mdc_status launched() { return hipGetLastError() == hipSuccess ? MDC_OK : MDC_ERR_HIP; }
 
 }  // namespace

@@ -478,9 +478,9 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   constexpr int kTokens = kGateThreads / LPT;
   const int lane = threadIdx.x & (LPT - 1);
   const int slot = threadIdx.x / LPT;
-  const int token = blockIdx.x * kTokens + slot;
-  const int t = min(token, a.T - 1);   // (lanes past the last token repeat it and store nothing)
-  const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.E;
+  const int64_t token = grid_block() * kTokens + slot;
+  const int64_t t = min(token, (int64_t)a.T - 1);   // (lanes past the last token repeat it and store nothing)
+  const T* row = static_cast<const T*>(a.logits) + t * a.E;
   const int base = lane * VPL;
   float z[VPL];
   gate_row<VPL>(row, base, a, z);
@@ -518,8 +518,8 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
     w = have ? expf(zc - zmax) / sum : 0.f;
   }
   if (lane < a.K && token < a.T) {
-    a.ids[(int64_t)token * a.K + lane] = id;
-    a.weights[(int64_t)token * a.K + lane] = w * a.scale;
+    a.ids[token * a.K + lane] = id;
+    a.weights[token * a.K + lane] = w * a.scale;
   }
 }
 
@@ -531,7 +531,7 @@ void launch_gate(GateArgs a, hipStream_t s) {
   a.vec = a.E % VPL == 0 && a.E * sizeof(T) % 16 == 0 && aligned16(a.logits) && aligned16(a.bias);
   constexpr int kTokens = kGateThreads / LPT;
   const size_t lds = a.groups > 1 && !gate_whole_lanes(a.E / a.groups, VPL) ? (size_t)kTokens * lds_slots(LPT, VPL) * sizeof(int64_t) : 0;
-  hipLaunchKernelGGL((k_gate<T, LPT, VPL>), dim3((a.T + kTokens - 1) / kTokens), dim3(kGateThreads), lds, s, a);
+  hipLaunchKernelGGL((k_gate<T, LPT, VPL>), grid_of(((int64_t)a.T + kTokens - 1) / kTokens), dim3(kGateThreads), lds, s, a);
 }
 
 template <typename T>

@@ -90,7 +90,9 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
   __shared__ float part[kNormThreads / 64];
   __shared__ uint32_t part_max[kNormThreads / 64];
   const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6;
-  const int64_t at = (int64_t)blockIdx.x * a.nvec;   // first vector of the row
+  const int64_t row = grid_block();
+  if (row >= a.rows) return;
+  const int64_t at = row * a.nvec;   // first vector of the row
   float h[VPT][8];
   float sum = 0.f;
 #pragma unroll
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
       if (i < a.nvec) {
         reinterpret_cast<uint2*>(a.q)[at + i] = uint2{s.codes4(h[u][0], h[u][1], h[u][2], h[u][3]),
                                                       s.codes4(h[u][4], h[u][5], h[u][6], h[u][7])};
-        if ((i & 15) == 0) a.q_scale[(int64_t)blockIdx.x * ((a.nvec + 15) >> 4) + (i >> 4)] = s.scale;
+        if ((i & 15) == 0) a.q_scale[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s.scale;
       }
     }
     amax = max(amax, m);
@@ -150,7 +152,8 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
     amax = 0;
     for (int w = 0; w < waves; ++w) amax = max(amax, part_max[w]);
     const float top = __uint_as_float(amax);
-    const float scale = amax != 0 ? 127.0f / top : 0.f;
+    float scale = amax != 0 ? 127.0f / top : 0.f;
+    if (scale > 3.402823466e38f) scale = 3.402823466e38f;   // (infinite, it would make NaN of the row's zeros)
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int i = tid + u * threads;
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
         reinterpret_cast<uint2*>(a.q)[at + i] = uint2{w[0], w[1]};
       }
     }
-    if (tid == 0) a.q_scale[blockIdx.x] = top / 127.0f;
+    if (tid == 0) a.q_scale[row] = top / 127.0f;
   }
 }
 
@@ -180,7 +183,7 @@ void launch_norm_quant(const NormArgs& a, hipStream_t s) {
   auto go = [&](auto vpt, auto kernel) {
     const int per = decltype(vpt)::value;
     const int threads = ((a.nvec + per - 1) / per + 63) / 64 * 64;
-    hipLaunchKernelGGL(kernel, dim3(a.rows), dim3(threads), 0, s, a);
+    hipLaunchKernelGGL(kernel, grid_of(a.rows), dim3(threads), 0, s, a);
   };
   if (a.nvec <= 64) go(std::integral_constant<int, 1>(), k_add_rms_norm<T, R, Wt, QUANT, 1>);
   else if (a.nvec <= 2 * 512) go(std::integral_constant<int, 2>(), k_add_rms_norm<T, R, Wt, QUANT, 2>);

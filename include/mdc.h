@@ -586,7 +586,7 @@ mdc_status mdc_gate(const mdc_shape* shape,
  *   q, q_scale = v in 8 bits (of the unrounded v):
  *     MDC_QUANT_INT8: one scale per row, as the quantised dispatch: amax =
  *       max|v|, q = clamp(rint(v * (127 / amax)), -127, 127), q_scale[row] =
- *       amax / 127; the form mdc_ffn_quant_input takes
+ *       amax / 127 (127 / amax at most the largest finite value); the form mdc_ffn_quant_input takes
  *     MDC_QUANT_FP8: e4m3 (OCP), one scale per 128 columns (the last run of
  *       a row may be shorter): amax = max(max|v|, 2^-110), q = rne_e4m3(448 v
  *       / amax), q_scale[row][ceil(H / 128)] = amax / 448; the form
@@ -598,8 +598,8 @@ mdc_status mdc_gate(const mdc_shape* shape,
  *   residual_dtype, weight [H] of weight_dtype (each dtype or fp32); q [rows][H]
  * residual may be NULL (then x is normalised as it is; residual_out, if given,
  * receives x in residual_dtype); residual_out, y and q may each be NULL, not
- * all of them.  residual_out may be residual or x itself, y may be x
- * itself (each element is read before it is written, by one thread); other
+ * all of them.  residual_out may be residual or (of its dtype) x itself, y may be
+ * x itself (each element is read before it is written, by one thread); other
  * overlaps are not allowed.  H must be a multiple of 8 (INVALID) and at most
  * MDC_MAX_NORM_HIDDEN (UNSUPPORTED); the rows' tensors are 16-byte aligned,
  * q 8-byte.
@@ -637,8 +637,11 @@ mdc_status mdc_add_rms_norm(const mdc_norm_params* params,
  *   y[r][c] = bf16_rne( sum over k-blocks b of a_scale[r][b] *
  *             w_scale[e][c / 128][b] * sum over k in block b of
  *             a[r][k] * w[e][c][k] ),  c < n
- * Products and sums are fp32; a k-block is 128 columns, the last one K % 128
- * where that is not zero.  Scales are any fp32 values.
+ * a k-block is 128 columns, the last one K % 128 where that is not zero.
+ * Scales are any fp32 values.  The sum over a k-block is the matrix
+ * instruction's: of eight consecutive k, each product is cut 2^13 below the
+ * power of two under the largest (2^(E - 13), E the sum of the exponents of
+ * that one's factors), their sum is exact; everything from there on is fp32.
  *
  *   a [A][K] e4m3, a_scale [A][ceil(K/128)] fp32, w [L][n][K] e4m3,
  *   w_scale [L][ceil(n/128)][ceil(K/128)] fp32, y [A][n] bf16 (rows past the
@@ -646,8 +649,8 @@ mdc_status mdc_add_rms_norm(const mdc_norm_params* params,
  *   all A rows.  Negative counts are read as zero.
  * a, w and y are 16-byte aligned.  K must be a multiple of 16 and n of 8, both
  * positive (else MDC_ERR_INVALID); n * K < 2^31, K <= 2^22, L <=
- * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and the tile count (A / 64 + L + 1) * ceil(n / 16) below 2^31 (else
- * MDC_ERR_UNSUPPORTED).  No workspace.
+ * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and (A / 32 + L + 1) * ceil(n / 16) <=
+ * 2^31 - 2^16 - 1 (else MDC_ERR_UNSUPPORTED).  No workspace.
  * ------------------------------------------------------------------------ */
 mdc_status mdc_gmm_fp8(int64_t capacity,
                        int32_t experts,
@@ -677,7 +680,8 @@ mdc_status mdc_gmm_fp8(int64_t capacity,
  * inter_n = N must be a positive multiple of 256 and H a multiple of 128; the
  * bounds of mdc_gmm_fp8 hold for both products.  The workspace (size from
  * mdc_ffn_fp8_workspace) holds the status block (all zero: nothing in this
- * call can fail on the data), q1, s1, q2, s2 and g of experts with few rows.
+ * call can fail on the data), q1, s1, q2, s2 and, where few columns meet few
+ * rows, g; two calls may share it if they do not run at the same time.
  * The flags of shape are checked and otherwise ignored.
  *
  * mdc_ffn_fp8_quant_input takes rows already in fp8: expand_q [A][H] e4m3 and
