@@ -23,7 +23,14 @@ namespace {
 // are too close for such keys, a few more choices are taken and put in order by
 // their scores in 64 bits, one choice a lane (gate_order); and only where that
 // cannot settle it (a long run of close keys, or close groups) are all of the
-// token's keys made again in 64 bits.
+// token's keys made again in 64 bits.  (Of sigmoid keys with a bias, 256 a
+// token, about one token in 100 goes the second way, one in 10^5 the third.)
+//
+// Bound: instructions.  32768 x 256 fp32 (sigmoid, bias, 4 of 8 groups, 8
+// choices) 24 us, of which memory needs 7: 14 us are a softmax without bias
+// where no keys are close, 2 the bias and the sigmoid, 5 wavefronts that take the
+// second way, whose code is read from memory first, 3 the groups.  16384 x 128
+// bf16 5.7 us, 32 x 256 6.4 us in a trace, where an empty kernel takes 5.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 
@@ -538,7 +545,9 @@ template <typename T>
 void launch_gate_typed(const GateArgs& a, hipStream_t s) {
   // Four tokens per wavefront where there are enough of them to fill the chip
   // that way; else, or where a token's experts need more registers than that
-  // leaves, a wavefront per token.
+  // leaves, a wavefront per token.  Sigmoid with bias, four tokens : one token, in
+  // us: 64 experts 6.6 : 6.7 at 2048 tokens, 6.7 : 7.5 at 4096, 8.1 : 13.3 at
+  // 16384; 256 experts in 8 groups 9.7 : 8.4, 9.9 : 9.9 and 16.6 : 20.8.
   const bool four = a.T >= 4096 && a.E <= 256 && a.groups <= 16;
   if (four && a.E <= 64) launch_gate<T, 16, 4>(a, s);
   else if (four && a.E <= 128) launch_gate<T, 16, 8>(a, s);

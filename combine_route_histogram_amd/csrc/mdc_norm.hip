@@ -12,6 +12,14 @@ namespace {
 // of squares is per-thread fp32 sums, then DPP adds and one LDS exchange.
 // Sixteen consecutive lanes hold one 128-column run, so an fp8 scale is a
 // maximum over a DPP row; the int8 row scale takes a second LDS exchange.
+//
+// Sums and everything up to the outputs are fp32; residual_out, y and q are
+// rounded once each, from the unrounded values.
+//
+// Bound: memory.  16384 rows of 7168 (bf16, residual in and out, y, fp8 rows
+// and scales: 1.06 GB) 184 us, 5.8 TB/s; 2051 x 5000 (fp16, fp32 residual, int8
+// out) 22 us, 5.1 TB/s; 32 x 7168 3.6 us, which is a launch and two trips to
+// memory.
 // ---------------------------------------------------------------------------
 struct NormArgs {
   const void* x;
@@ -185,8 +193,12 @@ void launch_norm_quant(const NormArgs& a, hipStream_t s) {
     const int threads = ((a.nvec + per - 1) / per + 63) / 64 * 64;
     hipLaunchKernelGGL(kernel, grid_of(a.rows), dim3(threads), 0, s, a);
   };
-  if (a.nvec <= 64) go(std::integral_constant<int, 1>(), k_add_rms_norm<T, R, Wt, QUANT, 1>);
-  else if (a.nvec <= 2 * 512) go(std::integral_constant<int, 2>(), k_add_rms_norm<T, R, Wt, QUANT, 2>);
+  // A vector per thread as far as a workgroup has threads: bf16 rows of 7168
+  // with y and fp8 out take 184 us (16384 rows) and 3.6 us (32 rows), with two
+  // vectors per thread 185 and 4.1, with four 200 and 5.3; rows of 512, 13.0,
+  // 13.5 and 14.0 us.  Longer rows need two or four.
+  if (a.nvec <= kNormThreads) go(std::integral_constant<int, 1>(), k_add_rms_norm<T, R, Wt, QUANT, 1>);
+  else if (a.nvec <= 2 * kNormThreads) go(std::integral_constant<int, 2>(), k_add_rms_norm<T, R, Wt, QUANT, 2>);
   else go(std::integral_constant<int, 4>(), k_add_rms_norm<T, R, Wt, QUANT, 4>);
 }
 
