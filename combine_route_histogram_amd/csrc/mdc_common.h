@@ -74,8 +74,6 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int k) {
 // Host side
 // ---------------------------------------------------------------------------
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Argument checks shared by every entry point.  MDC_ERR_INVALID: the fields do
@@ -103,14 +101,6 @@ mdc_status check_shape(const mdc_shape* sh) {
   if ((int64_t)sh->num_experts + sh->zero_experts + sh->copy_experts > INT32_MAX) return MDC_ERR_UNSUPPORTED;
   return MDC_OK;
 }
-
-// A grid of n workgroups in two dimensions: a launch takes fewer than 2^32
-// threads along one.  The kernel's number is grid_block(), which may be >= n.
-constexpr unsigned kGridRow = 1u << 20;
-inline dim3 grid_of(int64_t n) {
-  return n <= kGridRow ? dim3((unsigned)n) : dim3(kGridRow, (unsigned)((n + kGridRow - 1) / kGridRow));
-}
-__device__ __forceinline__ int64_t grid_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 mdc_status launched() { return hipGetLastError() == hipSuccess ? MDC_OK : MDC_ERR_HIP; }
 

@@ -2,7 +2,7 @@
 // norm, the row quantiser and the fp8 products.
 #pragma once
 
-#include "mdc_common.h"
+#include "mdc_ops.h"
 
 namespace {
 

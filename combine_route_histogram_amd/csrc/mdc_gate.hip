@@ -2,7 +2,7 @@
 // mdc_gate, whose ids and weights are the expert_ids and expert_scales of the
 // dispatch and the combine.
 
-#include "mdc_common.h"
+#include "mdc_ops.h"
 
 namespace {
 

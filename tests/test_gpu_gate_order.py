@@ -105,3 +105,15 @@ def test_no_tokens():
     e = torch.empty((0, 16), device=DEV)
     mdc.mdc_gate(shape, e, None, torch.empty((0, 2), dtype=torch.int32, device=DEV), torch.empty((0, 2), device=DEV))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,n,k,groups,topk_groups", [(5, 2040, 16, 8, 3), (4, 2048, 8, 2, 1), (4097, 250, 8, 5, 2),
+                                                     (4096, 256, 8, 16, 4), (4100, 240, 4, 15, 15), (6, 1530, 9, 51, 2),
+                                                     (4099, 16, 1, 16, 1), (3, 12, 12, 4, 4)])
+def test_groups_of_whole_lanes_and_others(T, n, k, groups, topk_groups, score):
+    logits, bias = make(T, n, torch.float32, n + groups)
+    for top in (1, 2):
+        if top <= n // groups:
+            check(logits, bias, k, score=score, groups=groups, topk_groups=topk_groups, group_top=top)
+    check(logits[:, :].bfloat16(), None, k, score=score, groups=groups, topk_groups=topk_groups, group_top=1)
