@@ -549,6 +549,13 @@ def _one_device(*tensors) -> Optional[int]:
     return device
 
 
+def _typed(t, name: str):
+    """`t`, which must be a tensor: its type or shape says what the call does."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"mdc: {name} must be a tensor, got {type(t).__name__}")
+    return t
+
+
 def _device_stream(stream, device: Optional[int]) -> Optional[int]:
     if stream is None and device is not None:
         return _raw_stream(device)
@@ -568,7 +575,7 @@ def prepare_gate(shape: Shape, logits, bias, expert_ids, expert_scales, score: s
     """Routes and weights from router logits [W*BS][E + Z + C] (bf16, fp16 or fp32); bias fp32 or None."""
     n = shape.num_experts + shape.zero_experts + shape.copy_experts
     tokens = shape.world * shape.bs
-    _need(logits, "logits", tuple(_DTYPES), tokens * n)
+    _need(_typed(logits, "logits"), "logits", tuple(_DTYPES), tokens * n)
     _need(bias, "bias", torch.float32, n)
     _need(expert_ids, "expert_ids", torch.int32, tokens * shape.topk)
     _need(expert_scales, "expert_scales", torch.float32, tokens * shape.topk)
@@ -590,6 +597,11 @@ def prepare_add_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=
     [H] of x's dtype or fp32; q int8 with q_scale [rows], or e4m3 (or uint8)
     with q_scale [rows][ceil(H / 128)].
     """
+    for t, name in ((x, "x"), (weight, "weight")):
+        _typed(t, name)
+    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (q, "q")):
+        if t is not None:
+            _typed(t, name)
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"mdc: x must be bf16 or fp16, got {x.dtype}")
     H = weight.numel()
@@ -624,7 +636,7 @@ def prepare_add_rms_norm(x, weight, residual=None, residual_out=None, y=None, q=
 def prepare_gmm_fp8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None) -> DevicePrepared:
     """Grouped fp8 product: a [A][K], a_scale [A][ceil(K/128)], w [L][n][K] (or [n][K]), w_scale
     [L][ceil(n/128)][ceil(K/128)], y [A][n] bf16; expert_token_nums [L], or None with one expert."""
-    if a.dim() != 2 or w.dim() not in (2, 3):
+    if _typed(a, "a").dim() != 2 or _typed(w, "w").dim() not in (2, 3):
         raise ValueError("mdc: a must have 2 dimensions, w 2 or 3")
     A, K = a.shape
     L, n = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2]
