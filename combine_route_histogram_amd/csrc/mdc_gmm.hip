@@ -147,6 +147,31 @@ __device__ __forceinline__ int gmm_tiles(const Gmm& g, GmmTable& t, int rows, in
   return __builtin_amdgcn_readfirstlane((int)(uint32_t)carry);
 }
 
+// Numbers of m-tiles of 128, 64 and 32 rows (at most 2^26 + L each).
+__device__ __forceinline__ void gmm_tile_counts(const Gmm& g, const GmmTable& t, int (&count)[3]) {
+  int n[3] = {0, 0, 0};
+  for (int e = threadIdx.x; e < g.L; e += kGmmThreads) {
+    const int rows = t.rows[e + 1] - t.rows[e];
+    if (rows > kThinRows)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) n[i] += (rows - 1) / (128 >> i) + 1;
+  }
+  __shared__ int part[3][kGmmWaves];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    n[i] = wave_inclusive_scan(n[i]);
+    if ((threadIdx.x & 63) == 63) part[i][threadIdx.x >> 6] = n[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    count[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kGmmWaves; ++w) count[i] += part[i][w];
+    count[i] = __builtin_amdgcn_readfirstlane(count[i]);
+  }
+}
+
 // Expert that m-tile m belongs to: the number of experts whose tiles end at or
 // before m.
 __device__ __forceinline__ int gmm_expert(const GmmTable& t, int L, int m) {
@@ -787,18 +812,17 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
   if (wide != 0) {
     // Tiles of 256, 128 or 64 rows, whichever rounds of tiles take less time:
     // large ones do more products per byte and stage, small ones fill the CUs.
-    int best = 256, cost = kCost256 * ((wide + G - 1) / G);
+    int best = 256, cost = kCost256 * ((wide + G - 1) / G), count[3];
+    gmm_tile_counts(g, tab, count);
 #pragma unroll
-    for (int rows = 128; rows >= 32; rows >>= 1) {
-      const int n = gmm_tiles(g, tab, rows, wave_total) * nn;
-      const int c = (rows == 128 ? kCost128 : rows == 64 ? kCost64 : kCost32) * ((n + G - 1) / G);
-      wide = n;
+    for (int i = 0; i < 3; ++i) {
+      const int c = (i == 0 ? kCost128 : i == 1 ? kCost64 : kCost32) * ((count[i] * nn + G - 1) / G);
       if (c < cost) {
-        best = rows;
+        best = 128 >> i;
         cost = c;
       }
     }
-    if (best != 32) wide = gmm_tiles(g, tab, best, wave_total) * nn;
+    if (best != 256) wide = gmm_tiles(g, tab, best, wave_total) * nn;
     if (best == 32) wide_walk<GLU, 32, DEEP ? 4 : 3>(g, tab, smem);
     else if (best == 64) wide_walk<GLU, 64, 3>(g, tab, smem);
     else if (best == 128) wide_walk<GLU, 128, DEEP ? 3 : 2>(g, tab, smem);
@@ -908,7 +932,8 @@ template <bool GLU>
 void launch_gmm(const Gmm& g, hipStream_t s) {
   const dim3 grid((device_cus() + 7) / 8 * 8), block(kGmmThreads);
   const size_t table = gmm_table_bytes(g.L);
-  if (table + kLdsDeep + 128 <= kLdsSize) hipLaunchKernelGGL((k_gmm<GLU, true>), grid, block, table, s, g);
+  if (table + kLdsDeep + 256 <= kLdsSize)   // (256: the plan's few words)
+    hipLaunchKernelGGL((k_gmm<GLU, true>), grid, block, table, s, g);
   else hipLaunchKernelGGL((k_gmm<GLU, false>), grid, block, table, s, g);
 }
 
