@@ -90,11 +90,9 @@ constexpr size_t gmm_table_bytes(int L) { return 2 * sizeof(int) * ((size_t)L + 
 template <int THREADS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* wave_total, int64_t& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t n = __shfl_up(v, o, 64);
-    if (lane >= o) v += n;
-  }
+  // in two halves of at most 30 bits' sum each: 0 <= v < 2^48
+  const int64_t low = wave_inclusive_scan((int)(v & 0xFFFFFF));
+  v = ((int64_t)wave_inclusive_scan((int)(v >> 24)) << 24) + low;
   if (lane == 63) wave_total[wave] = v;
   __syncthreads();
   all = 0;
