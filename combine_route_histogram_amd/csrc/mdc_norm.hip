@@ -131,23 +131,36 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int i = tid + u * threads;
+    float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // h * weight, v before the row's factor
     if (i < a.nvec) {
       if (a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
       float w[8];
       load8(static_cast<const Wt*>(a.weight) + i * 8, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[u][j] = h[u][j] * inv * w[j];
+      for (int j = 0; j < 8; ++j) {
+        t[j] = h[u][j] * w[j];
+        h[u][j] = t[j] * inv;
+      }
       if (a.y != nullptr) store8(static_cast<T*>(a.y) + (at + i) * 8, h[u]);
     }
     uint32_t m = 0;
     if (QUANT != MDC_QUANT_NONE)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(h[u][j]));
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(QUANT == MDC_QUANT_FP8 ? t[j] : h[u][j]));
     if (QUANT == MDC_QUANT_FP8) {
-      const Fp8Scaler s(row16_max(m));
+      // The row's factor is in v and in amax alike, so the codes are those of
+      // t, a rounding nearer (often all of 16-bit values' product); of v where
+      // t or v leaves the ordinary range.
+      m = row16_max(m);
+      const float top = __uint_as_float(m) * inv;
+      const bool plain = __uint_as_float(m) >= 0x1p-100f && top >= kFp8AmaxMin && top < __builtin_inff();
+      Fp8Scaler s(plain ? m : abs_bits(top));
+      if (plain) s.scale = top / kFp8Max;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = plain ? t[j] : h[u][j];
       if (i < a.nvec) {
-        reinterpret_cast<uint2*>(a.q)[at + i] = uint2{s.codes4(h[u][0], h[u][1], h[u][2], h[u][3]),
-                                                      s.codes4(h[u][4], h[u][5], h[u][6], h[u][7])};
+        reinterpret_cast<uint2*>(a.q)[at + i] = uint2{s.codes4(t[0], t[1], t[2], t[3]),
+                                                      s.codes4(t[4], t[5], t[6], t[7])};
         if ((i & 15) == 0) a.q_scale[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s.scale;
       }
     }
