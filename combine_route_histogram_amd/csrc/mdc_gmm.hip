@@ -28,10 +28,10 @@ namespace {
 //
 // Bounds (bf16 out): few rows per expert, memory (256 rows of 30 experts x 4096
 // x 7168, 880 MB of weights: 168 us, 5.27 TB/s); many rows, the matrix units'
-// power (2048 x 4096 x 7168 on one expert 64 us, 1.88 PFLOP/s; 16384 rows of 16
-// experts, both products of an FFN, 770 us, 1.87 PFLOP/s, where a library's fp8
+// power (2048 x 4096 x 7168 on one expert 60 us, 2.0 PFLOP/s; 16384 rows of 16
+// experts, both products of an FFN, 760 us, 1.9 PFLOP/s, where a library's fp8
 // product with one scale for all reaches 2.6); a few hundred rows, the time from
-// one stage of a tile to the next (512 rows, both products, 53 us).
+// one stage of a tile to the next (512 rows, both products, 49 us).
 // ---------------------------------------------------------------------------
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -786,8 +786,8 @@ __device__ __forceinline__ void wide_walk(const Gmm& g, const GmmTable& tab, uin
 
 // What a k-block of a tile of 256, 128, 64 and 32 rows takes, in tenths of a
 // microsecond (4096, 2048, 1024 and 512 rows x 4096 x 7168, so that 256
-// workgroups have one tile each: 118, 73, 48 and 39 us).  Both sides of the
-// choice: those 512 rows take 45 us in tiles of 64 rows and 65 us in tiles of
+// workgroups have one tile each: 118, 73, 48 and 39 us, the plan of the tiles 4
+// of them slower than now).  Both sides of the choice, likewise: those 512 rows take 45 us in tiles of 64 rows and 65 us in tiles of
 // 128; 512 x 7168 x 2048 takes 21 us in 224 tiles of 64 rows and 27 us in two
 // rounds of 32-row tiles; 2048 x 7168 x 2048 41 us in tiles of 256 rows, 47 us
 // in two rounds of 128 and 56 us in four of 64.
