@@ -33,6 +33,7 @@ namespace {
 // bf16 5.7 us, 32 x 256 6.4 us in a trace, where an empty kernel takes 5.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
+constexpr float kGateLowest = -709.7827f;   // 1 / (1 + exp(-z)) of this fp32 z and below is zero in 64 bits
 
 struct GateArgs {
   const void* logits;   // [T][E]
@@ -508,6 +509,12 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(GateArgs a) {
   if (a.sigmoid) {
     w = have ? 1.0f / (1.0f + expf(-zc)) : 0.f;
     if (a.renormalise) {
+      // Scores of logits below -87 leave fp32, their quotients do not: where the
+      // largest chosen logit is negative, every score is divided by its
+      // exponential.  (A score is zero where it is in 64 bits, whose exp(-z)
+      // ends at z = -709.78.)
+      const float top = lanes_max<LPT>(zc);
+      if (top < 0.f) w = zc > kGateLowest ? expf(zc - top) / (1.0f + expf(zc)) : 0.f;
       const float sum = lanes_sum<LPT>(w);
       w = sum > 0.f ? w / sum : 0.f;
     }

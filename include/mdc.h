@@ -540,9 +540,12 @@ typedef enum {
  *          such a route and, if it is active, counts it in dropped_ids)
  *   expert_scales = p of the chosen ids; with renormalise divided by
  *          their sum (all zero if that is zero); times scale.  0 for id -1.
- * The choice is the one exact arithmetic makes: with softmax or sigmoid keys
- * whose fp32 values are too close to tell apart, a token is decided in 64
- * bits.  Weights are computed in fp32.
+ * The choice is the one that scores in 64 bits give: with softmax or sigmoid
+ * keys whose fp32 values are too close to tell apart, a token is decided in 64
+ * bits.  (There, sigmoid scores of logits above 36.7 are one, those of logits
+ * below -709.78 zero: with a bias or groups such ids are ties.)  Weights are
+ * computed in fp32; renormalised sigmoid weights from quotients that stay in
+ * its range as long as the scores are not zero in 64 bits.
  *
  *   logits        [W][BS][n], of params->dtype
  *   bias          [n] fp32 or NULL
