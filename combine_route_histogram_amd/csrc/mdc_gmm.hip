@@ -133,7 +133,7 @@ __device__ __forceinline__ int gmm_tiles(const Gmm& g, GmmTable& t, int rows, in
     const int e = e0 + threadIdx.x;
     const int n = e < g.L ? t.rows[e + 1] - t.rows[e] : 0;
     const bool thin = n > 0 && n <= kThinRows;
-    const int64_t mine = thin ? (int64_t)1 << 32 : n > 0 ? (n + rows - 1) / rows : 0;
+    const int64_t mine = thin ? (int64_t)1 << 32 : n > 0 ? (n - 1) / rows + 1 : 0;   // (n up to 2^31 - 1)
     const int64_t end = carry + block_scan<kGmmThreads>(mine, wave_total, all);
     if (e < g.L) t.tiles[e + 1] = (int)(uint32_t)end;
     if (thin) t.thin[(int)(end >> 32) - 1] = (uint16_t)e;
