@@ -138,8 +138,8 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
       load8(static_cast<const Wt*>(a.weight) + i * 8, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        t[j] = h[u][j] * w[j];
-        h[u][j] = t[j] * inv;
+        if (QUANT == MDC_QUANT_FP8) t[j] = h[u][j] * w[j];
+        h[u][j] = h[u][j] * inv * w[j];   // (h times a large or tiny weight may leave fp32)
       }
       if (a.y != nullptr) store8(static_cast<T*>(a.y) + (at + i) * 8, h[u]);
     }
@@ -150,14 +150,21 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
     if (QUANT == MDC_QUANT_FP8) {
       // The row's factor is in v and in amax alike, so the codes are those of
       // t, a rounding nearer (often all of 16-bit values' product); of v where
-      // t or v leaves the ordinary range.
+      // t or v leaves the ordinary range (for all 16 lanes of a run or none).
       m = row16_max(m);
       const float top = __uint_as_float(m) * inv;
       const bool plain = __uint_as_float(m) >= 0x1p-100f && top >= kFp8AmaxMin && top < __builtin_inff();
-      Fp8Scaler s(plain ? m : abs_bits(top));
-      if (plain) s.scale = top / kFp8Max;
+      if (!plain) {
+        m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = plain ? t[j] : h[u][j];
+        for (int j = 0; j < 8; ++j) {
+          t[j] = h[u][j];
+          m = max(m, abs_bits(t[j]));
+        }
+        m = row16_max(m);
+      }
+      Fp8Scaler s(m);
+      if (plain) s.scale = top / kFp8Max;
       if (i < a.nvec) {
         reinterpret_cast<uint2*>(a.q)[at + i] = uint2{s.codes4(t[0], t[1], t[2], t[3]),
                                                       s.codes4(t[4], t[5], t[6], t[7])};
