@@ -94,9 +94,12 @@ def test_one_matrix_without_counts():
 def check_ffn_elements(counts, H, N, capacity, seed=0):
     """Each element of the FFN's y, from fp8 rows.  h is exact as above; g is then off by the rounding of fp32's
     operations only, so that its codes are known but for those whose value lies that near a border."""
-    used = sum(counts)
     g = torch.Generator().manual_seed(seed)
     L, I = len(counts), N // 2
+    given, counts, used = counts, [], 0
+    for c in given:   # negative counts are none, rows past the capacity are not there
+        counts.append(min(max(c, 0), capacity - used))
+        used += counts[-1]
     # sums of h: multiples of 2^-7, at most 4 H 2^-4
     q, qs = small_codes(g, capacity, H), powers(g, -2, 0, capacity, H // 128)
     w1, s1 = small_codes(g, L, N, H), powers(g, -5, -4, L, N // 128, H // 128)
@@ -104,7 +107,7 @@ def check_ffn_elements(counts, H, N, capacity, seed=0):
     shape = mdc.Shape(1, 0, capacity, H, 1, L, capacity)
     ws = torch.full((mdc.mdc_ffn_fp8_workspace(shape, N),), 0x5A, dtype=torch.uint8, device=DEV)
     y = torch.full((capacity, H), 3.0, dtype=BF, device=DEV)
-    mdc.mdc_ffn_fp8_quant_input(shape, N, *[t.to(DEV) for t in (q, qs, torch.tensor(counts), w1, s1, w2, s2)], y, ws)
+    mdc.mdc_ffn_fp8_quant_input(shape, N, *[t.to(DEV) for t in (q, qs, torch.tensor(given), w1, s1, w2, s2)], y, ws)
     torch.cuda.synchronize()
     h = O.grouped(widened(q[:used], qs[:used]), widened(w1, s1), counts)
     gate, up = h[:, :I], h[:, I:]
@@ -140,3 +143,8 @@ def test_elements_of_the_ffn(counts, H, N, capacity):
 @pytest.mark.parametrize("counts", [[1024, 1000], [900, 600, 200, 300, 40], [250, 200, 130], [100, 60], [20, 9] * 8])
 def test_elements_of_the_ffn_over_its_tiles(counts):
     check_ffn_elements(counts, 128, 8192, sum(counts) + 9, seed=sum(counts))
+
+
+@pytest.mark.parametrize("counts,capacity", [([20, -3, 30, 2 ** 40, 7], 70), ([30, 5, 9], 33), ([300, 50, -5, 900], 400)])
+def test_ffn_counts_past_the_capacity(counts, capacity):
+    check_ffn_elements(counts, 256, 512, capacity, seed=capacity)
