@@ -543,7 +543,8 @@ typedef enum {
  * The choice is the one that scores in 64 bits give: with softmax or sigmoid
  * keys whose fp32 values are too close to tell apart, a token is decided in 64
  * bits.  (There, sigmoid scores of logits above 36.7 are one, those of logits
- * below -709.78 zero: with a bias or groups such ids are ties.)  Weights are
+ * below -709.78 and softmax scores 745 below the largest logit zero: with a bias
+ * or groups such ids are ties.)  Weights are
  * computed in fp32; renormalised sigmoid weights from quotients that stay in
  * its range as long as the scores are not zero in 64 bits.
  *
@@ -596,6 +597,8 @@ mdc_status mdc_gate(const mdc_shape* shape,
  *       mdc_gmm_fp8 and mdc_ffn_fp8_quant_input take
  *     Zeros give codes 0 and scale 0.  A row or run that holds NaN or an
  *     infinity has a scale, and in fp8 codes, that are not finite.
+ * h^2 is summed in fp32: with values of about 1e19 and up, or of 1e-19 and
+ * below with eps = 0 (zero rows among them), a row's norm leaves its range.
  *
  *   x [rows][H] and y of dtype (bf16 or fp16); residual, residual_out of
  *   residual_dtype, weight [H] of weight_dtype (each dtype or fp32); q [rows][H]
@@ -641,7 +644,8 @@ mdc_status mdc_add_rms_norm(const mdc_norm_params* params,
  *             w_scale[e][c / 128][b] * sum over k in block b of
  *             a[r][k] * w[e][c][k] ),  c < n
  * a k-block is 128 columns, the last one K % 128 where that is not zero.
- * Scales are any fp32 values.  The sum over a k-block is the matrix
+ * Scales are any fp32 values whose products a_scale * w_scale, formed first,
+ * are fp32 values too.  The sum over a k-block is the matrix
  * instruction's: of eight consecutive k, each product is cut 2^13 below the
  * power of two under the largest (2^(E - 13), E the sum of the exponents of
  * that one's factors), their sum is exact; everything from there on is fp32.
@@ -685,7 +689,8 @@ mdc_status mdc_gmm_fp8(int64_t capacity,
  * mdc_ffn_fp8_workspace) holds the status block (all zero: nothing in this
  * call can fail on the data), q1, s1, q2, s2 and, where few columns meet few
  * rows, g; two calls may share it if they do not run at the same time.
- * The flags of shape are checked and otherwise ignored.
+ * With A == 0 nothing is written, the status block included.  The flags of shape
+ * are checked and otherwise ignored.
  *
  * mdc_ffn_fp8_quant_input takes rows already in fp8: expand_q [A][H] e4m3 and
  * dynamic_scales [A][H/128] (mdc_add_rms_norm's q and q_scale).
