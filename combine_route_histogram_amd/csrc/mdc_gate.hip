@@ -26,11 +26,14 @@ namespace {
 // token's keys made again in 64 bits.  (Of sigmoid keys with a bias, 256 a
 // token, about one token in 100 goes the second way, one in 10^5 the third.)
 //
-// Bound: instructions.  32768 x 256 fp32 (sigmoid, bias, 4 of 8 groups, 8
-// choices) 24 us, of which memory needs 7: 14 us are a softmax without bias
-// where no keys are close, 2 the bias and the sigmoid, 5 wavefronts that take the
-// second way, whose code is read from memory first, 3 the groups.  16384 x 128
-// bf16 5.7 us, 32 x 256 6.4 us in a trace, where an empty kernel takes 5.
+// Bound: vector instructions and the one round of wavefronts they run in.  32768
+// x 256 fp32, 8 choices, is 8192 wavefronts, 8 a SIMD: 700 instructions each for
+// a softmax without bias where no keys are close, 960 with sigmoid and bias, 1160
+// with 4 of 8 groups as well.  At 4 cycles each that is 9, 13 and 16 us of the
+// 19, 24 and 27 such launches take under the counters (23 to 25 us unprofiled;
+// memory needs 5): the rest is waiting, about 5 us of it for the code of the
+// second way, which few wavefronts run.  16384 x 128 bf16 take 5.8 us and 32 x 256
+// 5.2 to 7.8 in a trace, where an empty kernel of as many workgroups takes 1.4 to 1.6.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 constexpr float kGateLowest = -709.7827f;   // 1 / (1 + exp(-z)) of this fp32 z and below is zero in 64 bits

@@ -26,12 +26,17 @@ namespace {
 // two e4m3 significands have 8 bits, so only those far below the largest lose
 // any.  Nothing else is below fp32 until y is rounded to bf16 (or g to e4m3).
 //
-// Bounds (bf16 out): few rows per expert, memory (256 rows of 30 experts x 4096
-// x 7168, 880 MB of weights: 168 us, 5.27 TB/s); many rows, the matrix units'
-// power (2048 x 4096 x 7168 on one expert 60 us, 2.0 PFLOP/s; 16384 rows of 16
-// experts, both products of an FFN, 760 us, 1.9 PFLOP/s, where a library's fp8
-// product with one scale for all reaches 2.6); a few hundred rows, the time from
-// one stage of a tile to the next (512 rows, both products, 49 us).
+// Bounds (bf16 out).  Few rows per expert: memory, 256 rows of 30 experts x 4096
+// x 7168 (883 MB of weights) 168 us, 5.27 TB/s, where a plain read of 1 GiB reaches
+// 7.1.  Many rows: the matrix units have work for 38 to 47% of the time, at 1.9 to
+// 2.1 GHz in place of 2.4; 2048 x 4096 x 7168 on one expert 60 us, 2.0 PFLOP/s, as
+// fast as the library's product with one scale for all; 16384 rows of 16 experts,
+// both products of an FFN, 752 us, 1.9 PFLOP/s, where the library's keeps the units
+// busy for 76% of the time at the same clock (2.6 PFLOP/s): the direct loads are a
+// quarter of a stage and the scales' FMAs a seventh.  Up to a few hundred rows on
+// few experts: the number of k-blocks one workgroup walks, one after another
+// (48 rows of one expert x 4096 x 7168 take 45 us and 256 rows 46, on 32 of the 256
+// CUs and on 128; 512 rows, both products, 49 us).
 // ---------------------------------------------------------------------------
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -69,8 +74,12 @@ struct Gmm {
 // Rows and tiles of the experts.  Every workgroup works out the plan from the
 // counts by itself, in LDS.  Experts with at most kThinRows rows, two blocks of
 // the matrix instruction, are "thin": what counts there is to stream the
-// weights.  The others are "wide".  (With thin experts of up to 16 rows only, the
-// 256 rows above, 1 to 32 of them an expert, took 219 us in place of 168.)
+// weights.  The others are "wide".  Where the border lies between 16 and 32 rows
+// makes no difference to the 256 rows above, 1 to 32 of them an expert (167 and 168
+// us).  24 rows an expert x 4096 x 7168, thin : wide, in us: 1 expert 19 : 47, 4
+// experts 35 : 55, 8 experts 58 : 65, 16 experts 101 : 88, 32 experts 193 : 166.
+// The border is at 32 for the few experts' sake, where the wide tiles leave most
+// CUs idle; many experts with 17 to 32 rows each pay up to 20% for it.
 // ---------------------------------------------------------------------------
 constexpr int kGmmThreads = 512;
 constexpr int kGmmWaves = kGmmThreads / 64;
@@ -839,8 +848,8 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm(Gmm g) {
 
 // ---------------------------------------------------------------------------
 // Rows to fp8: one scale per 128 columns, 16 lanes x 8 values per block.  Bound:
-// memory (16384 x 7168 bf16 65 us, 5.4 TB/s; in a decode step, 256 rows, 5 us:
-// the launch).
+// memory (16384 x 7168 bf16 62 to 65 us, 5.5 to 5.7 TB/s; in a decode step, 256
+// rows, 5 us, of which an empty launch is 1.8).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 
@@ -916,9 +925,12 @@ unsigned device_cus() {
 // Whether thin experts' SwiGLU outputs go through memory in fp32 and a launch
 // that quantises them: where the 128-column blocks are too few for the CUs, and
 // the capacity says that thin experts are what there is (which experts are thin
-// is known on the device only).  FFN of 7168 and 4096 with 8 rows an expert, whole
-// blocks : split, in us: 16 blocks 62 : 31, 64 blocks 68 : 47, 128 blocks 100 :
-// 84, 192 blocks 120 : 120, 256 blocks 141 : 148.
+// is known on the device only, and g has a row for each of the capacity's).  FFN
+// of 7168 and 4096 with 8 rows an expert, whole blocks : split, in us: 16 blocks 74
+// : 33, 64 blocks 82 : 52, 128 blocks 98 : 83, 192 blocks 119 : 118, 256 blocks 138
+// : 142, 384 blocks 221 : 208 (one and a half rounds of 256 workgroups; a larger
+// bound would split the 256 blocks too).  A capacity above kSplitRows rows an expert
+// takes whole blocks at any number of them.
 constexpr int kSplitBlocks = 192, kSplitRows = 128;
 bool gmm_split(int64_t A, int64_t L, int64_t cols) {
   return L * (cols / kFp8Block) < kSplitBlocks && A <= L * kSplitRows;

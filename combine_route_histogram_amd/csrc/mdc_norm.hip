@@ -17,9 +17,9 @@ namespace {
 // rounded once each, from the unrounded values.
 //
 // Bound: memory.  16384 rows of 7168 (bf16, residual in and out, y, fp8 rows
-// and scales: 1.06 GB) 184 us, 5.8 TB/s; 2051 x 5000 (fp16, fp32 residual, int8
-// out) 22 us, 5.1 TB/s; 32 x 7168 3.6 us, which is a launch and two trips to
-// memory.
+// and scales: 1.06 GB) 184 us, 5.8 TB/s, where a plain read and a plain write of
+// its bytes take 172; 2051 x 5000 (fp16, fp32 residual, int8 out) 23 us, 4.9 TB/s;
+// 32 x 7168 3.8 us, of which an empty launch takes 1.4 and trips to memory the rest.
 // ---------------------------------------------------------------------------
 struct NormArgs {
   const void* x;
