@@ -50,6 +50,8 @@ MDC_MAX_GATE_EXPERTS = 2048
 MDC_MAX_GATE_GROUPS = 64
 MDC_QUANT_NONE, MDC_QUANT_INT8, MDC_QUANT_FP8 = 0, 1, 2
 MDC_MAX_NORM_HIDDEN = 32768
+MDC_ACT_NONE, MDC_ACT_SIGMOID, MDC_ACT_TANH = 0, 1, 2
+MDC_MAX_MOE_TOKENS = 32
 
 EXPORTS = (
     "mdc_status_string", "mdc_abi_version",
@@ -58,6 +60,7 @@ EXPORTS = (
     "mdc_ffn_workspace", "mdc_ffn_workspace_size", "mdc_ffn", "mdc_dispatch_quant", "mdc_dispatch_quant_gather",
     "mdc_ffn_quant_input", "mdc_dispatch_noalloc", "mdc_dispatch_ffn",
     "mdc_gate", "mdc_add_rms_norm", "mdc_gmm_fp8", "mdc_ffn_fp8_workspace", "mdc_ffn_fp8", "mdc_ffn_fp8_quant_input",
+    "mdc_gmm_int8", "mdc_block_rms_norm", "mdc_moe_workspace", "mdc_moe_fp8_workspace", "mdc_moe", "mdc_moe_fp8",
 )
 
 
@@ -78,6 +81,14 @@ class mdc_norm_params(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("quant", ctypes.c_int32),
                 ("eps", ctypes.c_float)]
+
+
+class mdc_block_norm_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("gate_every", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("gate_columns", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                ("quant", ctypes.c_int32), ("block_scale", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("post_eps", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 _P = ctypes.c_void_p
@@ -119,6 +130,14 @@ _sig("mdc_gmm_fp8", ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int
 _sig("mdc_ffn_fp8_workspace", _SHP, ctypes.c_int32, ctypes.POINTER(_SZ))
 _sig("mdc_ffn_fp8", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
 _sig("mdc_ffn_fp8_quant_input", _SHP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P)
+_sig("mdc_gmm_int8", ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P,
+     _P, _P)
+_sig("mdc_block_rms_norm", ctypes.POINTER(mdc_block_norm_params), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P)
+for _n in ("mdc_moe_workspace", "mdc_moe_fp8_workspace"):
+    _sig(_n, _SHP, ctypes.c_int32, ctypes.POINTER(_SZ))
+for _n in ("mdc_moe", "mdc_moe_fp8"):
+    _sig(_n, _SHP, ctypes.POINTER(mdc_gate_params), ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+         _SZ, _P)
 MDC_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -278,6 +297,20 @@ def mdc_ffn_fp8_workspace(shape: Shape, inter_n: int) -> int:
     out = _SZ(0)
     sh = shape.c()
     _check(_lib.mdc_ffn_fp8_workspace(ctypes.byref(sh), int(inter_n), ctypes.byref(out)), "mdc_ffn_fp8_workspace")
+    return int(out.value)
+
+
+def mdc_moe_workspace(shape: Shape, inter_n: int) -> int:
+    out = _SZ(0)
+    sh = shape.c()
+    _check(_lib.mdc_moe_workspace(ctypes.byref(sh), int(inter_n), ctypes.byref(out)), "mdc_moe_workspace")
+    return int(out.value)
+
+
+def mdc_moe_fp8_workspace(shape: Shape, inter_n: int) -> int:
+    out = _SZ(0)
+    sh = shape.c()
+    _check(_lib.mdc_moe_fp8_workspace(ctypes.byref(sh), int(inter_n), ctypes.byref(out)), "mdc_moe_fp8_workspace")
     return int(out.value)
 
 
@@ -499,7 +532,7 @@ def prepare_dispatch_ffn(shape: Shape, inter_n: int, x, expand_q, dynamic_scales
     return Prepared(_lib.mdc_dispatch_ffn, args, "mdc_dispatch_ffn", (sh, _tensors(locals())))
 
 
-# ---- gate, norm and fp8 products: these also check that their tensors are on one GPU, and run there ----
+# ---- gate, norms, products and the layer for a few tokens: these also check that their tensors are on one GPU, and run there ----
 
 # The handle of a device's current stream and the current device as plain
 # integers: building torch's Stream object takes longer than the smallest of
@@ -690,6 +723,149 @@ def prepare_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_sc
     return DevicePrepared(_lib.mdc_ffn_fp8_quant_input, args, "mdc_ffn_fp8_quant_input", keep, device)
 
 
+def prepare_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None) -> DevicePrepared:
+    """Grouped int8 product: a [A][K], a_scale [A], w [L][n][K] (or [n][K]), w_scale [L][n], y [A][n] bf16, fp16 or
+    fp32; expert_token_nums [L], or None with one expert."""
+    if _typed(a, "a").dim() != 2 or _typed(w, "w").dim() not in (2, 3):
+        raise ValueError("mdc: a must have 2 dimensions, w 2 or 3")
+    A, K = a.shape
+    L, n = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2]
+    if w.shape[-1] != K:
+        raise ValueError(f"mdc: w has rows of {w.shape[-1]} elements, a of {K}")
+    _need(a, "a", torch.int8, A * K)
+    _need(a_scale, "a_scale", torch.float32, A)
+    _need(expert_token_nums, "expert_token_nums", torch.int64, L)
+    _need(w, "w", torch.int8, L * n * K)
+    _need(w_scale, "w_scale", torch.float32, L * n)
+    _need(_typed(y, "y"), "y", tuple(_DTYPES), A * n)
+    keep = (a, a_scale, expert_token_nums, w, w_scale, y)
+    device = _one_device(*keep)
+    args = (A, L, n, K, _DTYPES[y.dtype], _ptr(a), _ptr(a_scale), _ptr(expert_token_nums), _ptr(w), _ptr(w_scale),
+            _ptr(y), _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_gmm_int8, args, "mdc_gmm_int8", keep, device)
+
+
+_ACTS = {"none": MDC_ACT_NONE, "sigmoid": MDC_ACT_SIGMOID, "tanh": MDC_ACT_TANH}
+
+
+def prepare_block_rms_norm(x, weight=None, post_weight=None, gate=None, gate_every: Optional[int] = None,
+                           gate_act: str = "none", residual=None, residual_out=None, y=None, q=None, q_scale=None,
+                           block_scale: float = 1.0, residual_scale: float = 1.0, post_eps: float = 1e-6,
+                           eps: float = 1e-6, stream=None) -> DevicePrepared:
+    """Norm of a block's output x [..., H] (bf16 or fp16), its gate, the scaled residual, and the norm behind it.
+
+    residual and residual_out are of x's dtype or fp32 (both the same), weight and post_weight [H] of x's dtype or
+    fp32 (both the same), gate [..., H] or [..., 1] of x's dtype or fp32, row r of x taking its row r // gate_every
+    (default: a gate of one row is for all rows, else each has its own); q int8 with q_scale [rows], or e4m3 (or
+    uint8) with q_scale [rows][ceil(H / 128)].
+    """
+    _typed(x, "x")
+    for t, name in ((weight, "weight"), (post_weight, "post_weight"), (gate, "gate"), (residual, "residual"),
+                    (residual_out, "residual_out"), (q, "q")):
+        if t is not None:
+            _typed(t, name)
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"mdc: x must be bf16 or fp16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("mdc: x must have rows")
+    H, numel = x.shape[-1], x.numel()
+    rows = numel // H if H else 0
+    wide = (x.dtype, torch.float32)
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        _need(t, name, wide, H)
+        if t is not None and t.numel() != H:
+            raise ValueError(f"mdc: x has rows of {H} elements, {name} holds {t.numel()}")
+    if weight is not None and post_weight is not None and weight.dtype != post_weight.dtype:
+        raise ValueError(f"mdc: post_weight must be {weight.dtype} as weight, got {post_weight.dtype}")
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        _need(t, name, wide, numel)
+    res_dtype = x.dtype if residual is None and residual_out is None else \
+        (residual if residual is not None else residual_out).dtype
+    if residual_out is not None and residual_out.dtype != res_dtype:
+        raise ValueError(f"mdc: residual_out must be {res_dtype} as residual, got {residual_out.dtype}")
+    columns, every, gate_dtype = 1, 1, x.dtype
+    if gate is not None:
+        gate_dtype, columns = gate.dtype, gate.shape[-1] if gate.dim() else 0
+        if columns not in (1, H):
+            raise ValueError(f"mdc: gate must have rows of {H} elements or of one, got {columns}")
+        gate_rows = gate.numel() // columns
+        every = (max(rows, 1) if gate_rows == 1 else 1) if gate_every is None else int(gate_every)
+        if every < 1:
+            raise ValueError(f"mdc: gate_every must be positive, got {every}")
+        _need(gate, "gate", wide, -(-rows // every) * columns)
+    if gate_act not in _ACTS:
+        raise ValueError(f"mdc: gate_act must be none, sigmoid or tanh, got {gate_act!r}")
+    _need(y, "y", x.dtype, numel)
+    quant = MDC_QUANT_NONE
+    if q is not None:
+        _need(q, "q", (torch.int8,) + _E4M3, numel)
+        quant = MDC_QUANT_INT8 if q.dtype == torch.int8 else MDC_QUANT_FP8
+        _need(q_scale, "q_scale", torch.float32, rows * (1 if quant == MDC_QUANT_INT8 else -(-H // 128)))
+    elif q_scale is not None:
+        raise ValueError("mdc: q_scale without q")
+    w_dtype = x.dtype if weight is None and post_weight is None else \
+        (weight if weight is not None else post_weight).dtype
+    pr = mdc_block_norm_params(rows, every, H, _DTYPES[x.dtype], _DTYPES[res_dtype], _DTYPES[w_dtype],
+                               _DTYPES[gate_dtype], columns, _ACTS[gate_act], quant, float(block_scale),
+                               float(residual_scale), float(post_eps), float(eps))
+    keep = (x, post_weight, gate, residual, weight, residual_out, y, q, q_scale)
+    device = _one_device(*keep)
+    args = (pr, *[_ptr(t) for t in keep], _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_block_rms_norm, args, "mdc_block_rms_norm", keep, device)
+
+
+def _prepare_moe(int8: bool, shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2,
+                 w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups,
+                 group_top, renormalise, scale, stream) -> DevicePrepared:
+    T, H, K, N, L = shape.bs, shape.hidden, shape.topk, int(inter_n), shape.local_experts
+    n = shape.num_experts + shape.zero_experts + shape.copy_experts
+    for t, name in ((x, "x"), (shared_expert_x, "shared_expert_x"), (ori_x, "ori_x"), (x_out, "x_out")):
+        _need(t, name, _BF16, T * H)
+    _need(expert_ids, "expert_ids", torch.int32, T * K)
+    _need(expert_scales, "expert_scales", torch.float32, T * K)
+    _check_mask(shape, x_active_mask, 1)
+    codes = torch.int8 if int8 else _E4M3
+    _need(w1, "w1", codes, L * N * H)
+    _need(w1_scale, "w1_scale", torch.float32, L * N if int8 else L * (N // 128) * (H // 128))
+    _need(w2, "w2", codes, L * H * (N // 2))
+    _need(w2_scale, "w2_scale", torch.float32, L * H if int8 else L * (H // 128) * (N // 256))
+    pr = None
+    if logits is not None:
+        _need(_typed(logits, "logits"), "logits", tuple(_DTYPES), T * n)
+        _need(bias, "bias", torch.float32, n)
+        if score not in _SCORES:
+            raise ValueError(f"mdc: score must be softmax or sigmoid, got {score!r}")
+        pr = mdc_gate_params(_DTYPES[logits.dtype], _SCORES[score], int(groups), int(topk_groups), int(group_top),
+                             1 if renormalise else 0, float(scale))
+    keep = (x, logits, bias, expert_ids, expert_scales, x_active_mask, w1, w1_scale, w2, w2_scale, shared_expert_x,
+            ori_x, x_out, workspace)
+    device = _one_device(*keep)
+    args = (shape.c(), pr, N, *[_ptr(t) for t in keep], _nbytes(workspace), _device_stream(stream, device))
+    return DevicePrepared(_lib.mdc_moe if int8 else _lib.mdc_moe_fp8, args, "mdc_moe" if int8 else "mdc_moe_fp8", keep,
+                          device)
+
+
+def prepare_moe(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                x_out, workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax",
+                groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+                stream=None) -> DevicePrepared:
+    """A layer of int8 experts for shape.bs tokens x [BS][H]; logits None: the routes are given in expert_ids and
+    expert_scales, else these are written (or None)."""
+    return _prepare_moe(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                        x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                        renormalise, scale, stream)
+
+
+def prepare_moe_fp8(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                    x_out, workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax",
+                    groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalise: bool = True,
+                    scale: float = 1.0, stream=None) -> DevicePrepared:
+    """prepare_moe with e4m3 experts, scales for each block of 128."""
+    return _prepare_moe(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                        x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                        renormalise, scale, stream)
+
+
 # ----------------------------------------------------------------------------
 # one-shot calls (marshal and launch)
 # ----------------------------------------------------------------------------
@@ -792,6 +968,37 @@ def mdc_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_scales
                             w2, w2_scale, y, workspace, stream=None, check: bool = True) -> int:
     return _run_on_device(prepare_ffn_fp8_quant_input(shape, inter_n, expand_q, dynamic_scales, expert_token_nums, w1,
                                                       w1_scale, w2, w2_scale, y, workspace, stream), check)
+
+
+def mdc_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream), check)
+
+
+def mdc_block_rms_norm(x, weight=None, post_weight=None, gate=None, gate_every: Optional[int] = None,
+                       gate_act: str = "none", residual=None, residual_out=None, y=None, q=None, q_scale=None,
+                       block_scale: float = 1.0, residual_scale: float = 1.0, post_eps: float = 1e-6, eps: float = 1e-6,
+                       stream=None, check: bool = True) -> int:
+    return _run_on_device(prepare_block_rms_norm(x, weight, post_weight, gate, gate_every, gate_act, residual,
+                                                 residual_out, y, q, q_scale, block_scale, residual_scale, post_eps,
+                                                 eps, stream), check)
+
+
+def mdc_moe(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale, x_out,
+            workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax", groups: int = 1,
+            topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None,
+            check: bool = True) -> int:
+    return _run_on_device(_prepare_moe(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale,
+                                       w2, w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score,
+                                       groups, topk_groups, group_top, renormalise, scale, stream), check)
+
+
+def mdc_moe_fp8(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                x_out, workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax",
+                groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+                stream=None, check: bool = True) -> int:
+    return _run_on_device(_prepare_moe(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale,
+                                       w2, w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score,
+                                       groups, topk_groups, group_top, renormalise, scale, stream), check)
 
 
 def alloc_dispatch_outputs(shape: Shape, device="cuda"):

@@ -1,0 +1,187 @@
+// libmdc: the norms before and after a block with its gate and residual scale,
+// for AMD Instinct MI355X (gfx950): mdc_block_rms_norm.
+
+#include "mdc_rows.h"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// h = residual_scale * residual + block_scale * act(gate) * x * inv_x * post,
+// with inv_x = 1 / sqrt(mean(x^2) + post_eps) known only after the row was read.
+// Everything a row needs is loaded before the sum of x^2: p = x * post * gate and
+// the scaled residual stay in registers, and one FMA with inv_x makes h of them.
+// (Where both norms are inside fp32's range, p is: it is h divided by inv_x.)
+// Then h^2 is summed and the outputs leave as for mdc_add_rms_norm.
+//
+// Sums and everything up to the outputs are fp32; residual_out, y and q are
+// rounded once each, from the unrounded values.
+// ---------------------------------------------------------------------------
+struct BlockArgs {
+  const void* x;
+  const void* post;      // or NULL: no norm of x
+  const void* gate;      // or NULL
+  const void* res;       // or NULL
+  const void* weight;    // or NULL: residual_out is the only output
+  void* res_out;         // or NULL
+  NormOut out;
+  int rows, nvec;        // vectors of 8 elements per row
+  int gate_every;        // rows that share a gate row
+  int gate_wide;         // a gate row has a value for each column
+  int gate32;            // the gate is fp32
+  int act;
+  float block_scale, res_scale, post_eps, eps, inv_hidden;
+};
+
+__device__ __forceinline__ float block_act(float g, int act) {
+  if (act == MDC_ACT_SIGMOID) return 1.0f / (1.0f + expf(-g));
+  if (act == MDC_ACT_TANH) return tanhf(g);
+  return g;
+}
+
+__device__ __forceinline__ float load1(const Bf16* p) { return __uint_as_float((uint32_t)p->bits << 16); }
+__device__ __forceinline__ float load1(const _Float16* p) { return (float)*p; }
+
+template <typename T, typename R, typename Wt, int QUANT, int VPT>
+__global__ __launch_bounds__(kNormThreads) void k_block_rms_norm(BlockArgs a) {
+  __shared__ float part[2][kNormThreads / 64];
+  __shared__ uint32_t part_max[kNormThreads / 64];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int64_t row = grid_block();
+  if (row >= a.rows) return;
+  const int64_t at = row * a.nvec;   // first vector of the row
+  const int64_t gate_row = (int)row / a.gate_every;
+  float gate1 = 1.f;
+  if (a.gate != nullptr && !a.gate_wide)
+    gate1 = block_act(a.gate32 ? static_cast<const float*>(a.gate)[gate_row] : load1(static_cast<const T*>(a.gate) + gate_row),
+                      a.act);
+  gate1 *= a.block_scale;
+  float h[VPT][8], r[VPT][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int i = tid + u * threads;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[u][j] = r[u][j] = 0.f;
+    if (i < a.nvec) {
+      load8(static_cast<const T*>(a.x) + (at + i) * 8, h[u]);
+      if (a.res != nullptr) load8(static_cast<const R*>(a.res) + (at + i) * 8, r[u]);
+      float w[8];
+      if (a.post != nullptr) {
+        load8(static_cast<const Wt*>(a.post) + i * 8, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[u][j], h[u][j], sum);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[u][j] *= w[j];
+      }
+      if (a.gate_wide) {
+        const int64_t g = (gate_row * a.nvec + i) * 8;
+        if (a.gate32) load8(static_cast<const float*>(a.gate) + g, w);
+        else load8(static_cast<const T*>(a.gate) + g, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[u][j] *= block_act(w[j], a.act) * a.block_scale;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[u][j] *= gate1;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[u][j] *= a.res_scale;
+    }
+  }
+  float inv = 1.f;
+  if (a.post != nullptr) inv = 1.0f / sqrtf(row_sum(sum, part[0]) * a.inv_hidden + a.post_eps);
+  sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int i = tid + u * threads;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[u][j] = __builtin_fmaf(h[u][j], inv, r[u][j]);
+      sum = __builtin_fmaf(h[u][j], h[u][j], sum);
+    }
+    if (i < a.nvec && a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
+  }
+  if (a.weight == nullptr) return;
+  inv = 1.0f / sqrtf(row_sum(sum, part[1]) * a.inv_hidden + a.eps);
+  norm_outputs<T, QUANT, VPT>(a.out, row, h, inv, part_max, [&](int, int i, float (&w)[8]) {
+    load8(static_cast<const Wt*>(a.weight) + i * 8, w);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <typename T, typename R, typename Wt, int QUANT>
+void launch_block_quant(const BlockArgs& a, hipStream_t s) {
+  auto go = [&](auto vpt, auto kernel) {
+    const int per = decltype(vpt)::value;
+    const int threads = ((a.nvec + per - 1) / per + 63) / 64 * 64;
+    hipLaunchKernelGGL(kernel, grid_of(a.rows), dim3(threads), 0, s, a);
+  };
+  // A vector per thread as far as a workgroup has threads; longer rows need two or four.
+  if (a.nvec <= kNormThreads) go(std::integral_constant<int, 1>(), k_block_rms_norm<T, R, Wt, QUANT, 1>);
+  else if (a.nvec <= 2 * kNormThreads) go(std::integral_constant<int, 2>(), k_block_rms_norm<T, R, Wt, QUANT, 2>);
+  else go(std::integral_constant<int, 4>(), k_block_rms_norm<T, R, Wt, QUANT, 4>);
+}
+
+template <typename T, typename R, typename Wt>
+void launch_block(const BlockArgs& a, int quant, hipStream_t s) {
+  if (quant == MDC_QUANT_INT8) launch_block_quant<T, R, Wt, MDC_QUANT_INT8>(a, s);
+  else if (quant == MDC_QUANT_FP8) launch_block_quant<T, R, Wt, MDC_QUANT_FP8>(a, s);
+  else launch_block_quant<T, R, Wt, MDC_QUANT_NONE>(a, s);
+}
+
+template <typename T>
+void launch_block_typed(const BlockArgs& a, const mdc_block_norm_params& p, hipStream_t s) {
+  const bool r32 = p.residual_dtype == MDC_DTYPE_FP32, w32 = p.weight_dtype == MDC_DTYPE_FP32;
+  if (r32 && w32) launch_block<T, float, float>(a, p.quant, s);
+  else if (r32) launch_block<T, float, T>(a, p.quant, s);
+  else if (w32) launch_block<T, T, float>(a, p.quant, s);
+  else launch_block<T, T, T>(a, p.quant, s);
+}
+
+bool finite(float v) { return v - v == 0.f; }
+
+}  // namespace
+
+extern "C" {
+
+mdc_status mdc_block_rms_norm(const mdc_block_norm_params* params, const void* x, const void* post_weight,
+                              const void* gate, const void* residual, const void* weight, void* residual_out, void* y,
+                              void* q, float* q_scale, void* stream) {
+  if (params == nullptr) return MDC_ERR_NULLPTR;
+  const mdc_block_norm_params& p = *params;
+  if (p.dtype != MDC_DTYPE_BF16 && p.dtype != MDC_DTYPE_FP16) return MDC_ERR_INVALID;
+  for (int32_t t : {p.residual_dtype, p.weight_dtype, p.gate_dtype})
+    if (t != p.dtype && t != MDC_DTYPE_FP32) return MDC_ERR_INVALID;
+  if (p.quant < MDC_QUANT_NONE || p.quant > MDC_QUANT_FP8) return MDC_ERR_INVALID;
+  if (p.gate_act < MDC_ACT_NONE || p.gate_act > MDC_ACT_TANH) return MDC_ERR_INVALID;
+  if (p.rows < 0 || p.hidden <= 0 || p.hidden % 8 != 0) return MDC_ERR_INVALID;
+  if (p.gate_columns != 1 && p.gate_columns != p.hidden) return MDC_ERR_INVALID;
+  if (p.gate_every < 1) return MDC_ERR_INVALID;
+  if (!(p.eps >= 0.f) || !finite(p.eps) || !(p.post_eps >= 0.f) || !finite(p.post_eps)) return MDC_ERR_INVALID;
+  if (!finite(p.block_scale) || !finite(p.residual_scale)) return MDC_ERR_INVALID;
+  if (p.rows > INT32_MAX || p.hidden > MDC_MAX_NORM_HIDDEN) return MDC_ERR_UNSUPPORTED;
+  if (p.rows == 0) return MDC_OK;
+  if (x == nullptr) return MDC_ERR_NULLPTR;
+  if ((p.quant != MDC_QUANT_NONE) != (q != nullptr) || (q != nullptr) != (q_scale != nullptr)) return MDC_ERR_NULLPTR;
+  if (residual_out == nullptr && y == nullptr && q == nullptr) return MDC_ERR_NULLPTR;
+  if (weight == nullptr && (y != nullptr || q != nullptr)) return MDC_ERR_NULLPTR;
+  const bool wide = gate != nullptr && p.gate_columns != 1;
+  if (!aligned16(x) || !aligned16(post_weight) || !aligned16(residual) || !aligned16(weight) ||
+      !aligned16(residual_out) || !aligned16(y) || !aligned8(q) || !aligned4(q_scale))
+    return MDC_ERR_INVALID;
+  const uintptr_t unit = wide ? 16 : p.gate_dtype == MDC_DTYPE_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(gate) % unit != 0) return MDC_ERR_INVALID;
+  const int nvec = p.hidden / 8;
+  if (y == nullptr && q == nullptr) weight = nullptr;   // (nothing to normalise for)
+  const BlockArgs a{x, post_weight, gate, residual, weight, residual_out, NormOut{y, q, q_scale, nvec}, (int)p.rows, nvec,
+                    (int)(p.gate_every < p.rows ? p.gate_every : p.rows), wide, p.gate_dtype == MDC_DTYPE_FP32, p.gate_act,
+                    p.block_scale, p.residual_scale, p.post_eps, p.eps, 1.0f / (float)p.hidden};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (p.dtype == MDC_DTYPE_BF16) launch_block_typed<Bf16>(a, p, s);
+  else launch_block_typed<_Float16>(a, p, s);
+  return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,734 @@
+// libmdc: a whole layer of experts for a few tokens, for AMD Instinct MI355X
+// (gfx950): mdc_moe (int8 experts), mdc_moe_fp8 (e4m3 experts).
+
+#include "mdc_group.h"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// x_out[t] = sum over the token's routes of scale * (W2 q(silu(W1g q(x)) * W1u
+// q(x)) + shared), all experts of all tokens in two launches:
+//
+//   k_moe_up    h = q(x) W1^T for every expert that has a token, and SwiGLU: g,
+//               fp32, into the workspace
+//   k_moe_down  q(g) W2^T times the routes' scales, summed over the experts
+//
+// With at most 32 tokens an expert's rows fill one or two blocks of the matrix
+// instruction, and what takes the time is to bring the weights of the experts in
+// use, once.  Both kernels run one workgroup of eight wavefronts per CU, each
+// wavefront streaming weights global -> LDS directly through a ring of its own
+// (eight rows x 128 bytes per instruction, non-temporal: they are read once).
+//
+// k_moe_up: a tile is 8 gate columns and the 8 up columns that go with them, one
+// 16-row block of the matrix instruction; the wavefronts split k.  Every token is
+// an operand row for every expert, so the tokens stay in registers, quantised
+// there once, for the whole kernel; rows of tokens that an expert does not have
+// are computed and dropped.  The sums of the eight wavefronts are joined through
+// LDS, by another wavefront for each tile.
+//
+// k_moe_down: a workgroup has the columns [cw b, cw (b + 1)) of the output and
+// walks all experts: no sum leaves the workgroup.  A unit of work is a k-block of
+// 128 of one expert; wavefront w takes units w, w + 8, ... and keeps sums for all
+// tokens in registers, scaled by its rows' route scales as they are added.  The
+// rows of g are quantised into LDS by all threads, as many units at a time as it
+// holds cells (a cell is 128 values of one row).
+//
+// Sums are fp32 (int32 inside an int8 product), in an order that depends on the
+// routes only.
+// ---------------------------------------------------------------------------
+constexpr int kMoeThreads = 512;
+constexpr int kMoeWaves = kMoeThreads / 64;
+constexpr int kMoeTokens = MDC_MAX_MOE_TOKENS;
+constexpr int kMoeRoutes = kMoeTokens * MDC_MAX_TOPK;
+constexpr int kMoeNt = 2;             // cache policy of the weights' loads: non-temporal
+constexpr int kUpRing = 12288;        // bytes of a wavefront's ring
+constexpr int kDownRing = 8192;
+constexpr int kUpRun = 8;             // most k-blocks of a wavefront
+constexpr int kCells = 256;           // rows x k-blocks of g in LDS at a time
+static_assert(kMoeRoutes <= kMoeThreads, "a thread for each route");
+
+struct Moe {
+  const void* x;             // [T][H] bf16
+  const int32_t* ids;        // [T][K]
+  const float* scales;       // [T][K]
+  const uint8_t* mask;       // [T] or [T][K], or NULL
+  const uint8_t* w1;         // [L][N][H]
+  const float* w1_scale;     // int8: [L][N]; fp8: [L][N / 128][H / 128]
+  const uint8_t* w2;         // [L][H][N / 2]
+  const float* w2_scale;     // int8: [L][H]; fp8: [L][H / 128][N / 256]
+  const uint16_t* shared;    // [T][H] bf16, or NULL
+  const uint16_t* ori;       // [T][H] bf16, or NULL
+  uint16_t* out;             // [T][H] bf16
+  float* g;                  // [rows N / 256][128]: cells, by expert, k-block and row
+  float* g_max;              // int8: [rows][N / 16] largest |g| of each tile
+  mdc_device_status* status;
+  int T, K, H, N, L;
+  int first;                 // id of local expert 0
+  int E, EZ, all;            // ids: routed, routed and zero, all of them
+  int per_route;
+  int cw;                    // output columns of a workgroup
+};
+
+// ---------------------------------------------------------------------------
+// The routes as both kernels see them: the experts in use, in the order of their
+// first routes, with the tokens that they have.
+// ---------------------------------------------------------------------------
+struct MoeTable {
+  uint16_t expert[kMoeRoutes];
+  uint32_t tokens[kMoeRoutes];      // bit t: token t has a route to it
+  int base[kMoeRoutes + 1];         // rows of the experts before it
+  float weight[kMoeRoutes];         // of each row: the sum of its routes' scales
+  float copy[kMoeTokens];           // sum of the scales of the token's copy experts
+  float present[kMoeTokens];        // and of all its routes
+  int64_t wave_total[kMoeWaves];
+  int experts, dropped;
+};
+
+// tmp: L ints of LDS, free again afterwards.
+__device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
+  const int i = threadIdx.x, R = a.T * a.K;
+  const int token = i / a.K;
+  int id = -1;
+  float scale = 0.f;
+  bool live = false;
+  if (i < R) {
+    id = a.ids[i];
+    scale = a.scales[i];
+    live = a.mask == nullptr || a.mask[a.per_route ? i : token] != 0;
+  }
+  const bool present = live && id >= 0 && id < a.all;
+  const int e = id - a.first;
+  const bool mine = present && id < a.E && e >= 0 && e < a.L;
+  for (int k = i; k < a.L; k += kMoeThreads) tmp[k] = INT32_MAX;
+  if (i < kMoeTokens) t.copy[i] = t.present[i] = 0.f;
+  if (i == 0) t.dropped = 0;
+  t.tokens[i] = 0;
+  __syncthreads();
+  if (mine) atomicMin(&tmp[e], i);
+  if (live && i < R && !present) atomicAdd(&t.dropped, 1);
+  __syncthreads();
+  // place of the expert of each first route
+  const bool first = mine && tmp[e] == i;
+  int64_t n;
+  const int place = (int)block_scan<kMoeThreads>(first ? 1 : 0, t.wave_total, n) - 1;
+  if (first) {
+    t.expert[place] = (uint16_t)e;
+    tmp[e] = -1 - place;
+  }
+  if (i == 0) t.experts = (int)n;
+  __syncthreads();
+  const int j = mine ? -1 - tmp[e] : 0;
+  if (mine) atomicOr(&t.tokens[j], 1u << token);
+  __syncthreads();
+  int64_t rows;
+  const int end = (int)block_scan<kMoeThreads>(__popc(t.tokens[i]), t.wave_total, rows);
+  t.base[i + 1] = end;
+  if (i == 0) t.base[0] = 0;
+  __syncthreads();
+  // sums over a token's routes, in order: by the first route of an expert, and by the first of the token
+  if (i < R) {
+    float sum = 0.f, copy = 0.f, all = 0.f;
+    bool lead = mine;
+    const int r0 = token * a.K;
+    for (int r = r0; r < r0 + a.K; ++r) {
+      const int other = a.ids[r];
+      const bool on = (a.mask == nullptr || a.mask[a.per_route ? r : token] != 0) && other >= 0 && other < a.all;
+      const float s = on ? a.scales[r] : 0.f;
+      if (on && other == id) {
+        sum += s;
+        lead = lead && r >= i;
+      }
+      if (on && other >= a.EZ) copy += s;
+      if (on) all += s;
+    }
+    if (lead) t.weight[t.base[j] + __popc(t.tokens[j] & ((1u << token) - 1))] = sum;
+    if (i == r0) {
+      t.copy[token] = copy;
+      t.present[token] = all;
+    }
+  }
+  __syncthreads();
+}
+
+// ---- one product of 16 weight rows x 128 k x 16 tokens ----
+template <bool INT8>
+struct MoeAcc {
+  typedef v4f type;
+};
+template <>
+struct MoeAcc<true> {
+  typedef v4i type;
+};
+__device__ __forceinline__ v4f moe_mfma_fp8(v8i w, v8i t) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, t, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ v4i moe_mfma_int8(v8i w, v8i t, v4i c) {
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v4i{w[0], w[1], w[2], w[3]}, v4i{t[0], t[1], t[2], t[3]}, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(v4i{w[4], w[5], w[6], w[7]}, v4i{t[4], t[5], t[6], t[7]}, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t int8_codes4(float a, float b, float c, float d, float inv) {
+  auto code = [&](float v) { return (uint32_t)(uint8_t)(int8_t)(int)fminf(fmaxf(rintf(v * inv), -127.f), 127.f); };
+  return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
+}
+__device__ __forceinline__ float int8_inverse(float amax) {
+  const float inv = amax > 0.f ? 127.0f / amax : 0.f;
+  return inv > 3.402823466e38f ? 3.402823466e38f : inv;
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {   // over the four lanes 16 apart
+  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  return max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+}
+
+// Loads of eight weight rows x 128 bytes into LDS: lane l takes the chunk that
+// belongs in slot l % 8 of row l / 8; `odd`: rows 8 .. 15 of the block.
+__device__ __forceinline__ unsigned moe_chunk(int lane, int odd) {
+  return (unsigned)((lane & 7) ^ ((4 * odd + (lane >> 4)) & 7)) << 4;
+}
+
+// ---------------------------------------------------------------------------
+template <bool INT8, int TB>
+__global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
+  typedef typename MoeAcc<INT8>::type Acc;
+  __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kUpRing];
+  __shared__ __attribute__((aligned(16))) v4f red[2][kMoeWaves * TB * 64];
+  __shared__ MoeTable tab;
+  __shared__ float row_scale[kMoeTokens];   // int8: amax / 127 of the tokens
+  __shared__ float row_inv[kMoeTokens];
+  static_assert(sizeof(ring_mem) >= MDC_MAX_LOCAL_EXPERTS * sizeof(int), "scratch of the table");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int H = a.H, N = a.N, nk = H / kFp8Block;
+  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
+  const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
+  const int tiles_per = N / 16;
+  const int64_t T = (int64_t)n_exp * tiles_per;
+  const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
+  if (t0 == t1) return;
+
+  // ---- weights ----
+  const int kb0 = wave * nk / kMoeWaves, steps = (wave + 1) * nk / kMoeWaves - kb0;
+  constexpr int kSlot = 2048, kSlots = kUpRing / kSlot;
+  const unsigned ring = lds_at(ring_mem) + wave * kUpRing;
+  auto weights = [&](int j) {
+    const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w1 + (int64_t)e * N * H), (short)0, N * H, 0x00020000);
+  };
+  struct {
+    int j, c, step, left;   // expert's place, tile of it, step, tiles to come
+  } f = {t0 / tiles_per, t0 % tiles_per, 0, steps > 0 ? t1 - t0 : 0};
+  __amdgpu_buffer_rsrc_t rw = weights(f.j);
+  unsigned slot = 0;
+  auto fetch = [&]() {
+    const unsigned k0 = (unsigned)(kb0 + f.step) * kFp8Block;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned row = (unsigned)(8 * f.c + (lane >> 3) + h * (N / 2));
+      const unsigned at = f.left > 0 ? row * (unsigned)H + k0 + moe_chunk(lane, h) : kPastEnd;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, at, 0, 0, kMoeNt);
+    }
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    if (++f.step >= steps) {
+      f.step = 0;
+      --f.left;
+      if (++f.c == tiles_per) {
+        f.c = 0;
+        if (f.left > 0) rw = weights(++f.j);
+      }
+    }
+  };
+
+  // ---- the tokens, quantised, in the matrix instruction's layout ----
+  const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  if (INT8) {
+    for (int t = wave; t < a.T; t += kMoeWaves) {
+      uint32_t m = 0;
+      const v4u* row = reinterpret_cast<const v4u*>(x + (int64_t)t * H);
+      for (int i = lane; i < H / 8; i += 64) {
+        const v4u v = row[i];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, max(abs_bits(bf16_lo(v[w])), abs_bits(bf16_hi(v[w]))));
+      }
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+      if (lane == 0) {
+        row_scale[t] = __uint_as_float(m) / 127.0f;
+        row_inv[t] = int8_inverse(__uint_as_float(m));
+      }
+    }
+    __syncthreads();
+  }
+  v8i tok[kUpRun][TB];
+  float sa[kUpRun][TB];
+#pragma unroll
+  for (int d = 0; d < kUpRun; ++d)
+#pragma unroll
+    for (int m = 0; m < TB; ++m) {
+      const int t = 16 * m + r16;
+      v4u v[4] = {v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}};
+      if (d < steps && t < a.T) {
+        const v4u* p = reinterpret_cast<const v4u*>(x + (int64_t)t * H + (kb0 + d) * kFp8Block + 16 * quad);
+        v[0] = p[0];
+        v[1] = p[1];
+        v[2] = p[8];   // 64 elements on
+        v[3] = p[9];
+      }
+      if (INT8) {
+        const float inv = t < a.T ? row_inv[t] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            tok[d][m][2 * i + w] = (int)int8_codes4(bf16_lo(v[i][2 * w]), bf16_hi(v[i][2 * w]), bf16_lo(v[i][2 * w + 1]),
+                                                    bf16_hi(v[i][2 * w + 1]), inv);
+        sa[d][m] = 0.f;
+      } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top = max(top, max(abs_bits(bf16_lo(v[i][w])), abs_bits(bf16_hi(v[i][w]))));
+        const Fp8Scaler s(quad_max(top));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            tok[d][m][2 * i + w] = (int)s.codes4(bf16_lo(v[i][2 * w]), bf16_hi(v[i][2 * w]), bf16_lo(v[i][2 * w + 1]),
+                                                 bf16_hi(v[i][2 * w + 1]));
+        sa[d][m] = s.scale;
+      }
+    }
+  __syncthreads();   // the table's scratch is free
+#pragma unroll
+  for (int d = 0; d < kSlots; ++d) fetch();
+
+  const int key = (r16 >> 1) & 7;
+  const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
+  unsigned read = 0;
+  int j = t0 / tiles_per, c = t0 % tiles_per;
+  for (int t = t0; t < t1; ++t) {
+    const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+    float sw[2][kUpRun];   // fp8: scales of the gate and the up rows
+    if (!INT8) {
+      const scalar_f* p = (const scalar_f*)(a.w1_scale + ((int64_t)e * (N / kFp8Block) + c / 16) * nk);
+#pragma unroll
+      for (int d = 0; d < kUpRun; ++d) {
+        const int b = min(kb0 + d, nk - 1);
+        sw[0][d] = p[b];
+        sw[1][d] = p[(int64_t)(N / 256) * nk + b];
+      }
+    }
+    Acc acc[TB];
+#pragma unroll
+    for (int m = 0; m < TB; ++m) acc[m] = Acc{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < kUpRun; ++d) {
+      if (d < steps) {
+        __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2));   // at most the loads of the other slots are out
+        const v8i w = lds_get2(f0 + read, f1 + read);
+        read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
+        fetch();
+        if constexpr (INT8) {
+#pragma unroll
+          for (int m = 0; m < TB; ++m) acc[m] = moe_mfma_int8(w, tok[d][m], acc[m]);
+        } else {
+          const float s = quad < 2 ? sw[0][d] : sw[1][d];
+#pragma unroll
+          for (int m = 0; m < TB; ++m) {
+            const v4f p = moe_mfma_fp8(w, tok[d][m]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(p[r], sa[d][m] * s, acc[m][r]);
+          }
+        }
+      }
+    }
+    const unsigned buf = lds_at(red[t & 1]);
+#pragma unroll
+    for (int m = 0; m < TB; ++m) lds_put(buf + ((wave * TB + m) * 64 + lane) * 16, __builtin_bit_cast(v4f, acc[m]));
+    lds_barrier();
+    // lane (m, half, r16) of one wavefront: token 16 m + r16, four of the tile's columns
+    if (wave == (t & (kMoeWaves - 1)) && (TB == 2 || lane < 32)) {
+      const int m = lane >> 5, half = quad & 1, token = 16 * m + r16;
+      const uint32_t tokens = tab.tokens[j];
+      Acc gate = Acc{0, 0, 0, 0}, up = Acc{0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kMoeWaves; ++w) {
+        const unsigned at = buf + ((w * TB + m) * 64 + half * 16 + r16) * 16;
+        const v8i p = lds_get2(at, at + 32 * 16);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (INT8) {
+            gate[r] += p[r];
+            up[r] += p[4 + r];
+          } else {
+            gate[r] += __int_as_float(p[r]);
+            up[r] += __int_as_float(p[4 + r]);
+          }
+        }
+      }
+      if ((tokens >> token) & 1) {
+        const int col = 8 * c + 4 * half;
+        v4f v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float hg = (float)gate[r], hu = (float)up[r];
+          if (INT8) {
+            const float* ws = a.w1_scale + (int64_t)e * N + col + r;
+            hg = hg * row_scale[token] * ws[0];
+            hu = hu * row_scale[token] * ws[N / 2];
+          }
+          v[r] = gmm_silu(hg) * hu;
+        }
+        const int rows = __popc(tokens), row = __popc(tokens & ((1u << token) - 1));
+        const int64_t cell = (int64_t)tab.base[j] * (N / 256) + col / kFp8Block * rows + row;
+        *reinterpret_cast<v4f*>(a.g + cell * kFp8Block + col % kFp8Block) = v;
+        if (INT8) {
+          uint32_t top = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+          top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));   // (the other half of the same token)
+          if (half == 0) a.g_max[(int64_t)(tab.base[j] + row) * (N / 16) + c] = __uint_as_float(top);
+        }
+      }
+    }
+    if (++c == tiles_per) {
+      c = 0;
+      ++j;
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
+}
+
+// ---------------------------------------------------------------------------
+template <bool INT8, int TB, int NB>
+__global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
+  __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kDownRing];
+  __shared__ __attribute__((aligned(16))) uint8_t cells[(kCells + 1) * kFp8Block];   // the last one: zeros
+  __shared__ float cell_scale[INT8 ? 1 : kCells + 1];
+  __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
+  __shared__ MoeTable tab;
+  static_assert(sizeof(ring_mem) >= kMoeWaves * 4 * 64 * 16, "the wavefronts' sums");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int H = a.H, K2 = a.N / 2, nk = K2 / kFp8Block;
+  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
+  const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
+  const int units = n_exp * nk;
+  const int c0 = blockIdx.x * a.cw, cols = min(a.cw, H - c0);
+
+  // ---- weights: units wave, wave + 8, ... ----
+  constexpr int kSlot = NB * 2048, kSlots = kDownRing / kSlot;
+  const unsigned ring = lds_at(ring_mem) + wave * kDownRing;
+  int fu = wave, fj = -1;
+  __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w2), (short)0, 0, 0x00020000);
+  unsigned slot = 0;
+  auto fetch = [&]() {
+    const bool in = fu < units;
+    const int j = in ? fu / nk : 0;
+    if (in && j != fj) {
+      const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+      rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w2 + ((int64_t)e * H + c0) * K2), (short)0, cols * K2,
+                                             0x00020000);
+      fj = j;
+    }
+    const unsigned k0 = (unsigned)(fu - j * nk) * kFp8Block;
+#pragma unroll
+    for (int h = 0; h < 2 * NB; ++h) {
+      const unsigned at = in ? (unsigned)(8 * h + (lane >> 3)) * (unsigned)K2 + k0 + moe_chunk(lane, h & 1) : kPastEnd;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, at, 0, 0, kMoeNt);
+    }
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    fu += kMoeWaves;
+  };
+  if (INT8) {
+    // scales of the rows, from the largest value of each of their tiles
+    const int rows = tab.base[kMoeRoutes], per = a.N / 16;
+    for (int r = wave; r < rows; r += kMoeWaves) {
+      uint32_t m = 0;
+      for (int i = lane; i < per; i += 64) m = max(m, __float_as_uint(a.g_max[(int64_t)r * per + i]));
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+      if (lane == 0) {
+        row_scale[r] = __uint_as_float(m) / 127.0f;
+        row_inv[r] = int8_inverse(__uint_as_float(m));
+      }
+    }
+  }
+  if (threadIdx.x < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[threadIdx.x] = 0;
+  if (!INT8 && threadIdx.x == 0) cell_scale[kCells] = 0.f;
+  __syncthreads();   // the table's scratch is free
+#pragma unroll
+  for (int d = 0; d < kSlots; ++d) fetch();
+
+  v4f acc[TB][NB];
+#pragma unroll
+  for (int m = 0; m < TB; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int key = (r16 >> 1) & 7;
+  const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
+  const unsigned cell0 = lds_at(cells);
+  unsigned read = 0;
+  int u0 = 0, first = 0, mine = wave;   // group: first unit, its first cell; this wavefront's next unit
+  while (u0 < units) {
+    // the units whose rows fit
+    int u1 = u0, used = 0;
+    while (u1 < units) {
+      const int j = u1 / nk, rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1] - tab.base[j]);
+      const int take = min((j + 1) * nk - u1, (kCells - used) / rows);
+      if (take == 0) break;
+      u1 += take;
+      used += take * rows;
+    }
+    if (u0 != 0) lds_barrier();   // the cells have been read
+    for (int i = threadIdx.x; i < used * 16; i += kMoeThreads) {
+      const int cell = i >> 4, u = i & 15;
+      const v4f* src = reinterpret_cast<const v4f*>(a.g + ((int64_t)first + cell) * kFp8Block) + 2 * u;
+      const v4f p = src[0], q = src[1];
+      uint2 code;
+      if (INT8) {
+        // the row: cells run by k-block and row inside an expert
+        const int at = first + cell;
+        int lo = 0, hi = n_exp;   // base[lo] nk <= at < base[hi] nk
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (tab.base[mid] * nk <= at) lo = mid;
+          else hi = mid;
+        }
+        const int row = tab.base[lo] + (at - tab.base[lo] * nk) % (tab.base[lo + 1] - tab.base[lo]);
+        const float inv = row_inv[row];
+        code = uint2{int8_codes4(p[0], p[1], p[2], p[3], inv), int8_codes4(q[0], q[1], q[2], q[3], inv)};
+      } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = max(top, max(abs_bits(p[r]), abs_bits(q[r])));
+        const Fp8Scaler s(row16_max(top));
+        code = uint2{s.codes4(p[0], p[1], p[2], p[3]), s.codes4(q[0], q[1], q[2], q[3])};
+        if (u == 0) cell_scale[cell] = s.scale;
+      }
+      *reinterpret_cast<uint2*>(cells + cell * kFp8Block + (((u >> 1) ^ ((cell >> 1) & 7)) << 4) + (u & 1) * 8) = code;
+    }
+    lds_barrier();
+    for (; mine < u1; mine += kMoeWaves) {
+      const int j = mine / nk, kb = mine - j * nk;
+      const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+      const int base = __builtin_amdgcn_readfirstlane(tab.base[j]), rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1]) - base;
+      const uint32_t tokens = __builtin_amdgcn_readfirstlane((int)tab.tokens[j]);
+      const int at = base * nk + kb * rows - first;   // the unit's first cell
+      v8i tok[TB];
+      float s[TB];
+      bool has[TB];   // (the others' sums stay: what an expert holds may be infinite or NaN)
+#pragma unroll
+      for (int m = 0; m < TB; ++m) {
+        const int token = 16 * m + r16, row = __popc(tokens & ((1u << token) - 1));
+        has[m] = (tokens >> token) & 1;
+        const int cell = has[m] ? at + row : kCells, k = (cell >> 1) & 7;
+        const unsigned p = cell0 + cell * kFp8Block;
+        tok[m] = lds_get2(p + ((quad ^ k) << 4), p + (((4 + quad) ^ k) << 4));
+        s[m] = has[m] ? (INT8 ? row_scale[INT8 ? base + row : 0] : cell_scale[INT8 ? 0 : cell]) * tab.weight[base + row] : 0.f;
+      }
+      float sw[NB][2];   // fp8: of the first and of the last column
+      v4f sc[NB];        // int8: of the lane's four columns
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int col = c0 + 16 * n;
+        if constexpr (INT8) {
+          const float* p = a.w2_scale + (int64_t)e * H;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sc[n][r] = p[min(col + 4 * quad + r, H - 1)];
+        } else {
+          const scalar_f* p = (const scalar_f*)(a.w2_scale + (int64_t)e * (H / kFp8Block) * nk + kb);
+          sw[n][0] = p[min(col, H - 1) / kFp8Block * nk];
+          sw[n][1] = p[min(col + 15, H - 1) / kFp8Block * nk];
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2 * NB));
+      v8i w[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) w[n] = lds_get2(f0 + read + n * 2048, f1 + read + n * 2048);
+      read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
+      fetch();
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float f = 0.f;
+        if (!INT8) f = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block ? sw[n][0] : sw[n][1];
+#pragma unroll
+        for (int m = 0; m < TB; ++m) {
+          if constexpr (INT8) {
+            const v4i p = moe_mfma_int8(w[n], tok[m], v4i{0, 0, 0, 0});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][n][r] = has[m] ? __builtin_fmaf((float)p[r], s[m] * sc[n][r], acc[m][n][r]) : acc[m][n][r];
+          } else {
+            const v4f p = moe_mfma_fp8(w[n], tok[m]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][n][r] = has[m] ? __builtin_fmaf(p[r], s[m] * f, acc[m][n][r]) : acc[m][n][r];
+          }
+        }
+      }
+    }
+    first += used;
+    u0 = u1;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
+  __syncthreads();
+
+  // ---- the wavefronts' sums, and the terms that are no expert's ----
+  const unsigned sums = lds_at(ring_mem);
+#pragma unroll
+  for (int m = 0; m < TB; ++m)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) lds_put(sums + ((wave * TB + m) * NB + n) * 1024 + lane * 16, acc[m][n]);
+  __syncthreads();
+  const float* part = reinterpret_cast<const float*>(ring_mem);
+  for (int i = threadIdx.x; i < 16 * NB * a.T; i += kMoeThreads) {
+    const int token = i / (16 * NB), cc = i - token * 16 * NB, col = c0 + cc;
+    if (cc >= cols) continue;
+    const int m = token >> 4, n = cc >> 4;
+    const int at = ((cc & 15) >> 2) * 64 + (token & 15) * 4 + (cc & 3);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMoeWaves; ++w) v += part[((w * TB + m) * NB + n) * 256 + at];
+    const int64_t o = (int64_t)token * H + col;
+    if (a.ori != nullptr) v = __builtin_fmaf(tab.copy[token], __uint_as_float((uint32_t)a.ori[o] << 16), v);
+    if (a.shared != nullptr) v = __builtin_fmaf(tab.present[token], __uint_as_float((uint32_t)a.shared[o] << 16), v);
+    a.out[o] = (uint16_t)bf16_rne(v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Workspace: [status block][ids][scales][g][g_max].
+struct MoePlan {
+  size_t off_ids, off_scales, off_g, off_max, bytes;
+};
+
+MoePlan make_moe_plan(const mdc_shape* sh, int inter_n) {
+  const size_t R = (size_t)sh->bs * sh->topk, N = (size_t)inter_n;
+  MoePlan p;
+  p.off_ids = MDC_STATUS_BYTES;
+  p.off_scales = p.off_ids + round_up(R * 4, 256);
+  p.off_g = p.off_scales + round_up(R * 4, 256);
+  p.off_max = p.off_g + round_up(R * (N / 2) * 4, 256);
+  p.bytes = p.off_max + round_up(R * (N / 16) * 4, 256);
+  return p;
+}
+
+mdc_status check_moe(const mdc_shape* sh, int inter_n) {
+  const mdc_status st = check_shape(sh);
+  if (st != MDC_OK) return st;
+  if (inter_n <= 0) return MDC_ERR_INVALID;
+  if (inter_n % 256 != 0 || sh->hidden % kFp8Block != 0) return MDC_ERR_UNSUPPORTED;
+  if (sh->bs > MDC_MAX_MOE_TOKENS || sh->hidden > kMoeWaves * kUpRun * kFp8Block) return MDC_ERR_UNSUPPORTED;
+  if ((int64_t)inter_n * sh->hidden > INT32_MAX) return MDC_ERR_UNSUPPORTED;
+  return MDC_OK;
+}
+
+template <bool INT8, int TB>
+void launch_moe(const Moe& a, unsigned cus, hipStream_t s) {
+  hipLaunchKernelGGL((k_moe_up<INT8, TB>), dim3(cus), dim3(kMoeThreads), 0, s, a);
+  const dim3 grid((unsigned)((a.H + a.cw - 1) / a.cw));
+  if (a.cw <= 16) hipLaunchKernelGGL((k_moe_down<INT8, TB, 1>), grid, dim3(kMoeThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_moe_down<INT8, TB, 2>), grid, dim3(kMoeThreads), 0, s, a);
+}
+
+template <bool INT8>
+mdc_status moe_impl(const mdc_shape* shape, const mdc_gate_params* params, int32_t inter_n, const void* x,
+                    const void* logits, const float* bias, int32_t* expert_ids, float* expert_scales,
+                    const uint8_t* x_active_mask, const void* w1, const float* w1_scale, const void* w2,
+                    const float* w2_scale, const void* shared_expert_x, const void* ori_x, void* x_out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const mdc_status st = check_moe(shape, inter_n);
+  if (st != MDC_OK) return st;
+  if ((params != nullptr) != (logits != nullptr)) return MDC_ERR_NULLPTR;
+  if ((expert_ids != nullptr) != (expert_scales != nullptr)) return MDC_ERR_NULLPTR;
+  mdc_shape one = *shape;   // the tokens, once
+  one.world = 1;
+  one.rank = 0;
+  one.mask_per_route = 0;
+  if (params != nullptr) {   // its checks: with no tokens nothing is enqueued
+    mdc_shape none = one;
+    none.bs = 0;
+    const mdc_status gate = mdc_gate(&none, params, logits, bias, expert_ids, expert_scales, stream);
+    if (gate != MDC_OK) return gate;
+  }
+  if (shape->bs == 0) return MDC_OK;
+  const MoePlan p = make_moe_plan(shape, inter_n);
+  if (x == nullptr || w1 == nullptr || w1_scale == nullptr || w2 == nullptr || w2_scale == nullptr || x_out == nullptr ||
+      workspace == nullptr || (params == nullptr && expert_ids == nullptr) ||
+      (ori_x == nullptr && shape->copy_experts > 0 && shape->world == 1))
+    return MDC_ERR_NULLPTR;
+  if (!aligned16(x) || !aligned16(w1) || !aligned4(w1_scale) || !aligned16(w2) || !aligned4(w2_scale) ||
+      !aligned16(shared_expert_x) || !aligned16(ori_x) || !aligned16(x_out) || !aligned16(workspace) ||
+      !aligned4(expert_ids) || !aligned4(expert_scales))
+    return MDC_ERR_INVALID;
+  if (workspace_bytes < p.bytes) return MDC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  if (expert_ids == nullptr) {
+    expert_ids = reinterpret_cast<int32_t*>(ws + p.off_ids);
+    expert_scales = reinterpret_cast<float*>(ws + p.off_scales);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (params != nullptr) {
+    const mdc_status gate = mdc_gate(&one, params, logits, bias, expert_ids, expert_scales, stream);
+    if (gate != MDC_OK) return gate;
+  }
+  (void)hipGetLastError();
+  const unsigned cus = device_cus();
+  const int L = shape->num_experts / shape->world;
+  const int cw = min(32, max(4, (int)round_up((shape->hidden + cus - 1) / cus, 4)));
+  const Moe a{x, expert_ids, expert_scales, x_active_mask, static_cast<const uint8_t*>(w1), w1_scale,
+              static_cast<const uint8_t*>(w2), w2_scale, static_cast<const uint16_t*>(shared_expert_x),
+              static_cast<const uint16_t*>(ori_x), static_cast<uint16_t*>(x_out), reinterpret_cast<float*>(ws + p.off_g),
+              reinterpret_cast<float*>(ws + p.off_max), reinterpret_cast<mdc_device_status*>(ws), shape->bs, shape->topk,
+              shape->hidden, inter_n, L, shape->rank * L, shape->num_experts,
+              shape->num_experts + shape->zero_experts, shape->num_experts + shape->zero_experts + shape->copy_experts,
+              shape->mask_per_route, cw};
+  if (a.T <= 16) launch_moe<INT8, 1>(a, cus, s);
+  else launch_moe<INT8, 2>(a, cus, s);
+  return launched();
+}
+
+mdc_status moe_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes) {
+  if (bytes == nullptr) return MDC_ERR_NULLPTR;
+  const mdc_status st = check_moe(shape, inter_n);
+  if (st != MDC_OK) return st;
+  *bytes = make_moe_plan(shape, inter_n).bytes;
+  return MDC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mdc_status mdc_moe_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes) {
+  return moe_workspace(shape, inter_n, bytes);
+}
+
+mdc_status mdc_moe_fp8_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes) {
+  return moe_workspace(shape, inter_n, bytes);
+}
+
+mdc_status mdc_moe(const mdc_shape* shape, const mdc_gate_params* params, int32_t inter_n, const void* x,
+                   const void* logits, const float* bias, int32_t* expert_ids, float* expert_scales,
+                   const uint8_t* x_active_mask, const int8_t* w1, const float* w1_scale, const int8_t* w2,
+                   const float* w2_scale, const void* shared_expert_x, const void* ori_x, void* x_out, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  return moe_impl<true>(shape, params, inter_n, x, logits, bias, expert_ids, expert_scales, x_active_mask, w1, w1_scale, w2,
+                        w2_scale, shared_expert_x, ori_x, x_out, workspace, workspace_bytes, stream);
+}
+
+mdc_status mdc_moe_fp8(const mdc_shape* shape, const mdc_gate_params* params, int32_t inter_n, const void* x,
+                       const void* logits, const float* bias, int32_t* expert_ids, float* expert_scales,
+                       const uint8_t* x_active_mask, const void* w1, const float* w1_scale, const void* w2,
+                       const float* w2_scale, const void* shared_expert_x, const void* ori_x, void* x_out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return moe_impl<false>(shape, params, inter_n, x, logits, bias, expert_ids, expert_scales, x_active_mask, w1, w1_scale,
+                         w2, w2_scale, shared_expert_x, ori_x, x_out, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,7 +1,7 @@
 // libmdc: residual addition and RMS norm with 16-bit and 8-bit outputs for
 // AMD Instinct MI355X (gfx950): mdc_add_rms_norm.
 
-#include "mdc_fp8.h"
+#include "mdc_rows.h"
 
 namespace {
 
@@ -33,71 +33,11 @@ struct NormArgs {
   float eps, inv_hidden;
 };
 
-struct Bf16 {
-  uint16_t bits;
-};
-
-// Eight elements from and to memory.
-__device__ __forceinline__ void load8(const Bf16* p, float (&v)[8]) {
-  const v4u w = *reinterpret_cast<const v4u*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef float v8f __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
-  const v8h w = *reinterpret_cast<const v8h*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)w[i];
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const v4f a = reinterpret_cast<const v4f*>(p)[0], b = reinterpret_cast<const v4f*>(p)[1];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
-  }
-}
-__device__ __forceinline__ void store8(Bf16* p, const float (&v)[8]) {
-  v8f f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = v[i];
-  *reinterpret_cast<v8b*>(p) = __builtin_convertvector(f, v8b);   // nearest, ties to even
-}
-__device__ __forceinline__ void store8(_Float16* p, const float (&v)[8]) {
-  v8h w;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = (_Float16)v[i];
-  *reinterpret_cast<v8h*>(p) = w;
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<v4f*>(p)[0] = v4f{v[0], v[1], v[2], v[3]};
-  reinterpret_cast<v4f*>(p)[1] = v4f{v[4], v[5], v[6], v[7]};
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-  return v;
-}
-
-constexpr int kNormThreads = 1024;   // most threads of a workgroup
-
 template <typename T, typename R, typename Wt, int QUANT, int VPT>
 __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
   __shared__ float part[kNormThreads / 64];
   __shared__ uint32_t part_max[kNormThreads / 64];
-  const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t row = grid_block();
   if (row >= a.rows) return;
   const int64_t at = row * a.nvec;   // first vector of the row
@@ -121,86 +61,12 @@ __global__ __launch_bounds__(kNormThreads) void k_add_rms_norm(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[u][j], h[u][j], sum);
   }
-  sum = wave_sum(sum);
-  if ((tid & 63) == 0) part[tid >> 6] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < waves; ++w) sum += part[w];
-  const float inv = 1.0f / sqrtf(sum * a.inv_hidden + a.eps);
-  uint32_t amax = 0;
-#pragma unroll
-  for (int u = 0; u < VPT; ++u) {
-    const int i = tid + u * threads;
-    float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // h * weight, v before the row's factor
-    if (i < a.nvec) {
-      if (a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
-      float w[8];
-      load8(static_cast<const Wt*>(a.weight) + i * 8, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (QUANT == MDC_QUANT_FP8) t[j] = h[u][j] * w[j];
-        h[u][j] = h[u][j] * inv * w[j];   // (h times a large or tiny weight may leave fp32)
-      }
-      if (a.y != nullptr) store8(static_cast<T*>(a.y) + (at + i) * 8, h[u]);
-    }
-    uint32_t m = 0;
-    if (QUANT != MDC_QUANT_NONE)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(QUANT == MDC_QUANT_FP8 ? t[j] : h[u][j]));
-    if (QUANT == MDC_QUANT_FP8) {
-      // The row's factor is in v and in amax alike, so the codes are those of
-      // t, a rounding nearer (often all of 16-bit values' product); of v where
-      // t or v leaves the ordinary range (for all 16 lanes of a run or none).
-      m = row16_max(m);
-      const float top = __uint_as_float(m) * inv;
-      const bool plain = __uint_as_float(m) >= 0x1p-100f && top >= kFp8AmaxMin && top < __builtin_inff();
-      if (!plain) {
-        m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          t[j] = h[u][j];
-          m = max(m, abs_bits(t[j]));
-        }
-        m = row16_max(m);
-      }
-      Fp8Scaler s(m);
-      if (plain) s.scale = top / kFp8Max;
-      if (i < a.nvec) {
-        reinterpret_cast<uint2*>(a.q)[at + i] = uint2{s.codes4(t[0], t[1], t[2], t[3]),
-                                                      s.codes4(t[4], t[5], t[6], t[7])};
-        if ((i & 15) == 0) a.q_scale[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s.scale;
-      }
-    }
-    amax = max(amax, m);
-  }
-  if (QUANT == MDC_QUANT_INT8) {
-    amax = wave_max(amax);
-    if ((tid & 63) == 0) part_max[tid >> 6] = amax;
-    __syncthreads();
-    amax = 0;
-    for (int w = 0; w < waves; ++w) amax = max(amax, part_max[w]);
-    const float top = __uint_as_float(amax);
-    float scale = amax != 0 ? 127.0f / top : 0.f;
-    if (scale > 3.402823466e38f) scale = 3.402823466e38f;   // (infinite, it would make NaN of the row's zeros)
-#pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      const int i = tid + u * threads;
-      if (i < a.nvec) {
-        uint32_t w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          w[k] = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = (int)fminf(fmaxf(rintf(h[u][4 * k + j] * scale), -127.f), 127.f);
-            w[k] |= (uint32_t)(uint8_t)(int8_t)c << (8 * j);
-          }
-        }
-        reinterpret_cast<uint2*>(a.q)[at + i] = uint2{w[0], w[1]};
-      }
-    }
-    if (tid == 0) a.q_scale[row] = top / 127.0f;
-  }
+  const float inv = 1.0f / sqrtf(row_sum(sum, part) * a.inv_hidden + a.eps);
+  const NormOut out{a.y, a.q, a.q_scale, a.nvec};
+  norm_outputs<T, QUANT, VPT>(out, row, h, inv, part_max, [&](int u, int i, float (&w)[8]) {
+    if (a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
+    load8(static_cast<const Wt*>(a.weight) + i * 8, w);
+  });
 }
 
 // ---------------------------------------------------------------------------

@@ -722,6 +722,180 @@ mdc_status mdc_ffn_fp8_quant_input(const mdc_shape* shape,
                                    void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * Grouped product in int8 with a scale for each row (token) and each output
+ * channel: what mdc_gmm_fp8 is for e4m3, on the rows that mdc_add_rms_norm's
+ * MDC_QUANT_INT8 and mdc_dispatch_quant make.
+ *
+ * Rows [0, min(sum(expert_token_nums), A)) of a, grouped by expert in order as
+ * the dispatch lays them out, each times its expert's weights:
+ *   y[r][c] = round( (sum over k of a[r][k] * w[e][c][k]) * a_scale[r] *
+ *             w_scale[e][c] ),  c < n
+ * The sum is exact; its conversion and the two products, in this order, are
+ * rounded to fp32 each, the result to y_dtype (nearest, ties to even).
+ *
+ *   a [A][K] int8, a_scale [A] fp32, w [L][n][K] int8, w_scale [L][n] fp32,
+ *   y [A][n] of y_dtype, any mdc_dtype (rows past the total are untouched);
+ *   expert_token_nums [L] int64, or NULL when L == 1: all A rows.  Negative
+ *   counts are read as zero.
+ * a, w and y are 16-byte aligned.  K must be a multiple of 16 and n of 8, both
+ * positive (else MDC_ERR_INVALID); n * K < 2^31, K < 2^17, L <=
+ * MDC_MAX_LOCAL_EXPERTS, A < 2^31 and (A / 32 + L + 1) * ceil(n / 16) <=
+ * 2^31 - 2^16 - 1 (else MDC_ERR_UNSUPPORTED).  No workspace.
+ * ------------------------------------------------------------------------ */
+mdc_status mdc_gmm_int8(int64_t capacity,
+                        int32_t experts,
+                        int32_t n,
+                        int32_t k,
+                        int32_t y_dtype,
+                        const int8_t* a,
+                        const float* a_scale,
+                        const int64_t* expert_token_nums,
+                        const int8_t* w,
+                        const float* w_scale,
+                        void* y,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms before and after a block (attention, experts) with the block's gate
+ * and the residual's scale: mdc_add_rms_norm for layers that also normalise and
+ * weigh what a block gives.  For each row, in fp32:
+ *   u  = x / sqrt(mean(x^2) + post_eps) * post_weight     (post_weight NULL: x)
+ *   h  = residual_scale * residual + block_scale * act(gate) * u
+ *        (residual NULL: no first term; gate NULL: act(gate) = 1)
+ *   residual_out = h rounded to residual_dtype
+ *   v  = h / sqrt(mean(h^2) + eps) * weight                (of the unrounded h)
+ *   y, q, q_scale = v in 16 and in 8 bits, as mdc_add_rms_norm makes them
+ * act is the identity, 1 / (1 + exp(-gate)) or tanh(gate).  Row r takes the gate's
+ * row r / gate_every: gate_every = rows is one row for all (a learned scale for
+ * each channel), 1 a row for each, a sequence's length one for each sequence.
+ * A gate row has H values or (gate_columns 1) a single one.
+ * Squares are summed in fp32: with x or h of about 1e19 and up, or of 1e-19 and
+ * below with an eps of 0, a row's norm leaves its range; so may, without a
+ * post_weight, x times gate and block_scale.
+ *
+ *   x [rows][H] and y of dtype (bf16 or fp16); gate [ceil(rows / gate_every)]
+ *   [gate_columns] of gate_dtype; residual, residual_out of residual_dtype;
+ *   post_weight, weight [H] of weight_dtype (each dtype or fp32); q [rows][H]
+ * residual_out, y and q may each be NULL, not all of them; weight may be NULL if
+ * y and q are.  residual_out may be residual or (of its dtype) x itself, y may be
+ * x itself (each element is read before it is written, by one thread); other
+ * overlaps are not allowed.  H must be a multiple of 8 (INVALID) and at most
+ * MDC_MAX_NORM_HIDDEN (UNSUPPORTED); the rows' tensors and a gate of H columns
+ * are 16-byte aligned, q 8-byte.
+ * ------------------------------------------------------------------------ */
+#define MDC_ACT_NONE 0
+#define MDC_ACT_SIGMOID 1
+#define MDC_ACT_TANH 2
+
+typedef struct {
+    int64_t rows;           /* >= 0, below 2^31 */
+    int64_t gate_every;     /* >= 1: rows that share a row of the gate */
+    int32_t hidden;         /* H */
+    int32_t dtype;          /* MDC_DTYPE_BF16 or MDC_DTYPE_FP16 */
+    int32_t residual_dtype; /* dtype or MDC_DTYPE_FP32 */
+    int32_t weight_dtype;   /* dtype or MDC_DTYPE_FP32 */
+    int32_t gate_dtype;     /* dtype or MDC_DTYPE_FP32 */
+    int32_t gate_columns;   /* H or 1 */
+    int32_t gate_act;       /* MDC_ACT_* */
+    int32_t quant;          /* MDC_QUANT_*; NONE: q and q_scale are NULL */
+    float block_scale;      /* finite */
+    float residual_scale;   /* finite */
+    float post_eps;         /* finite, >= 0 */
+    float eps;              /* finite, >= 0 */
+} mdc_block_norm_params;
+
+mdc_status mdc_block_rms_norm(const mdc_block_norm_params* params,
+                              const void* x,
+                              const void* post_weight,
+                              const void* gate,
+                              const void* residual,
+                              const void* weight,
+                              void* residual_out,
+                              void* y,
+                              void* q,
+                              float* q_scale,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * A whole layer of experts for a few tokens, in decode: gate, experts and
+ * weighted sum of BS <= MDC_MAX_MOE_TOKENS tokens, without the exchange's
+ * buffers.  For each token t:
+ *   expert_ids, expert_scales = mdc_gate of the token's logits (params, bias)
+ *   x_out[t] = bf16_rne( sum over its routes to local experts of s_k * y_k
+ *              + sum over its routes to copy experts of s_k * ori_x[t]
+ *              + (sum over all its present routes of s_k) * shared_expert_x[t] )
+ * as the combine weighs them; a route is present if it is active (x_active_mask)
+ * and its id is in [0, E + Z + C).  y_k is the expert FFN of x[t]:
+ *   mdc_moe      as mdc_ffn, int8 with scales for each row and channel, but g and
+ *                y are not rounded to 16 bits (q2, s2 are of the fp32 g)
+ *   mdc_moe_fp8  as mdc_ffn_fp8, y not rounded either
+ * Sums are fp32, in an order that the routes decide.
+ * The local experts are those of shape->rank, [rank * L, (rank + 1) * L): with
+ * world > 1 the tokens are given on every rank, x_out is the rank's part of the
+ * sum, and ori_x and shared_expert_x are for one of the ranks (else NULL); with
+ * world 1 ori_x is needed if there are copy experts.
+ * params and logits both NULL: the routes are inputs, in expert_ids and
+ * expert_scales; ids may repeat in a token, and those out of range are dropped.
+ *
+ *   x [BS][H] bf16; logits [BS][E + Z + C] of params->dtype; bias [E + Z + C] fp32
+ *   or NULL; expert_ids [BS][K] int32 and expert_scales [BS][K] fp32: written with
+ *   logits (both may be NULL then), else read; x_active_mask [BS], or [BS][K] with
+ *   mask_per_route, or NULL; weights and their scales as mdc_ffn's and
+ *   mdc_ffn_fp8's; shared_expert_x, ori_x [BS][H] bf16 or NULL; x_out [BS][H] bf16
+ * A token with no present route gets a row of zeros.  x_out may be x, ori_x or
+ * shared_expert_x; other overlaps are not allowed.  BS <= MDC_MAX_MOE_TOKENS, H a
+ * multiple of 128 and at most 8192, inter_n = N a multiple of 256, N * H < 2^31
+ * (else MDC_ERR_UNSUPPORTED); with logits the bounds of mdc_gate.  capacity and
+ * flags of shape are checked and otherwise ignored.
+ * The workspace (size from mdc_moe_workspace, mdc_moe_fp8_workspace) holds the
+ * status block (dropped_ids: active routes of these tokens whose id is out of
+ * range), the routes where the caller takes none, and g; two calls may share it if
+ * they do not run at the same time.  With BS == 0 nothing is written.
+ * ------------------------------------------------------------------------ */
+#define MDC_MAX_MOE_TOKENS 32
+
+mdc_status mdc_moe_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes);
+mdc_status mdc_moe_fp8_workspace(const mdc_shape* shape, int32_t inter_n, size_t* bytes);
+
+mdc_status mdc_moe(const mdc_shape* shape,
+                   const mdc_gate_params* params,
+                   int32_t inter_n,
+                   const void* x,
+                   const void* logits,
+                   const float* bias,
+                   int32_t* expert_ids,
+                   float* expert_scales,
+                   const uint8_t* x_active_mask,
+                   const int8_t* w1,
+                   const float* w1_scale,
+                   const int8_t* w2,
+                   const float* w2_scale,
+                   const void* shared_expert_x,
+                   const void* ori_x,
+                   void* x_out,
+                   void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+mdc_status mdc_moe_fp8(const mdc_shape* shape,
+                       const mdc_gate_params* params,
+                       int32_t inter_n,
+                       const void* x,
+                       const void* logits,
+                       const float* bias,
+                       int32_t* expert_ids,
+                       float* expert_scales,
+                       const uint8_t* x_active_mask,
+                       const void* w1,
+                       const float* w1_scale,
+                       const void* w2,
+                       const float* w2_scale,
+                       const void* shared_expert_x,
+                       const void* ori_x,
+                       void* x_out,
+                       void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -115,3 +115,53 @@ def ffn_fp8(q1, w1, w2, counts):
     half = h.shape[1] // 2
     gate_, up = h[:, :half], h[:, half:]
     return grouped(fp8_widen(*fp8_quant(gate_ / (1 + np.exp(-gate_)) * up)), w2, counts)
+
+
+def int8_quant(v: np.ndarray):
+    """[rows][H] -> (codes as numbers, scales [rows]): one scale for each row."""
+    amax = np.abs(v).max(1)
+    a = np.where(amax > 0, amax, 1.0)
+    return np.clip(np.rint(v * 127 / a[:, None]), -127, 127), amax / 127
+
+
+# ---- norms around a block ----
+
+def block_rms_norm(x, post, gate, gate_every, act, residual, weight, block_scale, residual_scale, post_eps, eps):
+    """-> (h, v) in 64 bits: the residual stream behind the block, and the normalised row (None without weight)."""
+    u = np.asarray(x, np.float64)
+    if post is not None:
+        u = u / np.sqrt((u * u).mean(1, keepdims=True) + post_eps) * np.asarray(post, np.float64)
+    if gate is not None:
+        g = np.asarray(gate, np.float64)
+        g = 1 / (1 + np.exp(-g)) if act == "sigmoid" else np.tanh(g) if act == "tanh" else g
+        u = u * g[np.arange(u.shape[0]) // gate_every]
+    h = block_scale * u + (0 if residual is None else residual_scale * np.asarray(residual, np.float64))
+    if weight is None:
+        return h, None
+    return h, h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+
+
+# ---- a layer of experts ----
+
+def moe_routes(ids, scales, mask, first, local, routed, zero, copy):
+    """The routes of a token batch -> (weight [T][local] of the local experts, has [T][local], weight of the copy
+    experts [T], of all present routes [T], number of dropped routes)."""
+    T, K = ids.shape
+    weight, has = np.zeros((T, local)), np.zeros((T, local), bool)
+    cp, present, dropped = np.zeros(T), np.zeros(T), 0
+    for t in range(T):
+        for k in range(K):
+            on = mask is None or (mask[t] if mask.ndim == 1 else mask[t, k])
+            e = int(ids[t, k])
+            if not on:
+                continue
+            if e < 0 or e >= routed + zero + copy:
+                dropped += 1
+                continue
+            present[t] += scales[t, k]
+            if e >= routed + zero:
+                cp[t] += scales[t, k]
+            elif first <= e < min(first + local, routed):
+                weight[t, e - first] += scales[t, k]
+                has[t, e - first] = True
+    return weight, has, cp, present, dropped
