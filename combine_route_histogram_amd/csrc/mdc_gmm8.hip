@@ -47,77 +47,426 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t channel_scales(const Gmm8& g, 
 }
 
 // ---------------------------------------------------------------------------
-// Tiles of 64 rows x 64 columns, four wavefronts of 32 x 32 each; k in stages of
-// 128 bytes through LDS.  Chunk c (16 bytes) of row r sits at chunk c ^ ((r / 2) &
-// 7) of the row's 128 bytes, so that the reads of a fragment cover all banks.
+// Thin experts.  A tile is one expert's rows times 16 rs output columns: wavefront
+// (rb, kh) takes 16 weight rows of it over the kh-th of ks runs of k-blocks,
+// rs ks = 8, and the runs' sums are joined through LDS.  A workgroup takes a run of
+// consecutive tiles.
+//
+// The weights, which are all that memory has to bring, go global -> LDS directly,
+// eight rows x 128 bytes per instruction, into a ring of each wavefront's own,
+// kThin8Ring bytes ahead and on into the next tile.  They are read once: with the
+// non-temporal policy such loads reach 6.8 TB/s, without it 6.0 (940 MB, tiles of
+// 16 rows; the same for runs of 128 to 512 bytes and rings of 8 to 18 KB).  The
+// expert's rows stay in registers from tile to tile, kThin8Run k-blocks of them.
+//
+// LDS accesses are written out with their waits: the compiler would make each wait
+// for every direct load in flight.
 // ---------------------------------------------------------------------------
-constexpr int kSimple = 64;
+constexpr int kThin8Ring = 12288;   // bytes of a wavefront's ring
+constexpr int kThin8Run = 8;        // k-blocks of rows in registers
+constexpr int kThin8Nt = 2;         // cache policy: non-temporal
+constexpr int kWide8Cost = 2;       // a wide tile's time in those of 128 columns of thin work
 
+struct Thin8Smem {
+  unsigned ring;   // this wavefront's, kThin8Ring bytes
+  unsigned red;    // [2][8 wavefronts][2 row blocks][64] v4i
+};
+
+__device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, int wide, int ks, const Thin8Smem& sm) {
+  constexpr int MB = kThinBlocks, kSlot = 2048, kSlots = kThin8Ring / kSlot;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int K = g.K, nk = g.nk, Nw = g.Nw;
+  const int rs = kGmmWaves / ks, rb = wave / ks, kh = wave - rb * ks;
+  const int per = (nk + ks - 1) / ks, kb0 = kh * per;
+  const int width = 16 * rs, tiles_per = (Nw + width - 1) / width;
+  // this workgroup's tiles: [t0, t1) of n_thin * tiles_per
+  const int64_t T = (int64_t)tab.n_thin * tiles_per;
+  const int cost = max(1, kWide8Cost * 8 / rs);
+  const int t0 = (int)thin_share(T, wide, cost, wide_line()), t1 = (int)thin_share(T, wide, cost, wide_line() + 1);
+  if (t0 == t1) return;
+
+  // ---- weights: tile by tile, step by step ----
+  auto weights = [&](int i) {
+    const int e = __builtin_amdgcn_readfirstlane((int)tab.thin[i]);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(g.w + (int64_t)e * Nw * K), (short)0, Nw * K, 0x00020000);
+  };
+  struct {
+    int i, n, step, left;   // place of the expert in the list, first column, step, tiles to come
+  } c = {t0 / tiles_per, (t0 % tiles_per) * width, 0, t1 - t0};
+  __amdgpu_buffer_rsrc_t rw = weights(c.i);
+  unsigned slot = 0;   // of the next load
+  const int lrow = lane >> 3;
+  auto fetch = [&]() {
+    const bool in = c.left > 0;
+    const unsigned k0 = in ? (unsigned)min(kb0 + c.step, nk) * kGmm8Block : (unsigned)nk * kGmm8Block;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // rows 8 h + lane / 8; the chunk whose place lane % 8 is
+      const unsigned chunk = (unsigned)((lane & 7) ^ ((4 * h + (lrow >> 1)) & 7)) << 4;
+      const int row = c.n + 16 * rb + 8 * h + lrow;
+      const unsigned at = k0 + chunk < (unsigned)K && row < Nw ? (unsigned)row * (unsigned)K + k0 + chunk : kPastEnd;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(sm.ring + slot + h * 1024), 16, at, 0, 0, kThin8Nt);
+    }
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    if (++c.step == per) {
+      c.step = 0;
+      --c.left;
+      c.n += width;
+      if (c.n >= Nw) {
+        c.n = 0;
+        if (c.left > 0) rw = weights(++c.i);
+      }
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < kSlots; ++d) fetch();
+
+  const int key = (r16 >> 1) & 7;
+  const unsigned f0 = sm.ring + r16 * kGmm8Block + ((quad ^ key) << 4);
+  const unsigned f1 = sm.ring + r16 * kGmm8Block + (((4 + quad) ^ key) << 4);
+  unsigned read = 0;
+  v8i tok[kThin8Run][MB];
+  float sa[MB];
+  int i = t0 / tiles_per, n0 = (t0 % tiles_per) * width, have = -1, e = 0, row0 = 0, rows = 0;
+  for (int t = t0; t < t1; ++t) {
+    if (i != have) {
+      e = __builtin_amdgcn_readfirstlane((int)tab.thin[i]);
+      row0 = __builtin_amdgcn_readfirstlane(tab.rows[e]);
+      rows = __builtin_amdgcn_readfirstlane(tab.rows[e + 1] - row0);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) sa[m] = g.a_scale[row0 + min(16 * m + r16, rows - 1)];
+    }
+    v4i acc[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[m] = v4i{0, 0, 0, 0};
+    for (int s0 = 0; s0 < per; s0 += kThin8Run) {
+      if (i != have || per > kThin8Run) {
+        // the rows' k-blocks of this run, in the matrix instruction's layout
+        const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<int8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
+#pragma unroll
+        for (int d = 0; d < kThin8Run; ++d) {
+          const int b = s0 + d < per ? kb0 + s0 + d : nk;
+          const unsigned k0 = (unsigned)b * kGmm8Block + 16u * quad, k1 = k0 + 64u;
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            const unsigned at = (unsigned)((16 * m + r16) * K);
+            tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
+                             __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kThin8Run; ++d) {
+        if (s0 + d < per) {
+          __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2));   // at most the loads of the other slots are out
+          const v8i w = lds_get2(f0 + read, f1 + read);
+          read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
+          fetch();
+          const v4i w0 = {w[0], w[1], w[2], w[3]}, w1 = {w[4], w[5], w[6], w[7]};
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            const v8i q = tok[d][m];
+            acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, v4i{q[0], q[1], q[2], q[3]}, acc[m], 0, 0, 0);
+            acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, v4i{q[4], q[5], q[6], q[7]}, acc[m], 0, 0, 0);
+          }
+        }
+      }
+      have = i;
+    }
+    // join the runs of k-blocks: job (column block, row block) by another wavefront for each tile
+    const unsigned red = sm.red + (t & 1) * (kGmmWaves * MB * 1024);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) lds_put(red + ((wave * MB + m) * 64 + lane) * 16, __builtin_bit_cast(v4f, acc[m]));
+    lds_barrier();
+    for (int job = (wave + MB * t) & (kGmmWaves - 1); job < MB * rs; job += kGmmWaves) {
+      const int ob = job / MB, m = job % MB;
+      const int col0 = n0 + 16 * ob;
+      if (16 * m < rows && col0 < Nw) {
+        v4i sum = {0, 0, 0, 0};
+        for (int k = 0; k < ks; ++k) {
+          const unsigned at = red + (((ob * ks + k) * MB + m) * 64 + lane) * 16;
+          const v8i p = lds_get2(at, at);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[r] += p[r];
+        }
+        const int row = 16 * m + r16, col = col0 + 4 * quad;
+        // the 16 channels' scales by scalar loads: they pass by the direct loads' count
+        const scalar_f* p = (const scalar_f*)(g.w_scale + (int64_t)e * Nw);
+        v4f sw;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float a0 = p[min(col0 + r, Nw - 1)], a1 = p[min(col0 + 4 + r, Nw - 1)];
+          const float a2 = p[min(col0 + 8 + r, Nw - 1)], a3 = p[min(col0 + 12 + r, Nw - 1)];
+          sw[r] = quad < 2 ? (quad == 0 ? a0 : a1) : (quad == 2 ? a2 : a3);
+        }
+        if (row < rows && col < Nw) gmm8_store(g, (int64_t)(row0 + row) * Nw + col, gmm8_scale(sum, m == 0 ? sa[0] : sa[1], sw));
+      }
+    }
+    n0 += width;
+    if (n0 >= Nw) {
+      n0 = 0;
+      ++i;
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
+}
+
+// ks: at least 6 k-blocks per wavefront, and as many tiles as workgroups.
+__device__ __forceinline__ int thin8_split(const Gmm8& g, int experts) {
+  int ks = g.nk >= 48 ? 8 : g.nk >= 24 ? 4 : g.nk >= 12 ? 2 : 1;
+  while (ks < kGmmWaves && experts * ((g.Nw + 128 / ks - 1) / (128 / ks)) < (int)gridDim.x) ks *= 2;
+  return ks;
+}
+
+// ---------------------------------------------------------------------------
+// Experts with more rows: tiles of BM = 32 to 256 rows x 256 weight rows, one
+// workgroup of W wavefronts per CU walking tiles.  Each k-block of 128 is one
+// stage, loaded global -> LDS directly into a ring of S stages while earlier ones
+// are multiplied.  Wavefront (wt, wn) holds the token blocks i WT + wt (32 rows
+// each, so that a short tile's blocks are shared) x WB weight blocks of 32.
+//
+// A stage is four steps of 32 k.  The fragments of a step are read while the one
+// before it is multiplied; the last step's products run behind the barrier that
+// opens the next stage, beside that stage's first reads.
+//
+// LDS: chunk c (16 bytes) of row r sits at chunk c ^ ((r / 2) & 7) of the row's
+// 128 bytes, so that 16 rows read at one chunk cover all banks.
+// ---------------------------------------------------------------------------
+constexpr int kWide8 = 256;   // weight rows of a tile
+constexpr int wide8_stage(int BM) { return (BM + kWide8) * kGmm8Block; }
+
+template <int BM, int W>
+struct Wide8 {
+  static constexpr int WT = BM >= (W == 8 ? 64 : 128) ? 2 : 1;   // wavefronts along the rows
+  static constexpr int TB = BM / 32 / WT, WW = W / WT, WB = kWide8 / 32 / WW;
+};
+
+template <int BM, int W, int S, int NB>
+__device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, unsigned lds,
+                                            v16i (&acc)[Wide8<BM, W>::TB][Wide8<BM, W>::WB]) {
+  typedef Wide8<BM, W> C;
+  constexpr int kStage = wide8_stage(BM), kRing = S * kStage, kTokenBytes = BM * kGmm8Block;
+  constexpr int kWeightLoads = 32 / W, kTokenLoads = BM / 8 >= W ? BM / 8 / W : 1;
+  constexpr int kLoads = kWeightLoads + kTokenLoads, kPart = (kLoads + 3) / 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / C::WW, wn = wave % C::WW;
+  const int K = g.K, nk = g.nk, Nw = g.Nw;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(g.a + (int64_t)t.row0 * K), (short)0, t.rows * K, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(g.w + ((int64_t)t.e * Nw + t.n0) * K), (short)0, (Nw - t.n0) * K, 0x00020000);
+  unsigned vo[2], chunk[2];   // lane part of a load of eight rows, by the parity of its place
+#pragma unroll
+  for (int par = 0; par < 2; ++par) {
+    chunk[par] = (unsigned)(((lane & 7) ^ ((4 * par + (lane >> 4)) & 7)) << 4);
+    vo[par] = (unsigned)((lane >> 3) * K) + chunk[par];
+  }
+  // direct loads of k-block b into the stage at `at` of the ring, in four parts
+  auto dma = [&](int at, int b, int part) {
+    unsigned v[2];
+    const unsigned k0 = (unsigned)b * kGmm8Block;
+#pragma unroll
+    for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kPastEnd;   // zeros past K
+#pragma unroll
+    for (int q = part * kPart; q < min(kLoads, (part + 1) * kPart); ++q) {
+      if (q < kWeightLoads) {
+        const int blk = kWeightLoads * wave + q;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(lds + at + kTokenBytes + blk * 1024), 16, v[q & 1],
+                                                 k0 + (unsigned)(8 * blk * K), 0, 0);
+      } else {
+        const int blk = (kTokenLoads * wave + q - kWeightLoads) & (BM / 8 - 1);   // (BM = 32, W = 8: two load the same)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(lds + at + blk * 1024), 16, v[blk & 1],
+                                                 k0 + (unsigned)(8 * blk * K), 0, 0);
+      }
+    }
+  };
+  // fragments: lane l reads row l % 32 of a block, chunk 2 q + l / 32 of step q
+  typedef const __attribute__((address_space(3))) v4i lds_v4i;
+  unsigned fr[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    fr[q] = lds + (lane & 31) * kGmm8Block + (((2 * q + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4);
+  v4i tf[2][NB], wf[2][C::WB];
+  auto frags = [&](int at, int q) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) tf[q & 1][i] = *(lds_v4i*)(size_t)(fr[q] + at + 32 * (i * C::WT + wt) * kGmm8Block);
+#pragma unroll
+    for (int j = 0; j < C::WB; ++j)
+      wf[q & 1][j] = *(lds_v4i*)(size_t)(fr[q] + at + kTokenBytes + 32 * (wn * C::WB + j) * kGmm8Block);
+  };
+  auto mfmas = [&](int q) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < C::WB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[q & 1][j], tf[q & 1][i], acc[i][j], 0, 0, 0);
+  };
+  constexpr int NR = NB + C::WB, NM = NB * C::WB;
+  // the step's reads and direct loads between its products
+  auto interleave = [&]() {
+#pragma unroll
+    for (int n = 0; n < (NR > NM ? NR : NM); ++n) {
+      if (n < NM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (n < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (n < kPart) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int kAhead = 0x0F70 | (((S - 2) * kLoads) & 15) | ((((S - 2) * kLoads) >> 4) << 14);   // vmcnt of S - 2 stages
+#pragma unroll
+  for (int d = 0; d < S - 1; ++d)
+#pragma unroll
+    for (int part = 0; part < 4; ++part) dma(d * kStage, d, part);
+  __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of stage 0 have landed
+  lds_barrier();
+  dma((S - 1) * kStage, S - 1, 0);
+  frags(0, 0);
+  int cur = 0, nxt = kStage, last = (S - 1) * kStage;   // places of k-blocks b, b + 1, b + S - 1
+  for (int b = 0; b < nk; ++b) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      frags(cur, q + 1);
+      dma(last, b + S - 1, q + 1);
+      mfmas(q);
+      interleave();
+    }
+    __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of k-block b + 1 have landed
+    lds_barrier();
+    frags(nxt, 0);   // (after the last stage: read, never used)
+    dma(cur, b + S, 0);
+    mfmas(3);
+    interleave();
+    last = cur;
+    cur = nxt;
+    nxt = nxt + kStage == kRing ? 0 : nxt + kStage;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the loads past the last stage (of zeros) have landed too
+}
+
+// One tile: the k loop, then the outputs, 16-bit ones through LDS as whole rows.
+template <int BM, int W, int S>
+__device__ __forceinline__ void wide8_tile(const Gmm8& g, const WideTile& t, uint8_t* smem) {
+  typedef Wide8<BM, W> C;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wt = wave / C::WW, wn = wave % C::WW;
+  v16i acc[C::TB][C::WB];
+#pragma unroll
+  for (int i = 0; i < C::TB; ++i)
+#pragma unroll
+    for (int j = 0; j < C::WB; ++j) acc[i][j] = v16i{};
+  const unsigned lds = lds_at(smem);
+  const int blocks = (t.rows + 32 * C::WT - 1) / (32 * C::WT);   // of each wavefront that hold rows
+  if constexpr (C::TB == 1) wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+  else if constexpr (C::TB == 2) {
+    if (blocks > 1) wide8_kloop<BM, W, S, 2>(g, t, lds, acc);
+    else wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+  } else {
+    if (blocks > 3) wide8_kloop<BM, W, S, 4>(g, t, lds, acc);
+    else if (blocks > 2) wide8_kloop<BM, W, S, 3>(g, t, lds, acc);
+    else if (blocks > 1) wide8_kloop<BM, W, S, 2>(g, t, lds, acc);
+    else wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+  }
+  const __amdgpu_buffer_rsrc_t rc = channel_scales(g, t.e);
+  v4f sw[C::WB][4];
+  float sa[C::TB];
+#pragma unroll
+  for (int j = 0; j < C::WB; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sw[j][q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rc, (unsigned)(t.n0 + 32 * (wn * C::WB + j) + 8 * q + 4 * (lane >> 5)) * 4u, 0, 0));
+#pragma unroll
+  for (int i = 0; i < C::TB; ++i) sa[i] = g.a_scale[t.row0 + min(32 * (i * C::WT + wt) + (lane & 31), t.rows - 1)];
+  __syncthreads();   // every wavefront has left the ring
+  auto outputs = [&](auto&& put) {   // put(row, column, four values): those of the tile
+#pragma unroll
+    for (int i = 0; i < C::TB; ++i)
+#pragma unroll
+      for (int j = 0; j < C::WB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          put(32 * (i * C::WT + wt) + (lane & 31), 32 * (wn * C::WB + j) + 8 * q + 4 * (lane >> 5),
+              gmm8_scale(v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}, sa[i], sw[j][q]));
+  };
+  const bool wide = g.dtype == MDC_DTYPE_FP32;
+  auto place = [&](int row, int in) {   // 16-byte units of 8 columns
+    return smem + row * 512 + (((in >> 3) ^ (row & 31)) << 4) + 8 * (lane >> 5);
+  };
+  if (wide)
+    outputs([&](int row, int in, v4f v) {
+      if (row < t.rows && t.n0 + in < g.Nw)
+        *reinterpret_cast<v4f*>(static_cast<float*>(g.y) + (int64_t)(t.row0 + row) * g.Nw + t.n0 + in) = v;
+    });
+  else if (g.dtype == MDC_DTYPE_BF16)
+    outputs([&](int row, int in, v4f v) { *reinterpret_cast<v4b*>(place(row, in)) = __builtin_convertvector(v, v4b); });
+  else outputs([&](int row, int in, v4f v) { *reinterpret_cast<v4h*>(place(row, in)) = __builtin_convertvector(v, v4h); });
+  if (!wide) {
+    __syncthreads();
+    const int unit = tid & 31, col = t.n0 + 8 * unit;
+    if (col < g.Nw)
+      for (int r = tid >> 5; r < t.rows; r += 64 * W / 32)
+        *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.y) + (int64_t)(t.row0 + r) * g.Nw + col) =
+            *reinterpret_cast<const v4u*>(smem + r * 512 + ((unit ^ (r & 31)) << 4));
+  }
+  __syncthreads();   // the ring is free
+}
+
+template <int BM, int W, int S>
+__device__ __forceinline__ void wide8_walk(const Gmm8& g, const GmmTable& tab, uint8_t* smem) {
+  const int nn = (g.Nw + kWide8 - 1) / kWide8;
+  const int T = tab.tiles[g.L] * nn;
+  for (int t = wide_line(); t < T; t += gridDim.x) wide8_tile<BM, W, S>(g, wide_place(g, tab, t, nn, BM, kWide8), smem);
+}
+
+// What a k-block of a tile of 256, 128, 64 and 32 rows takes, in tenths of a microsecond.
+constexpr int kCost8_256 = 20, kCost8_128 = 12, kCost8_64 = 8, kCost8_32 = 6;
+
+// LDS of the tiles; 128-row tiles take three stages and 32-row tiles four where the experts' table leaves that much.
+constexpr int kLds8Deep = 3 * wide8_stage(128), kLds8Flat = 2 * wide8_stage(256);
+static_assert(kLds8Flat >= 3 * wide8_stage(64) && kLds8Flat >= 3 * wide8_stage(32) && kLds8Deep >= 4 * wide8_stage(32) &&
+                  kLds8Deep >= kLds8Flat && kLds8Flat >= kGmmWaves * kThin8Ring + 2 * kGmmWaves * kThinBlocks * 1024,
+              "LDS of the tiles");
+
+// One workgroup per CU: the wide experts' tiles, then the thin experts'.
+template <bool DEEP>
 __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
   extern __shared__ int gmm_table[];
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kSimple * kGmm8Block];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[DEEP ? kLds8Deep : kLds8Flat];
   __shared__ int64_t wave_total[kGmmWaves];
   GmmTable tab{gmm_table, gmm_table + g.L + 1, reinterpret_cast<uint16_t*>(gmm_table + 2 * (g.L + 1)), 0};
   gmm_rows<kGmmThreads>(g, tab.rows, wave_total);
-  // every expert as a wide one
-  int64_t carry = 0, all;
-  for (int e0 = 0; e0 < g.L; e0 += kGmmThreads) {
-    const int e = e0 + threadIdx.x;
-    const int n = e < g.L ? tab.rows[e + 1] - tab.rows[e] : 0;
-    const int64_t end = carry + block_scan<kGmmThreads>(n > 0 ? (n - 1) / kSimple + 1 : 0, wave_total, all);
-    if (e < g.L) tab.tiles[e + 1] = (int)end;
-    carry += all;
+  const int nn = (g.Nw + kWide8 - 1) / kWide8;
+  const int G = gridDim.x;
+  constexpr int W = kGmmWaves;
+  int wide = gmm_tiles(g, tab, 256, wave_total) * nn;
+  if (wide != 0) {
+    // Tiles of 256, 128, 64 or 32 rows, whichever rounds of tiles take less time:
+    // large ones do more products per byte and stage, small ones fill the CUs.
+    int best = 256, cost = kCost8_256 * ((wide + G - 1) / G), count[3];
+    gmm_tile_counts(g, tab, count);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = (i == 0 ? kCost8_128 : i == 1 ? kCost8_64 : kCost8_32) * ((count[i] * nn + G - 1) / G);
+      if (c < cost) {
+        best = 128 >> i;
+        cost = c;
+      }
+    }
+    if (best != 256) wide = gmm_tiles(g, tab, best, wave_total) * nn;
+    if (best == 32) wide8_walk<32, W, DEEP ? 4 : 3>(g, tab, smem);
+    else if (best == 64) wide8_walk<64, W, 3>(g, tab, smem);
+    else if (best == 128) wide8_walk<128, W, DEEP ? 3 : 2>(g, tab, smem);
+    else wide8_walk<256, W, 2>(g, tab, smem);
   }
-  if (threadIdx.x == 0) tab.tiles[0] = 0;
-  __syncthreads();
-  const int nn = (g.Nw + kSimple - 1) / kSimple;
-  const int T = tab.tiles[g.L] * nn;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wt = (wave >> 1) & 1, wn = wave & 1;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const int m = t / nn, n0 = (t - m * nn) * kSimple;
-    const int e = gmm_expert(tab, g.L, m);
-    const int row0 = tab.rows[e] + (m - tab.tiles[e]) * kSimple, rows = min(kSimple, tab.rows[e + 1] - row0);
-    v16i acc = v16i{};
-    for (int b = 0; b < g.nk; ++b) {
-      __syncthreads();
-      // thread (row, chunk) of 128 rows (tokens, then weights): two chunks each
-      for (int i = tid; i < 2 * kSimple * 8; i += kGmmThreads) {
-        const int r = i >> 3, c = i & 7, k = b * kGmm8Block + 16 * c;
-        v4i v = {0, 0, 0, 0};
-        if (k < g.K) {
-          if (r < kSimple) {
-            if (r < rows) v = *reinterpret_cast<const v4i*>(g.a + (int64_t)(row0 + r) * g.K + k);
-          } else if (n0 + r - kSimple < g.Nw) {
-            v = *reinterpret_cast<const v4i*>(g.w + ((int64_t)e * g.Nw + n0 + r - kSimple) * g.K + k);
-          }
-        }
-        *reinterpret_cast<v4i*>(smem + r * kGmm8Block + ((c ^ ((r >> 1) & 7)) << 4)) = v;
-      }
-      __syncthreads();
-      if (wave < 4) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int rt = 32 * wt + (lane & 31), rw = kSimple + 32 * wn + (lane & 31), c = 2 * q + (lane >> 5);
-          const v4i ft = *reinterpret_cast<const v4i*>(smem + rt * kGmm8Block + ((c ^ ((rt >> 1) & 7)) << 4));
-          const v4i fw = *reinterpret_cast<const v4i*>(smem + rw * kGmm8Block + ((c ^ ((rw >> 1) & 7)) << 4));
-          acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw, ft, acc, 0, 0, 0);
-        }
-      }
-    }
-    const int r = 32 * wt + (lane & 31);
-    if (wave < 4 && r < rows) {
-      const __amdgpu_buffer_rsrc_t rc = channel_scales(g, e);
-      const float sa = g.a_scale[row0 + r];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = n0 + 32 * wn + 8 * q + 4 * (lane >> 5);
-        if (col < g.Nw) {
-          const v4f sw = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, col * 4, 0, 0));
-          gmm8_store(g, (int64_t)(row0 + r) * g.Nw + col, gmm8_scale(v4i{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]}, sa, sw));
-        }
-      }
-    }
+  if (tab.n_thin != 0) {
+    __syncthreads();   // smem is free
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    thin8_walk(g, tab, wide, thin8_split(g, tab.n_thin),
+               Thin8Smem{lds_at(smem) + wave * kThin8Ring, lds_at(smem) + kGmmWaves * kThin8Ring});
   }
 }
 
@@ -126,7 +475,10 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
 // ---------------------------------------------------------------------------
 void launch_gmm8(const Gmm8& g, hipStream_t s) {
   const dim3 grid((device_cus() + 7) / 8 * 8), block(kGmmThreads);
-  hipLaunchKernelGGL(k_gmm8, grid, block, gmm_table_bytes(g.L), s, g);
+  const size_t table = gmm_table_bytes(g.L);
+  if (table + kLds8Deep + 256 <= kLdsSize)   // (256: the plan's few words)
+    hipLaunchKernelGGL(k_gmm8<true>, grid, block, table, s, g);
+  else hipLaunchKernelGGL(k_gmm8<false>, grid, block, table, s, g);
 }
 
 constexpr int kGmm8MaxK = 1 << 17;   // below it 2^14 K fits 32 bits
