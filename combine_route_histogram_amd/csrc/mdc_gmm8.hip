@@ -249,7 +249,7 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
   typedef Wide8<BM, W> C;
   constexpr int kStage = wide8_stage(BM), kRing = S * kStage, kTokenBytes = BM * kGmm8Block;
   constexpr int kWeightLoads = 32 / W, kTokenLoads = BM / 8 >= W ? BM / 8 / W : 1;
-  constexpr int kLoads = kWeightLoads + kTokenLoads, kPart = (kLoads + 3) / 4;
+  constexpr int kLoads = kWeightLoads + kTokenLoads, kParts = S == 2 ? 2 : 4, kPart = (kLoads + kParts - 1) / kParts;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wt = wave / C::WW, wn = wave % C::WW;
@@ -270,16 +270,23 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
     const unsigned k0 = (unsigned)b * kGmm8Block;
 #pragma unroll
     for (int par = 0; par < 2; ++par) v[par] = k0 + chunk[par] < (unsigned)K ? vo[par] : kPastEnd;   // zeros past K
+    // (offsets step by step: hoisted out of the loop they would take a scalar register each)
+    unsigned so = k0 + (unsigned)(8 * kWeightLoads * K) * (unsigned)wave, st = k0 + (unsigned)(8 * kTokenLoads * K) * (unsigned)wave;
 #pragma unroll
     for (int q = part * kPart; q < min(kLoads, (part + 1) * kPart); ++q) {
+      if (q == part * kPart && q < kWeightLoads) so += (unsigned)(8 * q * K);
+      if (q == part * kPart && q > kWeightLoads) st += (unsigned)(8 * (q - kWeightLoads) * K);
       if (q < kWeightLoads) {
-        const int blk = kWeightLoads * wave + q;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(lds + at + kTokenBytes + blk * 1024), 16, v[q & 1],
-                                                 k0 + (unsigned)(8 * blk * K), 0, 0);
+        asm("" : "+s"(so));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(lds + at + kTokenBytes + (kWeightLoads * wave + q) * 1024), 16,
+                                                 v[q & 1], so, 0, 0);
+        so += 8u * (unsigned)K;
       } else {
+        asm("" : "+s"(st));
         const int blk = (kTokenLoads * wave + q - kWeightLoads) & (BM / 8 - 1);   // (BM = 32, W = 8: two load the same)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(lds + at + blk * 1024), 16, v[blk & 1],
-                                                 k0 + (unsigned)(8 * blk * K), 0, 0);
+        const unsigned off = BM / 8 >= W ? st : k0 + (unsigned)(8 * blk * K);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(lds + at + blk * 1024), 16, v[blk & 1], off, 0, 0);
+        st += 8u * (unsigned)K;
       }
     }
   };
@@ -306,12 +313,12 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
   };
   constexpr int NR = NB + C::WB, NM = NB * C::WB;
   // the step's reads and direct loads between its products
-  auto interleave = [&]() {
+  auto interleave = [&](bool loads) {
 #pragma unroll
     for (int n = 0; n < (NR > NM ? NR : NM); ++n) {
       if (n < NM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (n < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (n < kPart) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (loads && n < kPart) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -319,7 +326,7 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
 #pragma unroll
   for (int d = 0; d < S - 1; ++d)
 #pragma unroll
-    for (int part = 0; part < 4; ++part) dma(d * kStage, d, part);
+    for (int part = 0; part < kParts; ++part) dma(d * kStage, d, part);
   __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of stage 0 have landed
   lds_barrier();
   dma((S - 1) * kStage, S - 1, 0);
@@ -329,16 +336,16 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       frags(cur, q + 1);
-      dma(last, b + S - 1, q + 1);
+      if (q + 1 < kParts) dma(last, b + S - 1, q + 1);
       mfmas(q);
-      interleave();
+      interleave(q + 1 < kParts);
     }
     __builtin_amdgcn_s_waitcnt(kAhead);   // this wavefront's loads of k-block b + 1 have landed
     lds_barrier();
     frags(nxt, 0);   // (after the last stage: read, never used)
     dma(cur, b + S, 0);
     mfmas(3);
-    interleave();
+    interleave(true);
     last = cur;
     cur = nxt;
     nxt = nxt + kStage == kRing ? 0 : nxt + kStage;
@@ -409,10 +416,10 @@ __device__ __forceinline__ void wide8_tile(const Gmm8& g, const WideTile& t, uin
     const int unit = tid & 31, col = t.n0 + 8 * unit;
     if (col < g.Nw)
       for (int r = tid >> 5; r < t.rows; r += 64 * W / 32)
-        *reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.y) + (int64_t)(t.row0 + r) * g.Nw + col) =
-            *reinterpret_cast<const v4u*>(smem + r * 512 + ((unit ^ (r & 31)) << 4));
+        __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(smem + r * 512 + ((unit ^ (r & 31)) << 4)),
+            reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.y) + (int64_t)(t.row0 + r) * g.Nw + col));
   }
-  __syncthreads();   // the ring is free
+  lds_barrier();   // the ring is free
 }
 
 template <int BM, int W, int S>
