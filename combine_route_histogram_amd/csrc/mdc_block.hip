@@ -15,6 +15,12 @@ namespace {
 //
 // Sums and everything up to the outputs are fp32; residual_out, y and q are
 // rounded once each, from the unrounded values.
+//
+// Bound: memory.  16384 rows of 7168 (bf16, residual in and out, y, fp8 rows and
+// scales: 1.06 GB) 196 us, 5.4 TB/s, where mdc_add_rms_norm takes 184 and a plain
+// read and write of its bytes 172: a row waits at one sum more.  With a gate value
+// for each element 226 us (5.7 TB/s), with its sigmoid 241: two exact functions of
+// fp32, an exponential and a quotient.
 // ---------------------------------------------------------------------------
 struct BlockArgs {
   const void* x;
@@ -32,14 +38,48 @@ struct BlockArgs {
   float block_scale, res_scale, post_eps, eps, inv_hidden;
 };
 
-__device__ __forceinline__ float block_act(float g, int act) {
-  if (act == MDC_ACT_SIGMOID) return 1.0f / (1.0f + expf(-g));
-  if (act == MDC_ACT_TANH) return tanhf(g);
-  return g;
+// act(g) * scale of n gate values
+template <int n>
+__device__ __forceinline__ void block_act(float (&g)[n], int act, float scale) {
+  if (act == MDC_ACT_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < n; ++j) g[j] = 1.0f / (1.0f + expf(-g[j]));
+  } else if (act == MDC_ACT_TANH) {
+#pragma unroll
+    for (int j = 0; j < n; ++j) g[j] = tanhf(g[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < n; ++j) g[j] *= scale;
 }
 
 __device__ __forceinline__ float load1(const Bf16* p) { return __uint_as_float((uint32_t)p->bits << 16); }
 __device__ __forceinline__ float load1(const _Float16* p) { return (float)*p; }
+
+// Eight elements as they lie in memory, to be loaded now and looked at later.
+template <typename T>
+struct Raw {
+  v4u v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const v4u*>(p); }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    const v4u w = v;
+    load8(reinterpret_cast<const T*>(&w), f);
+  }
+};
+template <>
+struct Raw<float> {
+  v4f a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const v4f*>(p)[0];
+    b = reinterpret_cast<const v4f*>(p)[1];
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = a[i];
+      f[4 + i] = b[i];
+    }
+  }
+};
 
 template <typename T, typename R, typename Wt, int QUANT, int VPT>
 __global__ __launch_bounds__(kNormThreads) void k_block_rms_norm(BlockArgs a) {
@@ -50,42 +90,67 @@ __global__ __launch_bounds__(kNormThreads) void k_block_rms_norm(BlockArgs a) {
   if (row >= a.rows) return;
   const int64_t at = row * a.nvec;   // first vector of the row
   const int64_t gate_row = (int)row / a.gate_every;
-  float gate1 = 1.f;
-  if (a.gate != nullptr && !a.gate_wide)
-    gate1 = block_act(a.gate32 ? static_cast<const float*>(a.gate)[gate_row] : load1(static_cast<const T*>(a.gate) + gate_row),
-                      a.act);
-  gate1 *= a.block_scale;
+  Raw<T> x[VPT];
+  Raw<R> res[VPT];
+  Raw<Wt> post[VPT], weight[VPT];
+  v4u gate[VPT][2];
+  // every load before the first use: one trip to memory for all of them
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int i = min(tid + u * threads, a.nvec - 1);   // (threads past the row's end load its last vector)
+    x[u].load(static_cast<const T*>(a.x) + (at + i) * 8);
+    if (a.res != nullptr) res[u].load(static_cast<const R*>(a.res) + (at + i) * 8);
+    if (a.gate_wide) {
+      const int64_t g = gate_row * a.nvec + i;
+      gate[u][0] = static_cast<const v4u*>(a.gate)[a.gate32 ? 2 * g : g];
+      if (a.gate32) gate[u][1] = static_cast<const v4u*>(a.gate)[2 * g + 1];
+    }
+    if (a.post != nullptr) post[u].load(static_cast<const Wt*>(a.post) + i * 8);
+    if (VPT < 4 && a.weight != nullptr) weight[u].load(static_cast<const Wt*>(a.weight) + i * 8);
+  }
+  float gate1[1] = {1.f};
+  if (a.gate != nullptr && !a.gate_wide) {
+    gate1[0] = a.gate32 ? static_cast<const float*>(a.gate)[gate_row] : load1(static_cast<const T*>(a.gate) + gate_row);
+    block_act(gate1, a.act, a.block_scale);
+  } else {
+    gate1[0] = a.block_scale;
+  }
   float h[VPT][8], r[VPT][8];
   float sum = 0.f;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
-    const int i = tid + u * threads;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[u][j] = r[u][j] = 0.f;
-    if (i < a.nvec) {
-      load8(static_cast<const T*>(a.x) + (at + i) * 8, h[u]);
-      if (a.res != nullptr) load8(static_cast<const R*>(a.res) + (at + i) * 8, r[u]);
-      float w[8];
-      if (a.post != nullptr) {
-        load8(static_cast<const Wt*>(a.post) + i * 8, w);
+    const bool in = tid + u * threads < a.nvec;
+    x[u].values(h[u]);
+    float w[8];
+    if (a.post != nullptr) {
+      if (in)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[u][j], h[u][j], sum);
+      post[u].values(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[u][j] *= w[j];
-      }
-      if (a.gate_wide) {
-        const int64_t g = (gate_row * a.nvec + i) * 8;
-        if (a.gate32) load8(static_cast<const float*>(a.gate) + g, w);
-        else load8(static_cast<const T*>(a.gate) + g, w);
+      for (int j = 0; j < 8; ++j) h[u][j] *= w[j];
+    }
+    if (a.gate_wide) {
+      if (a.gate32) Raw<float>{__builtin_bit_cast(v4f, gate[u][0]), __builtin_bit_cast(v4f, gate[u][1])}.values(w);
+      else Raw<T>{gate[u][0]}.values(w);
+      block_act(w, a.act, a.block_scale);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[u][j] *= block_act(w[j], a.act) * a.block_scale;
-      } else {
+      for (int j = 0; j < 8; ++j) h[u][j] *= w[j];
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[u][j] *= gate1;
-      }
+      for (int j = 0; j < 8; ++j) h[u][j] *= gate1[0];
+    }
+    if (a.res != nullptr) {
+      res[u].values(r[u]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[u][j] *= a.res_scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[u][j] = 0.f;
     }
+    if (!in)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[u][j] = r[u][j] = 0.f;
   }
   float inv = 1.f;
   if (a.post != nullptr) inv = 1.0f / sqrtf(row_sum(sum, part[0]) * a.inv_hidden + a.post_eps);
@@ -94,16 +159,18 @@ __global__ __launch_bounds__(kNormThreads) void k_block_rms_norm(BlockArgs a) {
   for (int u = 0; u < VPT; ++u) {
     const int i = tid + u * threads;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[u][j] = __builtin_fmaf(h[u][j], inv, r[u][j]);
-      sum = __builtin_fmaf(h[u][j], h[u][j], sum);
+    for (int j = 0; j < 8; ++j) h[u][j] = __builtin_fmaf(h[u][j], inv, r[u][j]);
+    if (i < a.nvec) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[u][j], h[u][j], sum);
+      if (a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
     }
-    if (i < a.nvec && a.res_out != nullptr) store8(static_cast<R*>(a.res_out) + (at + i) * 8, h[u]);
   }
   if (a.weight == nullptr) return;
   inv = 1.0f / sqrtf(row_sum(sum, part[1]) * a.inv_hidden + a.eps);
-  norm_outputs<T, QUANT, VPT>(a.out, row, h, inv, part_max, [&](int, int i, float (&w)[8]) {
-    load8(static_cast<const Wt*>(a.weight) + i * 8, w);
+  norm_outputs<T, QUANT, VPT>(a.out, row, h, inv, part_max, [&](int u, int i, float (&w)[8]) {
+    if (VPT < 4) weight[u].values(w);
+    else load8(static_cast<const Wt*>(a.weight) + i * 8, w);
   });
 }
 
@@ -117,8 +184,12 @@ void launch_block_quant(const BlockArgs& a, hipStream_t s) {
     const int threads = ((a.nvec + per - 1) / per + 63) / 64 * 64;
     hipLaunchKernelGGL(kernel, grid_of(a.rows), dim3(threads), 0, s, a);
   };
-  // A vector per thread as far as a workgroup has threads; longer rows need two or four.
-  if (a.nvec <= kNormThreads) go(std::integral_constant<int, 1>(), k_block_rms_norm<T, R, Wt, QUANT, 1>);
+  // Two vectors a thread from 257 on: smaller workgroups, of which a CU holds more,
+  // so that one's waits at its sums are another's loads.  16384 rows of 7168 (bf16,
+  // a gate row for 2048 rows, y and fp8 out) take 227 us with one vector a thread,
+  // 196 with two, 201 with four; 2051 x 5000 36, 33 and 38; 8192 rows of 16384 228
+  // with two, 242 with four.
+  if (a.nvec <= kNormThreads / 4) go(std::integral_constant<int, 1>(), k_block_rms_norm<T, R, Wt, QUANT, 1>);
   else if (a.nvec <= 2 * kNormThreads) go(std::integral_constant<int, 2>(), k_block_rms_norm<T, R, Wt, QUANT, 2>);
   else go(std::integral_constant<int, 4>(), k_block_rms_norm<T, R, Wt, QUANT, 4>);
 }
