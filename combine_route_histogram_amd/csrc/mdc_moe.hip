@@ -1,21 +1,23 @@
 // libmdc: a whole layer of experts for a few tokens, for AMD Instinct MI355X
 // (gfx950): mdc_moe (int8 experts), mdc_moe_fp8 (e4m3 experts).
 
+#include "mdc_gate.h"
 #include "mdc_group.h"
 
 namespace {
 
 // ---------------------------------------------------------------------------
 // x_out[t] = sum over the token's routes of scale * (W2 q(silu(W1g q(x)) * W1u
-// q(x)) + shared), all experts of all tokens in two launches:
+// q(x)) + shared), all experts of all tokens in three launches:
 //
+//   k_moe_prep  the gate, and q(x), a workgroup each for a token
 //   k_moe_up    h = q(x) W1^T for every expert that has a token, and SwiGLU: g,
 //               fp32, into the workspace
 //   k_moe_down  q(g) W2^T times the routes' scales, summed over the experts
 //
 // With at most 32 tokens an expert's rows fill one or two blocks of the matrix
 // instruction, and what takes the time is to bring the weights of the experts in
-// use, once.  Both kernels run one workgroup of eight wavefronts per CU, each
+// use, once.  The last two kernels run one workgroup of eight wavefronts per CU, each
 // wavefront streaming weights global -> LDS directly through a ring of its own
 // (eight rows x 128 bytes per instruction, non-temporal: they are read once).
 //
@@ -47,8 +49,12 @@ constexpr int kUpRun = 8;             // most k-blocks of a wavefront
 constexpr int kCells = 256;           // rows x k-blocks of g in LDS at a time
 static_assert(kMoeRoutes <= kMoeThreads, "a thread for each route");
 
+struct MoeTable;
 struct Moe {
   const void* x;             // [T][H] bf16
+  uint8_t* q;                // [T][H] codes of x
+  float* q_scale;            // int8: [T]; fp8: [T][H / 128]
+  MoeTable* table;           // as k_moe_up worked it out, for k_moe_down
   const int32_t* ids;        // [T][K]
   const float* scales;       // [T][K]
   const uint8_t* mask;       // [T] or [T][K], or NULL
@@ -83,6 +89,22 @@ struct MoeTable {
   int64_t wave_total[kMoeWaves];
   int experts, dropped;
 };
+
+// By all threads of a workgroup; no barrier.
+__device__ __forceinline__ void table_copy(MoeTable& to, const MoeTable& from) {
+  const int i = threadIdx.x, n = from.experts;
+  if (i < n) {
+    to.expert[i] = from.expert[i];
+    to.tokens[i] = from.tokens[i];
+  }
+  if (i <= n) to.base[i] = from.base[i];
+  to.weight[i] = from.weight[i];
+  if (i < kMoeTokens) {
+    to.copy[i] = from.copy[i];
+    to.present[i] = from.present[i];
+  }
+  if (i == 0) to.experts = n;
+}
 
 // tmp: L ints of LDS, free again afterwards.
 __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
@@ -188,21 +210,78 @@ __device__ __forceinline__ unsigned moe_chunk(int lane, int odd) {
 }
 
 // ---------------------------------------------------------------------------
+// Workgroup (t, 0) quantises token t, workgroup (t, 1) routes it.
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+template <typename T, int VPL>
+__global__ __launch_bounds__(kPrepThreads) void k_moe_prep(Moe a, GateArgs gate, int int8) {
+  extern __shared__ int64_t gate_lds[];
+  __shared__ uint32_t part[kPrepThreads / 64];
+  const int tid = threadIdx.x, token = blockIdx.x;
+  if (blockIdx.y == 1) {
+    if (tid < 64) gate_token<T, 64, VPL>(gate, token, true, tid, gate_lds);
+    return;
+  }
+  const int nvec = a.H / 8;   // a multiple of 16, at most 4 a thread
+  const v4u* row = static_cast<const v4u*>(a.x) + (int64_t)token * nvec;
+  uint2* q = reinterpret_cast<uint2*>(a.q) + (int64_t)token * nvec;
+  v4u v[4];
+  uint32_t top[4], all = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) v[u] = tid + u * kPrepThreads < nvec ? row[tid + u * kPrepThreads] : v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    top[u] = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top[u] = max(top[u], max(abs_bits(bf16_lo(v[u][w])), abs_bits(bf16_hi(v[u][w]))));
+    top[u] = row16_max(top[u]);
+    all = max(all, top[u]);
+  }
+  float inv = 0.f;
+  if (int8) {
+#pragma unroll
+    for (int o = 32; o >= 16; o >>= 1) all = max(all, (uint32_t)__shfl_xor((int)all, o, 64));
+    if ((tid & 63) == 0) part[tid >> 6] = all;
+    __syncthreads();
+    all = max(max(part[0], part[1]), max(part[2], part[3]));
+    inv = int8_inverse(__uint_as_float(all));
+    if (tid == 0) a.q_scale[token] = __uint_as_float(all) / 127.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = tid + u * kPrepThreads;
+    const v4u w = v[u];
+    if (int8) {
+      if (i < nvec)
+        q[i] = uint2{int8_codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), inv),
+                     int8_codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), inv)};
+    } else if (i < nvec) {
+      const Fp8Scaler s(top[u]);
+      q[i] = uint2{s.codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])),
+                   s.codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]))};
+      if ((i & 15) == 0) a.q_scale[(int64_t)token * (nvec >> 4) + (i >> 4)] = s.scale;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 template <bool INT8, int TB>
 __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   typedef typename MoeAcc<INT8>::type Acc;
   __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kUpRing];
   __shared__ __attribute__((aligned(16))) v4f red[2][kMoeWaves * TB * 64];
   __shared__ MoeTable tab;
-  __shared__ float row_scale[kMoeTokens];   // int8: amax / 127 of the tokens
-  __shared__ float row_inv[kMoeTokens];
   static_assert(sizeof(ring_mem) >= MDC_MAX_LOCAL_EXPERTS * sizeof(int), "scratch of the table");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
   const int H = a.H, N = a.N, nk = H / kFp8Block;
   moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
+    table_copy(*a.table, tab);
+  }
   const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
   const int tiles_per = N / 16;
   const int64_t T = (int64_t)n_exp * tiles_per;
@@ -241,66 +320,26 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
     }
   };
 
-  // ---- the tokens, quantised, in the matrix instruction's layout ----
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  if (INT8) {
-    for (int t = wave; t < a.T; t += kMoeWaves) {
-      uint32_t m = 0;
-      const v4u* row = reinterpret_cast<const v4u*>(x + (int64_t)t * H);
-      for (int i = lane; i < H / 8; i += 64) {
-        const v4u v = row[i];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) m = max(m, max(abs_bits(bf16_lo(v[w])), abs_bits(bf16_hi(v[w]))));
-      }
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-      if (lane == 0) {
-        row_scale[t] = __uint_as_float(m) / 127.0f;
-        row_inv[t] = int8_inverse(__uint_as_float(m));
-      }
-    }
-    __syncthreads();
-  }
+  // ---- the tokens' codes in the matrix instruction's layout ----
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, a.T * H, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(a.q_scale, (short)0, a.T * (INT8 ? 1 : nk) * 4, 0x00020000);
   v8i tok[kUpRun][TB];
   float sa[kUpRun][TB];
 #pragma unroll
   for (int d = 0; d < kUpRun; ++d)
 #pragma unroll
     for (int m = 0; m < TB; ++m) {
-      const int t = 16 * m + r16;
-      v4u v[4] = {v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}, v4u{0u, 0u, 0u, 0u}};
-      if (d < steps && t < a.T) {
-        const v4u* p = reinterpret_cast<const v4u*>(x + (int64_t)t * H + (kb0 + d) * kFp8Block + 16 * quad);
-        v[0] = p[0];
-        v[1] = p[1];
-        v[2] = p[8];   // 64 elements on
-        v[3] = p[9];
-      }
-      if (INT8) {
-        const float inv = t < a.T ? row_inv[t] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            tok[d][m][2 * i + w] = (int)int8_codes4(bf16_lo(v[i][2 * w]), bf16_hi(v[i][2 * w]), bf16_lo(v[i][2 * w + 1]),
-                                                    bf16_hi(v[i][2 * w + 1]), inv);
-        sa[d][m] = 0.f;
-      } else {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) top = max(top, max(abs_bits(bf16_lo(v[i][w])), abs_bits(bf16_hi(v[i][w]))));
-        const Fp8Scaler s(quad_max(top));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            tok[d][m][2 * i + w] = (int)s.codes4(bf16_lo(v[i][2 * w]), bf16_hi(v[i][2 * w]), bf16_lo(v[i][2 * w + 1]),
-                                                 bf16_hi(v[i][2 * w + 1]));
-        sa[d][m] = s.scale;
-      }
+      const int t = 16 * m + r16;   // (rows past the last token read as zeros)
+      const unsigned at = d < steps ? (unsigned)(t * H + (kb0 + d) * kFp8Block + 16 * quad) : kPastEnd;
+      tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0), __builtin_amdgcn_raw_buffer_load_b128(rx, at + 64u, 0, 0));
+      if (!INT8)
+        sa[d][m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                 rs, d < steps ? (unsigned)(t * nk + kb0 + d) * 4u : kPastEnd, 0, 0));
     }
+  float row_scale = 0.f;   // int8: of token 16 (lane / 32) + r16
+  if (INT8)
+    row_scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (unsigned)(16 * (lane >> 5) + r16) * 4u, 0, 0));
   __syncthreads();   // the table's scratch is free
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
@@ -308,11 +347,11 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   const int key = (r16 >> 1) & 7;
   const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
   unsigned read = 0;
-  int j = t0 / tiles_per, c = t0 % tiles_per;
+  int j = t0 / tiles_per, c = t0 % tiles_per, e = 0;
+  float sw[2][kUpRun];   // fp8: scales of the gate and the up rows, 16 tiles' at a time
   for (int t = t0; t < t1; ++t) {
-    const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
-    float sw[2][kUpRun];   // fp8: scales of the gate and the up rows
-    if (!INT8) {
+    if (t == t0 || c == 0) e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+    if (!INT8 && (t == t0 || c % 16 == 0)) {
       const scalar_f* p = (const scalar_f*)(a.w1_scale + ((int64_t)e * (N / kFp8Block) + c / 16) * nk);
 #pragma unroll
       for (int d = 0; d < kUpRun; ++d) {
@@ -353,35 +392,34 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
     if (wave == (t & (kMoeWaves - 1)) && (TB == 2 || lane < 32)) {
       const int m = lane >> 5, half = quad & 1, token = 16 * m + r16;
       const uint32_t tokens = tab.tokens[j];
-      Acc gate = Acc{0, 0, 0, 0}, up = Acc{0, 0, 0, 0};
+      const Acc __attribute__((address_space(3)))* p =
+          (const Acc __attribute__((address_space(3)))*)(size_t)(buf + (m * 64 + half * 16 + r16) * 16);
+      Acc gate = p[0], up = p[32];
 #pragma unroll
-      for (int w = 0; w < kMoeWaves; ++w) {
-        const unsigned at = buf + ((w * TB + m) * 64 + half * 16 + r16) * 16;
-        const v8i p = lds_get2(at, at + 32 * 16);
+      for (int w = 1; w < kMoeWaves; ++w) {
+        gate += p[w * TB * 64];
+        up += p[w * TB * 64 + 32];
+      }
+      v4f hg, hu;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        hg[r] = (float)gate[r];
+        hu[r] = (float)up[r];
+      }
+      if constexpr (INT8) {
+        // the channels' scales by scalar loads: they pass by the direct loads' count
+        const scalar_f* ws = (const scalar_f*)(a.w1_scale + (int64_t)e * N + 8 * c);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if constexpr (INT8) {
-            gate[r] += p[r];
-            up[r] += p[4 + r];
-          } else {
-            gate[r] += __int_as_float(p[r]);
-            up[r] += __int_as_float(p[4 + r]);
-          }
+          hg[r] = hg[r] * row_scale * (half ? ws[4 + r] : ws[r]);
+          hu[r] = hu[r] * row_scale * (half ? ws[N / 2 + 4 + r] : ws[N / 2 + r]);
         }
       }
       if ((tokens >> token) & 1) {
         const int col = 8 * c + 4 * half;
         v4f v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float hg = (float)gate[r], hu = (float)up[r];
-          if (INT8) {
-            const float* ws = a.w1_scale + (int64_t)e * N + col + r;
-            hg = hg * row_scale[token] * ws[0];
-            hu = hu * row_scale[token] * ws[N / 2];
-          }
-          v[r] = gmm_silu(hg) * hu;
-        }
+        for (int r = 0; r < 4; ++r) v[r] = gmm_silu(hg[r]) * hu[r];
         const int rows = __popc(tokens), row = __popc(tokens & ((1u << token) - 1));
         const int64_t cell = (int64_t)tab.base[j] * (N / 256) + col / kFp8Block * rows + row;
         *reinterpret_cast<v4f*>(a.g + cell * kFp8Block + col % kFp8Block) = v;
@@ -407,13 +445,17 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   __shared__ __attribute__((aligned(16))) uint8_t cells[(kCells + 1) * kFp8Block];   // the last one: zeros
   __shared__ float cell_scale[INT8 ? 1 : kCells + 1];
   __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
+  __shared__ uint16_t cell_row[INT8 ? kCells : 1];
+  // w2's scales: fp8, of the first and of the last column of each block, a unit's; int8, of all columns, an expert's
+  __shared__ __attribute__((aligned(16))) float w_scale[kCells * NB * (INT8 ? 16 : 2)];
   __shared__ MoeTable tab;
   static_assert(sizeof(ring_mem) >= kMoeWaves * 4 * 64 * 16, "the wavefronts' sums");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
   const int H = a.H, K2 = a.N / 2, nk = K2 / kFp8Block;
-  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
+  table_copy(tab, *a.table);
+  __syncthreads();
   const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
   const int units = n_exp * nk;
   const int c0 = blockIdx.x * a.cw, cols = min(a.cw, H - c0);
@@ -443,14 +485,15 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     fu += kMoeWaves;
   };
   if (INT8) {
-    // scales of the rows, from the largest value of each of their tiles
-    const int rows = tab.base[kMoeRoutes], per = a.N / 16;
-    for (int r = wave; r < rows; r += kMoeWaves) {
+    // scales of the rows, from the largest value of each of their tiles: 16 lanes a row
+    const int rows = tab.base[n_exp], per = a.N / 16;
+    for (int r = threadIdx.x >> 4; r < rows; r += kMoeThreads / 16) {
       uint32_t m = 0;
-      for (int i = lane; i < per; i += 64) m = max(m, __float_as_uint(a.g_max[(int64_t)r * per + i]));
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-      if (lane == 0) {
+      const float* p = a.g_max + (int64_t)r * per;
+#pragma unroll 8
+      for (int i = r16; i < per; i += 16) m = max(m, __float_as_uint(p[i]));
+      m = row16_max(m);
+      if (r16 == 0) {
         row_scale[r] = __uint_as_float(m) / 127.0f;
         row_inv[r] = int8_inverse(__uint_as_float(m));
       }
@@ -458,9 +501,9 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   }
   if (threadIdx.x < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[threadIdx.x] = 0;
   if (!INT8 && threadIdx.x == 0) cell_scale[kCells] = 0.f;
-  __syncthreads();   // the table's scratch is free
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
+  lds_barrier();
 
   v4f acc[TB][NB];
 #pragma unroll
@@ -482,23 +525,31 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       u1 += take;
       used += take * rows;
     }
+    const int j0 = u0 / nk;   // first expert of the group
     if (u0 != 0) lds_barrier();   // the cells have been read
+    if (INT8) {
+      // which row a cell is of; the experts' channel scales
+      for (int u = u0 + threadIdx.x; u < u1; u += kMoeThreads) {
+        const int j = u / nk, rows = tab.base[j + 1] - tab.base[j], at = tab.base[j] * nk + (u - j * nk) * rows - first;
+        for (int r = 0; r < rows; ++r) cell_row[at + r] = (uint16_t)(tab.base[j] + r);
+      }
+      for (int i = threadIdx.x; i < ((u1 - 1) / nk - j0 + 1) * 16 * NB; i += kMoeThreads)
+        w_scale[i] = a.w2_scale[(int64_t)tab.expert[j0 + i / (16 * NB)] * H + min(c0 + i % (16 * NB), H - 1)];
+      lds_barrier();
+    } else {
+      for (int i = threadIdx.x; i < (u1 - u0) * 2 * NB; i += kMoeThreads) {
+        const int u = u0 + i / (2 * NB), n = i / 2 % NB, j = u / nk;
+        const int col = min(c0 + 16 * n + 15 * (i & 1), H - 1);
+        w_scale[i] = a.w2_scale[((int64_t)tab.expert[j] * (H / kFp8Block) + col / kFp8Block) * nk + (u - j * nk)];
+      }
+    }
     for (int i = threadIdx.x; i < used * 16; i += kMoeThreads) {
       const int cell = i >> 4, u = i & 15;
       const v4f* src = reinterpret_cast<const v4f*>(a.g + ((int64_t)first + cell) * kFp8Block) + 2 * u;
       const v4f p = src[0], q = src[1];
       uint2 code;
       if (INT8) {
-        // the row: cells run by k-block and row inside an expert
-        const int at = first + cell;
-        int lo = 0, hi = n_exp;   // base[lo] nk <= at < base[hi] nk
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (tab.base[mid] * nk <= at) lo = mid;
-          else hi = mid;
-        }
-        const int row = tab.base[lo] + (at - tab.base[lo] * nk) % (tab.base[lo + 1] - tab.base[lo]);
-        const float inv = row_inv[row];
+        const float inv = row_inv[cell_row[cell]];
         code = uint2{int8_codes4(p[0], p[1], p[2], p[3], inv), int8_codes4(q[0], q[1], q[2], q[3], inv)};
       } else {
         uint32_t top = 0;
@@ -513,7 +564,6 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     lds_barrier();
     for (; mine < u1; mine += kMoeWaves) {
       const int j = mine / nk, kb = mine - j * nk;
-      const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
       const int base = __builtin_amdgcn_readfirstlane(tab.base[j]), rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1]) - base;
       const uint32_t tokens = __builtin_amdgcn_readfirstlane((int)tab.tokens[j]);
       const int at = base * nk + kb * rows - first;   // the unit's first cell
@@ -529,19 +579,15 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
         tok[m] = lds_get2(p + ((quad ^ k) << 4), p + (((4 + quad) ^ k) << 4));
         s[m] = has[m] ? (INT8 ? row_scale[INT8 ? base + row : 0] : cell_scale[INT8 ? 0 : cell]) * tab.weight[base + row] : 0.f;
       }
-      float sw[NB][2];   // fp8: of the first and of the last column
-      v4f sc[NB];        // int8: of the lane's four columns
+      v4f sc[NB];   // int8: of the lane's four columns
+      float f[NB];  // fp8: of their block of 128
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const int col = c0 + 16 * n;
         if constexpr (INT8) {
-          const float* p = a.w2_scale + (int64_t)e * H;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sc[n][r] = p[min(col + 4 * quad + r, H - 1)];
+          sc[n] = *reinterpret_cast<const v4f*>(w_scale + ((j - j0) * NB + n) * 16 + 4 * quad);
         } else {
-          const scalar_f* p = (const scalar_f*)(a.w2_scale + (int64_t)e * (H / kFp8Block) * nk + kb);
-          sw[n][0] = p[min(col, H - 1) / kFp8Block * nk];
-          sw[n][1] = p[min(col + 15, H - 1) / kFp8Block * nk];
+          const bool same = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block;
+          f[n] = w_scale[((mine - u0) * NB + n) * 2 + (same ? 0 : 1)];
         }
       }
       __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2 * NB));
@@ -552,8 +598,6 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       fetch();
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        float f = 0.f;
-        if (!INT8) f = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block ? sw[n][0] : sw[n][1];
 #pragma unroll
         for (int m = 0; m < TB; ++m) {
           if constexpr (INT8) {
@@ -565,7 +609,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
             const v4f p = moe_mfma_fp8(w[n], tok[m]);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              acc[m][n][r] = has[m] ? __builtin_fmaf(p[r], s[m] * f, acc[m][n][r]) : acc[m][n][r];
+              acc[m][n][r] = has[m] ? __builtin_fmaf(p[r], s[m] * f[n], acc[m][n][r]) : acc[m][n][r];
           }
         }
       }
@@ -602,17 +646,20 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// Workspace: [status block][ids][scales][g][g_max].
+// Workspace: [status block][table][ids][scales][codes of x][their scales][g][g_max].
 struct MoePlan {
-  size_t off_ids, off_scales, off_g, off_max, bytes;
+  size_t off_table, off_ids, off_scales, off_q, off_q_scale, off_g, off_max, bytes;
 };
 
 MoePlan make_moe_plan(const mdc_shape* sh, int inter_n) {
-  const size_t R = (size_t)sh->bs * sh->topk, N = (size_t)inter_n;
+  const size_t T = (size_t)sh->bs, R = T * sh->topk, H = (size_t)sh->hidden, N = (size_t)inter_n;
   MoePlan p;
-  p.off_ids = MDC_STATUS_BYTES;
+  p.off_table = MDC_STATUS_BYTES;
+  p.off_ids = p.off_table + round_up(sizeof(MoeTable), 256);
   p.off_scales = p.off_ids + round_up(R * 4, 256);
-  p.off_g = p.off_scales + round_up(R * 4, 256);
+  p.off_q = p.off_scales + round_up(R * 4, 256);
+  p.off_q_scale = p.off_q + round_up(T * H, 256);
+  p.off_g = p.off_q_scale + round_up(T * (H / kFp8Block) * 4, 256);
   p.off_max = p.off_g + round_up(R * (N / 2) * 4, 256);
   p.bytes = p.off_max + round_up(R * (N / 16) * 4, 256);
   return p;
@@ -626,6 +673,23 @@ mdc_status check_moe(const mdc_shape* sh, int inter_n) {
   if (sh->bs > MDC_MAX_MOE_TOKENS || sh->hidden > kMoeWaves * kUpRun * kFp8Block) return MDC_ERR_UNSUPPORTED;
   if ((int64_t)inter_n * sh->hidden > INT32_MAX) return MDC_ERR_UNSUPPORTED;
   return MDC_OK;
+}
+
+template <typename T, int VPL>
+void launch_prep(const Moe& a, GateArgs g, bool gated, bool int8, hipStream_t s) {
+  g.vec = g.E % VPL == 0 && g.E * sizeof(T) % 16 == 0 && aligned16(g.logits) && aligned16(g.bias);
+  const size_t lds = gated && g.groups > 1 && !gate_whole_lanes(g.E / g.groups, VPL) ? lds_slots(64, VPL) * sizeof(int64_t) : 0;
+  hipLaunchKernelGGL((k_moe_prep<T, VPL>), dim3(a.T, gated ? 2 : 1), dim3(kPrepThreads), lds, s, a, g, int8 ? 1 : 0);
+}
+
+template <typename T>
+void launch_prep_typed(const Moe& a, const GateArgs& g, bool int8, hipStream_t s) {
+  if (g.E <= 64) launch_prep<T, 1>(a, g, true, int8, s);
+  else if (g.E <= 128) launch_prep<T, 2>(a, g, true, int8, s);
+  else if (g.E <= 256) launch_prep<T, 4>(a, g, true, int8, s);
+  else if (g.E <= 512) launch_prep<T, 8>(a, g, true, int8, s);
+  else if (g.E <= 1024) launch_prep<T, 16>(a, g, true, int8, s);
+  else launch_prep<T, 32>(a, g, true, int8, s);
 }
 
 template <bool INT8, int TB>
@@ -646,14 +710,9 @@ mdc_status moe_impl(const mdc_shape* shape, const mdc_gate_params* params, int32
   if (st != MDC_OK) return st;
   if ((params != nullptr) != (logits != nullptr)) return MDC_ERR_NULLPTR;
   if ((expert_ids != nullptr) != (expert_scales != nullptr)) return MDC_ERR_NULLPTR;
-  mdc_shape one = *shape;   // the tokens, once
-  one.world = 1;
-  one.rank = 0;
-  one.mask_per_route = 0;
-  if (params != nullptr) {   // its checks: with no tokens nothing is enqueued
-    mdc_shape none = one;
-    none.bs = 0;
-    const mdc_status gate = mdc_gate(&none, params, logits, bias, expert_ids, expert_scales, stream);
+  const int64_t E = (int64_t)shape->num_experts + shape->zero_experts + shape->copy_experts;
+  if (params != nullptr) {
+    const mdc_status gate = check_gate(*params, E, shape->topk);
     if (gate != MDC_OK) return gate;
   }
   if (shape->bs == 0) return MDC_OK;
@@ -664,7 +723,8 @@ mdc_status moe_impl(const mdc_shape* shape, const mdc_gate_params* params, int32
     return MDC_ERR_NULLPTR;
   if (!aligned16(x) || !aligned16(w1) || !aligned4(w1_scale) || !aligned16(w2) || !aligned4(w2_scale) ||
       !aligned16(shared_expert_x) || !aligned16(ori_x) || !aligned16(x_out) || !aligned16(workspace) ||
-      !aligned4(expert_ids) || !aligned4(expert_scales))
+      !aligned4(expert_ids) || !aligned4(expert_scales) || !aligned4(bias) ||
+      (params != nullptr && reinterpret_cast<uintptr_t>(logits) % (params->dtype == MDC_DTYPE_FP32 ? 4 : 2) != 0))
     return MDC_ERR_INVALID;
   if (workspace_bytes < p.bytes) return MDC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -673,21 +733,27 @@ mdc_status moe_impl(const mdc_shape* shape, const mdc_gate_params* params, int32
     expert_scales = reinterpret_cast<float*>(ws + p.off_scales);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (params != nullptr) {
-    const mdc_status gate = mdc_gate(&one, params, logits, bias, expert_ids, expert_scales, stream);
-    if (gate != MDC_OK) return gate;
-  }
   (void)hipGetLastError();
   const unsigned cus = device_cus();
   const int L = shape->num_experts / shape->world;
   const int cw = min(32, max(4, (int)round_up((shape->hidden + cus - 1) / cus, 4)));
-  const Moe a{x, expert_ids, expert_scales, x_active_mask, static_cast<const uint8_t*>(w1), w1_scale,
+  const Moe a{x, reinterpret_cast<uint8_t*>(ws + p.off_q), reinterpret_cast<float*>(ws + p.off_q_scale),
+              reinterpret_cast<MoeTable*>(ws + p.off_table), expert_ids, expert_scales, x_active_mask, static_cast<const uint8_t*>(w1), w1_scale,
               static_cast<const uint8_t*>(w2), w2_scale, static_cast<const uint16_t*>(shared_expert_x),
               static_cast<const uint16_t*>(ori_x), static_cast<uint16_t*>(x_out), reinterpret_cast<float*>(ws + p.off_g),
               reinterpret_cast<float*>(ws + p.off_max), reinterpret_cast<mdc_device_status*>(ws), shape->bs, shape->topk,
               shape->hidden, inter_n, L, shape->rank * L, shape->num_experts,
               shape->num_experts + shape->zero_experts, shape->num_experts + shape->zero_experts + shape->copy_experts,
               shape->mask_per_route, cw};
+  if (params != nullptr) {
+    const GateArgs g{logits, bias, expert_ids, expert_scales, a.T, (int)E, a.K, params->groups, params->topk_groups,
+                     params->group_top, params->score == MDC_GATE_SIGMOID, params->renormalise, params->scale, 0};
+    if (params->dtype == MDC_DTYPE_BF16) launch_prep_typed<uint16_t>(a, g, INT8, s);
+    else if (params->dtype == MDC_DTYPE_FP16) launch_prep_typed<_Float16>(a, g, INT8, s);
+    else launch_prep_typed<float>(a, g, INT8, s);
+  } else {
+    launch_prep<float, 1>(a, GateArgs{}, false, INT8, s);
+  }
   if (a.T <= 16) launch_moe<INT8, 1>(a, cus, s);
   else launch_moe<INT8, 2>(a, cus, s);
   return launched();
