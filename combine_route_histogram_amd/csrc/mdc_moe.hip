@@ -47,6 +47,7 @@ constexpr int kUpRing = 12288;        // bytes of a wavefront's ring
 constexpr int kDownRing = 8192;
 constexpr int kUpRun = 8;             // most k-blocks of a wavefront
 constexpr int kCells = 256;           // rows x k-blocks of g in LDS at a time
+constexpr int kGroupExperts = 64;     // int8: and experts' channel scales
 static_assert(kMoeRoutes <= kMoeThreads, "a thread for each route");
 
 struct MoeTable;
@@ -90,24 +91,34 @@ struct MoeTable {
   int experts, dropped;
 };
 
-// By all threads of a workgroup; no barrier.
-__device__ __forceinline__ void table_copy(MoeTable& to, const MoeTable& from) {
-  const int i = threadIdx.x, n = from.experts;
-  if (i < n) {
-    to.expert[i] = from.expert[i];
-    to.tokens[i] = from.tokens[i];
+// By all threads of a workgroup, the entries of R routes; no barrier.
+__device__ __forceinline__ void table_copy(MoeTable& to, const MoeTable& from, int R) {
+  const int i = threadIdx.x;
+  if (i < R) {
+    const uint16_t e = from.expert[i];
+    const uint32_t t = from.tokens[i];
+    const int b = from.base[i + 1];
+    const float w = from.weight[i];
+    to.expert[i] = e;
+    to.tokens[i] = t;
+    to.base[i + 1] = b;
+    to.weight[i] = w;
   }
-  if (i <= n) to.base[i] = from.base[i];
-  to.weight[i] = from.weight[i];
   if (i < kMoeTokens) {
-    to.copy[i] = from.copy[i];
-    to.present[i] = from.present[i];
+    const float c = from.copy[i], p = from.present[i];
+    to.copy[i] = c;
+    to.present[i] = p;
   }
-  if (i == 0) to.experts = n;
+  if (i == 0) {
+    to.base[0] = 0;
+    to.experts = from.experts;
+  }
 }
 
 // tmp: L ints of LDS, free again afterwards.
 __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
+  __shared__ int ids[kMoeRoutes];        // -1: not present
+  __shared__ float scales[kMoeRoutes];
   const int i = threadIdx.x, R = a.T * a.K;
   const int token = i / a.K;
   int id = -1;
@@ -122,12 +133,13 @@ __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
   const int e = id - a.first;
   const bool mine = present && id < a.E && e >= 0 && e < a.L;
   for (int k = i; k < a.L; k += kMoeThreads) tmp[k] = INT32_MAX;
-  if (i < kMoeTokens) t.copy[i] = t.present[i] = 0.f;
   if (i == 0) t.dropped = 0;
   t.tokens[i] = 0;
+  ids[i] = present ? id : -1;
+  scales[i] = scale;
   __syncthreads();
   if (mine) atomicMin(&tmp[e], i);
-  if (live && i < R && !present) atomicAdd(&t.dropped, 1);
+  if (live && !present) atomicAdd(&t.dropped, 1);
   __syncthreads();
   // place of the expert of each first route
   const bool first = mine && tmp[e] == i;
@@ -152,16 +164,15 @@ __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
     float sum = 0.f, copy = 0.f, all = 0.f;
     bool lead = mine;
     const int r0 = token * a.K;
+#pragma unroll 4
     for (int r = r0; r < r0 + a.K; ++r) {
-      const int other = a.ids[r];
-      const bool on = (a.mask == nullptr || a.mask[a.per_route ? r : token] != 0) && other >= 0 && other < a.all;
-      const float s = on ? a.scales[r] : 0.f;
-      if (on && other == id) {
-        sum += s;
-        lead = lead && r >= i;
-      }
-      if (on && other >= a.EZ) copy += s;
-      if (on) all += s;
+      const int other = ids[r];
+      const float s = other >= 0 ? scales[r] : 0.f;
+      const bool same = other >= 0 && other == id;
+      sum += same ? s : 0.f;
+      lead = lead && !(same && r < i);
+      copy += other >= a.EZ ? s : 0.f;
+      all += s;
     }
     if (lead) t.weight[t.base[j] + __popc(t.tokens[j] & ((1u << token) - 1))] = sum;
     if (i == r0) {
@@ -277,49 +288,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
   const int H = a.H, N = a.N, nk = H / kFp8Block;
-  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
-    table_copy(*a.table, tab);
-  }
-  const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
-  const int tiles_per = N / 16;
-  const int64_t T = (int64_t)n_exp * tiles_per;
-  const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
-  if (t0 == t1) return;
-
-  // ---- weights ----
-  const int kb0 = wave * nk / kMoeWaves, steps = (wave + 1) * nk / kMoeWaves - kb0;
-  constexpr int kSlot = 2048, kSlots = kUpRing / kSlot;
-  const unsigned ring = lds_at(ring_mem) + wave * kUpRing;
-  auto weights = [&](int j) {
-    const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w1 + (int64_t)e * N * H), (short)0, N * H, 0x00020000);
-  };
-  struct {
-    int j, c, step, left;   // expert's place, tile of it, step, tiles to come
-  } f = {t0 / tiles_per, t0 % tiles_per, 0, steps > 0 ? t1 - t0 : 0};
-  __amdgpu_buffer_rsrc_t rw = weights(f.j);
-  unsigned slot = 0;
-  auto fetch = [&]() {
-    const unsigned k0 = (unsigned)(kb0 + f.step) * kFp8Block;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const unsigned row = (unsigned)(8 * f.c + (lane >> 3) + h * (N / 2));
-      const unsigned at = f.left > 0 ? row * (unsigned)H + k0 + moe_chunk(lane, h) : kPastEnd;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, at, 0, 0, kMoeNt);
-    }
-    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
-    if (++f.step >= steps) {
-      f.step = 0;
-      --f.left;
-      if (++f.c == tiles_per) {
-        f.c = 0;
-        if (f.left > 0) rw = weights(++f.j);
-      }
-    }
-  };
-
+  const int kb0 = wave * nk / kMoeWaves, steps = (wave + 1) * nk / kMoeWaves - kb0;   // this wavefront's k-blocks
   // ---- the tokens' codes in the matrix instruction's layout ----
   const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, a.T * H, 0x00020000);
   const __amdgpu_buffer_rsrc_t rs =
@@ -340,6 +309,54 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   float row_scale = 0.f;   // int8: of token 16 (lane / 32) + r16
   if (INT8)
     row_scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (unsigned)(16 * (lane >> 5) + r16) * 4u, 0, 0));
+  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
+    table_copy(*a.table, tab, a.T * a.K);
+  }
+  const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
+  const int tiles_per = N / 16;
+  const int64_t T = (int64_t)n_exp * tiles_per;
+  const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
+  if (t0 == t1) return;
+
+  // ---- weights ----
+  constexpr int kSlot = 2048, kSlots = kUpRing / kSlot;
+  const unsigned ring = lds_at(ring_mem) + wave * kUpRing;
+  auto weights = [&](int j) {
+    const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w1 + (int64_t)e * N * H), (short)0, N * H, 0x00020000);
+  };
+  struct {
+    int j, c, step, left;   // expert's place, tile of it, step, tiles to come
+  } f = {t0 / tiles_per, t0 % tiles_per, 0, steps > 0 ? t1 - t0 : 0};
+  const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, 0, 0x00020000);   // reads as zeros
+  __amdgpu_buffer_rsrc_t rw = f.left > 0 ? weights(f.j) : none;
+  unsigned slot = 0, so = (unsigned)kb0 * kFp8Block;
+  // lane parts of the two loads: rows 8 c + lane / 8 of the gate's and of the up's columns
+  unsigned v0 = (unsigned)(8 * f.c + (lane >> 3)) * (unsigned)H + moe_chunk(lane, 0);
+  unsigned v1 = (unsigned)(8 * f.c + (lane >> 3) + N / 2) * (unsigned)H + moe_chunk(lane, 1);
+  auto fetch = [&]() {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot), 16, v0, so, 0, kMoeNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + 1024), 16, v1, so, 0, kMoeNt);
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    so += kFp8Block;
+    if (++f.step >= steps) {
+      f.step = 0;
+      so = (unsigned)kb0 * kFp8Block;
+      v0 += 8u * (unsigned)H;
+      v1 += 8u * (unsigned)H;
+      const bool more = --f.left > 0;
+      if (++f.c == tiles_per) {
+        f.c = 0;
+        v0 -= (unsigned)(N / 2) * (unsigned)H;
+        v1 -= (unsigned)(N / 2) * (unsigned)H;
+        if (more) rw = weights(++f.j);
+      }
+      if (!more) rw = none;
+    }
+  };
+
   __syncthreads();   // the table's scratch is free
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
@@ -348,7 +365,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
   unsigned read = 0;
   int j = t0 / tiles_per, c = t0 % tiles_per, e = 0;
-  float sw[2][kUpRun];   // fp8: scales of the gate and the up rows, 16 tiles' at a time
+  float sc[kUpRun][TB];   // fp8: scales of the tokens times those of the lane's rows, the same for 16 tiles
   for (int t = t0; t < t1; ++t) {
     if (t == t0 || c == 0) e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
     if (!INT8 && (t == t0 || c % 16 == 0)) {
@@ -356,8 +373,10 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
 #pragma unroll
       for (int d = 0; d < kUpRun; ++d) {
         const int b = min(kb0 + d, nk - 1);
-        sw[0][d] = p[b];
-        sw[1][d] = p[(int64_t)(N / 256) * nk + b];
+        const float gate = p[b], up = p[(int64_t)(N / 256) * nk + b];
+        const float s = quad < 2 ? gate : up;
+#pragma unroll
+        for (int m = 0; m < TB; ++m) sc[d][m] = sa[d][m] * s;
       }
     }
     Acc acc[TB];
@@ -374,12 +393,11 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
 #pragma unroll
           for (int m = 0; m < TB; ++m) acc[m] = moe_mfma_int8(w, tok[d][m], acc[m]);
         } else {
-          const float s = quad < 2 ? sw[0][d] : sw[1][d];
 #pragma unroll
           for (int m = 0; m < TB; ++m) {
             const v4f p = moe_mfma_fp8(w, tok[d][m]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(p[r], sa[d][m] * s, acc[m][r]);
+            for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(p[r], sc[d][m], acc[m][r]);
           }
         }
       }
@@ -439,71 +457,182 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
 }
 
 // ---------------------------------------------------------------------------
+typedef const __attribute__((address_space(3))) v4i lds_v4i;
+
+struct MoeGroup {
+  int u0, u1, first, used;   // units, first cell, cells
+};
+
+// A unit's operands besides the weights.
+template <int TB, int NB>
+struct MoeUnit {
+  v8i tok[TB];
+  float s[TB];
+  bool has[TB];   // (the others' sums stay: what an expert holds may be infinite or NaN)
+  v4f sc[NB];     // int8: scales of the lane's four columns; fp8: [0], of their block of 128
+};
+
 template <bool INT8, int TB, int NB>
 __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kDownRing];
   __shared__ __attribute__((aligned(16))) uint8_t cells[(kCells + 1) * kFp8Block];   // the last one: zeros
-  __shared__ float cell_scale[INT8 ? 1 : kCells + 1];
-  __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
-  __shared__ uint16_t cell_row[INT8 ? kCells : 1];
+  __shared__ float cell_scale[kCells + 1];   // of its values, times its row's route scale
+  __shared__ uint16_t cell_row[kCells];
+  __shared__ int4 unit_info[kCells];         // first cell; tokens; place of w2's scales
   // w2's scales: fp8, of the first and of the last column of each block, a unit's; int8, of all columns, an expert's
-  __shared__ __attribute__((aligned(16))) float w_scale[kCells * NB * (INT8 ? 16 : 2)];
+  __shared__ __attribute__((aligned(16))) float w_scale[INT8 ? kGroupExperts * NB * 16 : kCells * NB * 2];
+  __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
   __shared__ MoeTable tab;
   static_assert(sizeof(ring_mem) >= kMoeWaves * 4 * 64 * 16, "the wavefronts' sums");
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
-  const int H = a.H, K2 = a.N / 2, nk = K2 / kFp8Block;
-  table_copy(tab, *a.table);
+  const int H = a.H, K2 = a.N / 2, nk = K2 / kFp8Block, R = a.T * a.K;
+  const int c0 = blockIdx.x * a.cw, cols = min(a.cw, H - c0);
+
+  // ---- what the units' groups need of memory, in registers ----
+  constexpr int kPasses = kCells * 16 / kMoeThreads;   // 16 lanes x 8 values a cell
+  constexpr int kScales = (int)(sizeof(w_scale) / sizeof(float)) / kMoeThreads;
+  v4f ga[kPasses], gb[kPasses];
+  float gs[kScales];
+  auto load_cells = [&](int first, int n) {   // n cells, all of which are inside g
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int cell = (tid + p * kMoeThreads) >> 4;
+      const v4f* src = reinterpret_cast<const v4f*>(a.g + ((int64_t)first + min(cell, n - 1)) * kFp8Block) + 2 * (tid & 15);
+      ga[p] = src[0];
+      gb[p] = src[1];
+    }
+  };
+  // largest values of 32 rows' tiles (int8), 16 lanes a row
+  auto row_top = [&](int r) {
+    uint32_t m = 0;
+    const int per = a.N / 16;
+    const float* p = a.g_max + (int64_t)min(r, R - 1) * per;
+#pragma unroll 8
+    for (int i = r16; i < per; i += 16) m = max(m, __float_as_uint(p[i]));
+    m = row16_max(m);
+    if (r16 == 0 && r < kMoeRoutes) {
+      row_scale[r] = __uint_as_float(m) / 127.0f;
+      row_inv[r] = int8_inverse(__uint_as_float(m));
+    }
+  };
+  // (the first cells and rows before it is known how many there are: the workspace has room for every route's)
+  load_cells(0, (int)min((int64_t)R * nk, (int64_t)kCells));
+  table_copy(tab, *a.table, R);
+  if (INT8) row_top(tid >> 4);
+  if (tid < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[tid] = 0;
+  if (tid == 0) cell_scale[kCells] = 0.f;
   __syncthreads();
   const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
   const int units = n_exp * nk;
-  const int c0 = blockIdx.x * a.cw, cols = min(a.cw, H - c0);
 
   // ---- weights: units wave, wave + 8, ... ----
   constexpr int kSlot = NB * 2048, kSlots = kDownRing / kSlot;
   const unsigned ring = lds_at(ring_mem) + wave * kDownRing;
-  int fu = wave, fj = -1;
-  __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w2), (short)0, 0, 0x00020000);
-  unsigned slot = 0;
-  auto fetch = [&]() {
-    const bool in = fu < units;
-    const int j = in ? fu / nk : 0;
-    if (in && j != fj) {
-      const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[j]);
-      rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w2 + ((int64_t)e * H + c0) * K2), (short)0, cols * K2,
-                                             0x00020000);
-      fj = j;
-    }
-    const unsigned k0 = (unsigned)(fu - j * nk) * kFp8Block;
+  const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, 0, 0x00020000);   // reads as zeros
+  __amdgpu_buffer_rsrc_t rw = none;
+  int fj = wave / nk, fk = wave - fj * nk;   // expert's place and k-block of the next unit to be loaded
+  bool turn = true;                          // another expert than the last one
+  unsigned slot = 0, vo[4];   // (2 NB of them)
 #pragma unroll
-    for (int h = 0; h < 2 * NB; ++h) {
-      const unsigned at = in ? (unsigned)(8 * h + (lane >> 3)) * (unsigned)K2 + k0 + moe_chunk(lane, h & 1) : kPastEnd;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, at, 0, 0, kMoeNt);
-    }
-    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
-    fu += kMoeWaves;
-  };
-  if (INT8) {
-    // scales of the rows, from the largest value of each of their tiles: 16 lanes a row
-    const int rows = tab.base[n_exp], per = a.N / 16;
-    for (int r = threadIdx.x >> 4; r < rows; r += kMoeThreads / 16) {
-      uint32_t m = 0;
-      const float* p = a.g_max + (int64_t)r * per;
-#pragma unroll 8
-      for (int i = r16; i < per; i += 16) m = max(m, __float_as_uint(p[i]));
-      m = row16_max(m);
-      if (r16 == 0) {
-        row_scale[r] = __uint_as_float(m) / 127.0f;
-        row_inv[r] = int8_inverse(__uint_as_float(m));
+  for (int h = 0; h < 2 * NB; ++h) vo[h] = (unsigned)(8 * h + (lane >> 3)) * (unsigned)K2 + moe_chunk(lane, h & 1);
+  auto fetch = [&]() {
+    if (turn) {
+      rw = none;
+      if (fj < n_exp) {
+        const int e = __builtin_amdgcn_readfirstlane((int)tab.expert[fj]);
+        rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.w2 + ((int64_t)e * H + c0) * K2), (short)0, cols * K2,
+                                               0x00020000);
       }
     }
-  }
-  if (threadIdx.x < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[threadIdx.x] = 0;
-  if (!INT8 && threadIdx.x == 0) cell_scale[kCells] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2 * NB; ++h)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, vo[h],
+                                               (unsigned)fk * kFp8Block, 0, kMoeNt);
+    slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
+    fk += kMoeWaves;
+    turn = fk >= nk;
+    while (fk >= nk) {
+      fk -= nk;
+      ++fj;
+    }
+  };
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
-  lds_barrier();
+  if (INT8)
+    for (int r = 32 + (tid >> 4); r < tab.base[n_exp]; r += 32) row_top(r);
+
+  // ---- groups: as many units as the cells hold rows of ----
+  MoeGroup g = {0, 0, 0, 0};
+  auto next_group = [&]() {
+    g.u0 = g.u1;
+    g.first += g.used;
+    g.used = 0;
+    const int j0 = g.u0 / nk;
+    while (g.u1 < units) {
+      const int j = g.u1 / nk, rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1] - tab.base[j]);
+      const int take = INT8 && j - j0 == kGroupExperts ? 0 : min((j + 1) * nk - g.u1, (kCells - g.used) / rows);
+      if (take == 0) break;
+      g.u1 += take;
+      g.used += take * rows;
+    }
+  };
+  auto load_scales = [&]() {
+    const int j0 = g.u0 / nk;
+#pragma unroll
+    for (int p = 0; p < kScales; ++p) {
+      const int i = tid + p * kMoeThreads;
+      int64_t at;
+      if (INT8) {
+        const int j = min(j0 + i / (16 * NB), (g.u1 - 1) / nk);
+        at = (int64_t)tab.expert[j] * H + min(c0 + i % (16 * NB), H - 1);
+      } else {
+        const int u = min(g.u0 + i / (2 * NB), g.u1 - 1), n = i / 2 % NB, j = u / nk;
+        const int col = min(c0 + 16 * n + 15 * (i & 1), H - 1);
+        at = ((int64_t)tab.expert[j] * (H / kFp8Block) + col / kFp8Block) * nk + (u - j * nk);
+      }
+      gs[p] = a.w2_scale[at];
+    }
+  };
+  // the group's cells, scales and units into LDS
+  auto place_units = [&]() {
+    const int j0 = g.u0 / nk;
+    for (int u = g.u0 + tid; u < g.u1; u += kMoeThreads) {
+      const int j = u / nk, base = tab.base[j], rows = tab.base[j + 1] - base;
+      const int at = base * nk + (u - j * nk) * rows - g.first;
+      unit_info[u - g.u0] = int4{at, (int)tab.tokens[j], INT8 ? (j - j0) * NB * 16 : (u - g.u0) * NB * 2, 0};
+      for (int r = 0; r < rows; ++r) cell_row[at + r] = (uint16_t)(base + r);
+    }
+#pragma unroll
+    for (int p = 0; p < kScales; ++p) w_scale[tid + p * kMoeThreads] = gs[p];
+  };
+  auto place_cells = [&]() {
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int cell = (tid + p * kMoeThreads) >> 4, u = tid & 15;
+      if (cell < g.used) {
+        const v4f x = ga[p], y = gb[p];
+        const int row = cell_row[cell];
+        uint2 code;
+        float scale;
+        if (INT8) {
+          const float inv = row_inv[INT8 ? row : 0];
+          code = uint2{int8_codes4(x[0], x[1], x[2], x[3], inv), int8_codes4(y[0], y[1], y[2], y[3], inv)};
+          scale = row_scale[INT8 ? row : 0];
+        } else {
+          uint32_t top = 0;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = max(top, max(abs_bits(x[r]), abs_bits(y[r])));
+          const Fp8Scaler s(row16_max(top));
+          code = uint2{s.codes4(x[0], x[1], x[2], x[3]), s.codes4(y[0], y[1], y[2], y[3])};
+          scale = s.scale;
+        }
+        if (u == 0) cell_scale[cell] = scale * tab.weight[row];
+        *reinterpret_cast<uint2*>(cells + cell * kFp8Block + (((u >> 1) ^ ((cell >> 1) & 7)) << 4) + (u & 1) * 8) = code;
+      }
+    }
+  };
 
   v4f acc[TB][NB];
 #pragma unroll
@@ -513,83 +642,52 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   const int key = (r16 >> 1) & 7;
   const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
   const unsigned cell0 = lds_at(cells);
-  unsigned read = 0;
-  int u0 = 0, first = 0, mine = wave;   // group: first unit, its first cell; this wavefront's next unit
-  while (u0 < units) {
-    // the units whose rows fit
-    int u1 = u0, used = 0;
-    while (u1 < units) {
-      const int j = u1 / nk, rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1] - tab.base[j]);
-      const int take = min((j + 1) * nk - u1, (kCells - used) / rows);
-      if (take == 0) break;
-      u1 += take;
-      used += take * rows;
+  auto load_unit = [&](int u, MoeUnit<TB, NB>& x) {
+    const int4 info = unit_info[u - g.u0];
+    const uint32_t tokens = (uint32_t)info.y;
+#pragma unroll
+    for (int m = 0; m < TB; ++m) {
+      const int token = 16 * m + r16;
+      x.has[m] = (tokens >> token) & 1;
+      const int cell = x.has[m] ? info.x + __popc(tokens & ((1u << token) - 1)) : kCells, k = (cell >> 1) & 7;
+      const unsigned p = cell0 + cell * kFp8Block;
+      x.tok[m] = join(*(lds_v4i*)(size_t)(p + ((quad ^ k) << 4)), *(lds_v4i*)(size_t)(p + (((4 + quad) ^ k) << 4)));
+      x.s[m] = cell_scale[cell];
     }
-    const int j0 = u0 / nk;   // first expert of the group
-    if (u0 != 0) lds_barrier();   // the cells have been read
-    if (INT8) {
-      // which row a cell is of; the experts' channel scales
-      for (int u = u0 + threadIdx.x; u < u1; u += kMoeThreads) {
-        const int j = u / nk, rows = tab.base[j + 1] - tab.base[j], at = tab.base[j] * nk + (u - j * nk) * rows - first;
-        for (int r = 0; r < rows; ++r) cell_row[at + r] = (uint16_t)(tab.base[j] + r);
-      }
-      for (int i = threadIdx.x; i < ((u1 - 1) / nk - j0 + 1) * 16 * NB; i += kMoeThreads)
-        w_scale[i] = a.w2_scale[(int64_t)tab.expert[j0 + i / (16 * NB)] * H + min(c0 + i % (16 * NB), H - 1)];
-      lds_barrier();
-    } else {
-      for (int i = threadIdx.x; i < (u1 - u0) * 2 * NB; i += kMoeThreads) {
-        const int u = u0 + i / (2 * NB), n = i / 2 % NB, j = u / nk;
-        const int col = min(c0 + 16 * n + 15 * (i & 1), H - 1);
-        w_scale[i] = a.w2_scale[((int64_t)tab.expert[j] * (H / kFp8Block) + col / kFp8Block) * nk + (u - j * nk)];
-      }
-    }
-    for (int i = threadIdx.x; i < used * 16; i += kMoeThreads) {
-      const int cell = i >> 4, u = i & 15;
-      const v4f* src = reinterpret_cast<const v4f*>(a.g + ((int64_t)first + cell) * kFp8Block) + 2 * u;
-      const v4f p = src[0], q = src[1];
-      uint2 code;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
       if (INT8) {
-        const float inv = row_inv[cell_row[cell]];
-        code = uint2{int8_codes4(p[0], p[1], p[2], p[3], inv), int8_codes4(q[0], q[1], q[2], q[3], inv)};
+        x.sc[n] = *reinterpret_cast<const v4f*>(w_scale + info.z + n * 16 + 4 * quad);
       } else {
-        uint32_t top = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) top = max(top, max(abs_bits(p[r]), abs_bits(q[r])));
-        const Fp8Scaler s(row16_max(top));
-        code = uint2{s.codes4(p[0], p[1], p[2], p[3]), s.codes4(q[0], q[1], q[2], q[3])};
-        if (u == 0) cell_scale[cell] = s.scale;
+        const bool same = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block;
+        x.sc[n][0] = w_scale[info.z + n * 2 + (same ? 0 : 1)];
       }
-      *reinterpret_cast<uint2*>(cells + cell * kFp8Block + (((u >> 1) ^ ((cell >> 1) & 7)) << 4) + (u & 1) * 8) = code;
     }
+  };
+  unsigned read = 0;
+  int mine = wave;   // this wavefront's next unit
+  next_group();
+  if (units != 0) {
+    load_scales();
+    lds_barrier();   // the rows' scales are there
+  }
+  while (g.u0 < units) {
+    place_units();
     lds_barrier();
-    for (; mine < u1; mine += kMoeWaves) {
-      const int j = mine / nk, kb = mine - j * nk;
-      const int base = __builtin_amdgcn_readfirstlane(tab.base[j]), rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1]) - base;
-      const uint32_t tokens = __builtin_amdgcn_readfirstlane((int)tab.tokens[j]);
-      const int at = base * nk + kb * rows - first;   // the unit's first cell
-      v8i tok[TB];
-      float s[TB];
-      bool has[TB];   // (the others' sums stay: what an expert holds may be infinite or NaN)
-#pragma unroll
-      for (int m = 0; m < TB; ++m) {
-        const int token = 16 * m + r16, row = __popc(tokens & ((1u << token) - 1));
-        has[m] = (tokens >> token) & 1;
-        const int cell = has[m] ? at + row : kCells, k = (cell >> 1) & 7;
-        const unsigned p = cell0 + cell * kFp8Block;
-        tok[m] = lds_get2(p + ((quad ^ k) << 4), p + (((4 + quad) ^ k) << 4));
-        s[m] = has[m] ? (INT8 ? row_scale[INT8 ? base + row : 0] : cell_scale[INT8 ? 0 : cell]) * tab.weight[base + row] : 0.f;
-      }
-      v4f sc[NB];   // int8: of the lane's four columns
-      float f[NB];  // fp8: of their block of 128
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if constexpr (INT8) {
-          sc[n] = *reinterpret_cast<const v4f*>(w_scale + ((j - j0) * NB + n) * 16 + 4 * quad);
-        } else {
-          const bool same = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block;
-          f[n] = w_scale[((mine - u0) * NB + n) * 2 + (same ? 0 : 1)];
-        }
-      }
+    place_cells();
+    lds_barrier();
+    const MoeGroup cur = g;
+    next_group();
+    if (g.u0 < units) {   // the next group's, on their way while this one's units are multiplied
+      load_cells(g.first, g.used);
+      load_scales();
+    }
+    const MoeGroup ahead = g;
+    g = cur;
+    MoeUnit<TB, NB> now, next;
+    if (mine < g.u1) load_unit(mine, now);
+    for (; mine < g.u1; mine += kMoeWaves) {
+      if (mine + kMoeWaves < g.u1) load_unit(mine + kMoeWaves, next);
       __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2 * NB));
       v8i w[NB];
 #pragma unroll
@@ -597,25 +695,25 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
       fetch();
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int m = 0; m < TB; ++m) {
           if constexpr (INT8) {
-            const v4i p = moe_mfma_int8(w[n], tok[m], v4i{0, 0, 0, 0});
+            const v4i p = moe_mfma_int8(w[n], now.tok[m], v4i{0, 0, 0, 0});
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              acc[m][n][r] = has[m] ? __builtin_fmaf((float)p[r], s[m] * sc[n][r], acc[m][n][r]) : acc[m][n][r];
+              acc[m][n][r] = now.has[m] ? __builtin_fmaf((float)p[r], now.s[m] * now.sc[n][r], acc[m][n][r]) : acc[m][n][r];
           } else {
-            const v4f p = moe_mfma_fp8(w[n], tok[m]);
+            const v4f p = moe_mfma_fp8(w[n], now.tok[m]);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              acc[m][n][r] = has[m] ? __builtin_fmaf(p[r], s[m] * f[n], acc[m][n][r]) : acc[m][n][r];
+              acc[m][n][r] = now.has[m] ? __builtin_fmaf(p[r], now.s[m] * now.sc[n][0], acc[m][n][r]) : acc[m][n][r];
           }
         }
-      }
+      now = next;
     }
-    first += used;
-    u0 = u1;
+    g = ahead;
+    lds_barrier();   // the cells have been read
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
   __syncthreads();
@@ -628,7 +726,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     for (int n = 0; n < NB; ++n) lds_put(sums + ((wave * TB + m) * NB + n) * 1024 + lane * 16, acc[m][n]);
   __syncthreads();
   const float* part = reinterpret_cast<const float*>(ring_mem);
-  for (int i = threadIdx.x; i < 16 * NB * a.T; i += kMoeThreads) {
+  for (int i = tid; i < 16 * NB * a.T; i += kMoeThreads) {
     const int token = i / (16 * NB), cc = i - token * 16 * NB, col = c0 + cc;
     if (cc >= cols) continue;
     const int m = token >> 4, n = cc >> 4;
