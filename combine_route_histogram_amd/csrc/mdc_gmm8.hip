@@ -197,8 +197,8 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
         v4f sw;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float a0 = p[min(col0 + r, Nw - 1)], a1 = p[min(col0 + 4 + r, Nw - 1)];
-          const float a2 = p[min(col0 + 8 + r, Nw - 1)], a3 = p[min(col0 + 12 + r, Nw - 1)];
+          const float a0 = scalar(p[min(col0 + r, Nw - 1)]), a1 = scalar(p[min(col0 + 4 + r, Nw - 1)]);
+          const float a2 = scalar(p[min(col0 + 8 + r, Nw - 1)]), a3 = scalar(p[min(col0 + 12 + r, Nw - 1)]);
           sw[r] = quad < 2 ? (quad == 0 ? a0 : a1) : (quad == 2 ? a2 : a3);
         }
         if (row < rows && col < Nw) gmm8_store(g, (int64_t)(row0 + row) * Nw + col, gmm8_scale(sum, m == 0 ? sa[0] : sa[1], sw));

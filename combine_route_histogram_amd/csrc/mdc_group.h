@@ -16,6 +16,10 @@ typedef __bf16 v4b __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(4))) float scalar_f;   // read by scalar loads
 
+// A value that all lanes share, in a scalar register (a choice between two of them
+// does not become a vector load of the one chosen).
+__device__ __forceinline__ float scalar(float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); }
+
 __device__ __forceinline__ v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
 
 __device__ __forceinline__ float gmm_silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }

@@ -44,7 +44,7 @@ constexpr int kMoeTokens = MDC_MAX_MOE_TOKENS;
 constexpr int kMoeRoutes = kMoeTokens * MDC_MAX_TOPK;
 constexpr int kMoeNt = 2;             // cache policy of the weights' loads: non-temporal
 constexpr int kUpRing = 12288;        // bytes of a wavefront's ring
-constexpr int kDownRing = 8192;
+constexpr int kDownRing = 12288;
 constexpr int kUpRun = 8;             // most k-blocks of a wavefront
 constexpr int kCells = 256;           // rows x k-blocks of g in LDS at a time
 constexpr int kGroupExperts = 64;     // int8: and experts' channel scales
@@ -53,8 +53,8 @@ static_assert(kMoeRoutes <= kMoeThreads, "a thread for each route");
 struct MoeTable;
 struct Moe {
   const void* x;             // [T][H] bf16
-  uint8_t* q;                // [T][H] codes of x
-  float* q_scale;            // int8: [T]; fp8: [T][H / 128]
+  uint8_t* q;                // codes of x as k_moe_up loads them: moe_code
+  float* q_scale;            // int8: [T]; fp8: [H / 128][kMoeTokens]
   MoeTable* table;           // as k_moe_up worked it out, for k_moe_down
   const int32_t* ids;        // [T][K]
   const float* scales;       // [T][K]
@@ -225,6 +225,13 @@ __device__ __forceinline__ unsigned moe_chunk(int lane, int odd) {
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 
+// Place of chunk c (16 codes) of a token's k-block: k-block, token block, half of
+// the chunks, then lane 16 (c % 4) + token % 16 of the matrix instruction, so that
+// a load of a fragment is a kilobyte at once.
+__device__ __forceinline__ int moe_code(int blocks, int kb, int token, int c) {
+  return ((kb * blocks + (token >> 4)) * 2 + (c >> 2)) * 1024 + ((c & 3) * 16 + (token & 15)) * 16;
+}
+
 template <typename T, int VPL>
 __global__ __launch_bounds__(kPrepThreads) void k_moe_prep(Moe a, GateArgs gate, int int8) {
   extern __shared__ int64_t gate_lds[];
@@ -236,7 +243,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_moe_prep(Moe a, GateArgs gate,
   }
   const int nvec = a.H / 8;   // a multiple of 16, at most 4 a thread
   const v4u* row = static_cast<const v4u*>(a.x) + (int64_t)token * nvec;
-  uint2* q = reinterpret_cast<uint2*>(a.q) + (int64_t)token * nvec;
+  const int blocks = a.T <= 16 ? 1 : 2;
   v4u v[4];
   uint32_t top[4], all = 0;
 #pragma unroll
@@ -263,15 +270,16 @@ __global__ __launch_bounds__(kPrepThreads) void k_moe_prep(Moe a, GateArgs gate,
   for (int u = 0; u < 4; ++u) {
     const int i = tid + u * kPrepThreads;
     const v4u w = v[u];
+    uint2* q = reinterpret_cast<uint2*>(a.q + moe_code(blocks, i >> 4, token, (i & 15) >> 1) + 8 * (i & 1));
     if (int8) {
       if (i < nvec)
-        q[i] = uint2{int8_codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), inv),
-                     int8_codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), inv)};
+        *q = uint2{int8_codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), inv),
+                   int8_codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), inv)};
     } else if (i < nvec) {
       const Fp8Scaler s(top[u]);
-      q[i] = uint2{s.codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])),
-                   s.codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]))};
-      if ((i & 15) == 0) a.q_scale[(int64_t)token * (nvec >> 4) + (i >> 4)] = s.scale;
+      *q = uint2{s.codes4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])),
+                 s.codes4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]))};
+      if ((i & 15) == 0) a.q_scale[(i >> 4) * kMoeTokens + token] = s.scale;
     }
   }
 }
@@ -290,25 +298,21 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   const int H = a.H, N = a.N, nk = H / kFp8Block;
   const int kb0 = wave * nk / kMoeWaves, steps = (wave + 1) * nk / kMoeWaves - kb0;   // this wavefront's k-blocks
   // ---- the tokens' codes in the matrix instruction's layout ----
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, a.T * H, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rs =
-      __builtin_amdgcn_make_buffer_rsrc(a.q_scale, (short)0, a.T * (INT8 ? 1 : nk) * 4, 0x00020000);
+  // (columns of tokens that there are not hold anything; nobody looks at their sums)
   v8i tok[kUpRun][TB];
   float sa[kUpRun][TB];
 #pragma unroll
   for (int d = 0; d < kUpRun; ++d)
 #pragma unroll
-    for (int m = 0; m < TB; ++m) {
-      const int t = 16 * m + r16;   // (rows past the last token read as zeros)
-      const unsigned at = d < steps ? (unsigned)(t * H + (kb0 + d) * kFp8Block + 16 * quad) : kPastEnd;
-      tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0), __builtin_amdgcn_raw_buffer_load_b128(rx, at + 64u, 0, 0));
-      if (!INT8)
-        sa[d][m] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                 rs, d < steps ? (unsigned)(t * nk + kb0 + d) * 4u : kPastEnd, 0, 0));
-    }
+    for (int m = 0; m < TB; ++m)
+      if (d < steps) {
+        const v4i* p = reinterpret_cast<const v4i*>(a.q + moe_code(TB, kb0 + d, 16 * m, 0)) + lane;
+        tok[d][m] = join(p[0], p[64]);
+        sa[d][m] = INT8 ? 0.f : a.q_scale[(kb0 + d) * kMoeTokens + 16 * m + r16];
+      }
   float row_scale = 0.f;   // int8: of token 16 (lane / 32) + r16
   if (INT8)
-    row_scale = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (unsigned)(16 * (lane >> 5) + r16) * 4u, 0, 0));
+    row_scale = a.q_scale[min(16 * (lane >> 5) + r16, a.T - 1)];
   moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
@@ -429,8 +433,9 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
         const scalar_f* ws = (const scalar_f*)(a.w1_scale + (int64_t)e * N + 8 * c);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          hg[r] = hg[r] * row_scale * (half ? ws[4 + r] : ws[r]);
-          hu[r] = hu[r] * row_scale * (half ? ws[N / 2 + 4 + r] : ws[N / 2 + r]);
+          const float g0 = scalar(ws[r]), g1 = scalar(ws[4 + r]), u0 = scalar(ws[N / 2 + r]), u1 = scalar(ws[N / 2 + 4 + r]);
+          hg[r] = hg[r] * row_scale * (half ? g1 : g0);
+          hu[r] = hu[r] * row_scale * (half ? u1 : u0);
         }
       }
       if ((tokens >> token) & 1) {
@@ -457,7 +462,11 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
 }
 
 // ---------------------------------------------------------------------------
+// LDS by its address as a number: of an array the compiler would think that the
+// direct loads write it, and wait for all of them.
 typedef const __attribute__((address_space(3))) v4i lds_v4i;
+typedef const __attribute__((address_space(3))) v4f lds_v4f;
+typedef const __attribute__((address_space(3))) float lds_float;
 
 struct MoeGroup {
   int u0, u1, first, used;   // units, first cell, cells
@@ -472,13 +481,15 @@ struct MoeUnit {
   v4f sc[NB];     // int8: scales of the lane's four columns; fp8: [0], of their block of 128
 };
 
-template <bool INT8, int TB, int NB>
+// NH: halves of eight columns.
+template <bool INT8, int TB, int NH>
 __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
+  constexpr int NB = (NH + 1) / 2;   // blocks of 16 columns
   __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kDownRing];
   __shared__ __attribute__((aligned(16))) uint8_t cells[(kCells + 1) * kFp8Block];   // the last one: zeros
   __shared__ float cell_scale[kCells + 1];   // of its values, times its row's route scale
   __shared__ uint16_t cell_row[kCells];
-  __shared__ int4 unit_info[kCells];         // first cell; tokens; place of w2's scales
+  __shared__ v4i unit_info[kCells];          // first cell; tokens; place of w2's scales
   // w2's scales: fp8, of the first and of the last column of each block, a unit's; int8, of all columns, an expert's
   __shared__ __attribute__((aligned(16))) float w_scale[INT8 ? kGroupExperts * NB * 16 : kCells * NB * 2];
   __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
@@ -528,15 +539,15 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   const int units = n_exp * nk;
 
   // ---- weights: units wave, wave + 8, ... ----
-  constexpr int kSlot = NB * 2048, kSlots = kDownRing / kSlot;
+  constexpr int kSlot = NH * 1024, kSlots = kDownRing / kSlot;
   const unsigned ring = lds_at(ring_mem) + wave * kDownRing;
   const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(a.q, (short)0, 0, 0x00020000);   // reads as zeros
   __amdgpu_buffer_rsrc_t rw = none;
   int fj = wave / nk, fk = wave - fj * nk;   // expert's place and k-block of the next unit to be loaded
   bool turn = true;                          // another expert than the last one
-  unsigned slot = 0, vo[4];   // (2 NB of them)
+  unsigned slot = 0, vo[4];   // (NH of them)
 #pragma unroll
-  for (int h = 0; h < 2 * NB; ++h) vo[h] = (unsigned)(8 * h + (lane >> 3)) * (unsigned)K2 + moe_chunk(lane, h & 1);
+  for (int h = 0; h < NH; ++h) vo[h] = (unsigned)(8 * h + (lane >> 3)) * (unsigned)K2 + moe_chunk(lane, h & 1);
   auto fetch = [&]() {
     if (turn) {
       rw = none;
@@ -547,7 +558,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2 * NB; ++h)
+    for (int h = 0; h < NH; ++h)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + slot + h * 1024), 16, vo[h],
                                                (unsigned)fk * kFp8Block, 0, kMoeNt);
     slot = slot + kSlot == kSlots * kSlot ? 0 : slot + kSlot;
@@ -601,7 +612,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     for (int u = g.u0 + tid; u < g.u1; u += kMoeThreads) {
       const int j = u / nk, base = tab.base[j], rows = tab.base[j + 1] - base;
       const int at = base * nk + (u - j * nk) * rows - g.first;
-      unit_info[u - g.u0] = int4{at, (int)tab.tokens[j], INT8 ? (j - j0) * NB * 16 : (u - g.u0) * NB * 2, 0};
+      unit_info[u - g.u0] = v4i{at, (int)tab.tokens[j], INT8 ? (j - j0) * NB * 16 : (u - g.u0) * NB * 2, 0};
       for (int r = 0; r < rows; ++r) cell_row[at + r] = (uint16_t)(base + r);
     }
 #pragma unroll
@@ -641,26 +652,29 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     for (int n = 0; n < NB; ++n) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
   const int key = (r16 >> 1) & 7;
   const unsigned f0 = ring + r16 * kFp8Block + ((quad ^ key) << 4), f1 = ring + r16 * kFp8Block + (((4 + quad) ^ key) << 4);
-  const unsigned cell0 = lds_at(cells);
+  // (the second half of a block that has one half: its first again, whose products nobody looks at)
+  const int key8 = ((r16 & 7) >> 1) & 7;
+  const unsigned h0 = ring + (r16 & 7) * kFp8Block + ((quad ^ key8) << 4), h1 = ring + (r16 & 7) * kFp8Block + (((4 + quad) ^ key8) << 4);
+  const unsigned cell0 = lds_at(cells), scale0 = lds_at(cell_scale), info0 = lds_at(unit_info), w0 = lds_at(w_scale);
   auto load_unit = [&](int u, MoeUnit<TB, NB>& x) {
-    const int4 info = unit_info[u - g.u0];
-    const uint32_t tokens = (uint32_t)info.y;
+    const v4i info = *(lds_v4i*)(size_t)(info0 + (u - g.u0) * 16);
+    const uint32_t tokens = (uint32_t)info[1];
 #pragma unroll
     for (int m = 0; m < TB; ++m) {
       const int token = 16 * m + r16;
       x.has[m] = (tokens >> token) & 1;
-      const int cell = x.has[m] ? info.x + __popc(tokens & ((1u << token) - 1)) : kCells, k = (cell >> 1) & 7;
+      const int cell = x.has[m] ? info[0] + __popc(tokens & ((1u << token) - 1)) : kCells, k = (cell >> 1) & 7;
       const unsigned p = cell0 + cell * kFp8Block;
       x.tok[m] = join(*(lds_v4i*)(size_t)(p + ((quad ^ k) << 4)), *(lds_v4i*)(size_t)(p + (((4 + quad) ^ k) << 4)));
-      x.s[m] = cell_scale[cell];
+      x.s[m] = *(lds_float*)(size_t)(scale0 + cell * 4);
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       if (INT8) {
-        x.sc[n] = *reinterpret_cast<const v4f*>(w_scale + info.z + n * 16 + 4 * quad);
+        x.sc[n] = *(lds_v4f*)(size_t)(w0 + (info[2] + n * 16 + 4 * quad) * 4);
       } else {
         const bool same = (c0 + 16 * n + 4 * quad) / kFp8Block == (c0 + 16 * n) / kFp8Block;
-        x.sc[n][0] = w_scale[info.z + n * 2 + (same ? 0 : 1)];
+        x.sc[n][0] = *(lds_float*)(size_t)(w0 + (info[2] + n * 2 + (same ? 0 : 1)) * 4);
       }
     }
   };
@@ -688,10 +702,12 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
     if (mine < g.u1) load_unit(mine, now);
     for (; mine < g.u1; mine += kMoeWaves) {
       if (mine + kMoeWaves < g.u1) load_unit(mine + kMoeWaves, next);
-      __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * 2 * NB));
+      __builtin_amdgcn_s_waitcnt(0x0F70 | ((kSlots - 1) * NH));
       v8i w[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) w[n] = lds_get2(f0 + read + n * 2048, f1 + read + n * 2048);
+      for (int n = 0; n < NB; ++n)
+        w[n] = 2 * n + 1 == NH ? lds_get2(h0 + read + n * 2048, h1 + read + n * 2048)
+                               : lds_get2(f0 + read + n * 2048, f1 + read + n * 2048);
       read = read + kSlot == kSlots * kSlot ? 0 : read + kSlot;
       fetch();
 #pragma unroll
@@ -756,8 +772,8 @@ MoePlan make_moe_plan(const mdc_shape* sh, int inter_n) {
   p.off_ids = p.off_table + round_up(sizeof(MoeTable), 256);
   p.off_scales = p.off_ids + round_up(R * 4, 256);
   p.off_q = p.off_scales + round_up(R * 4, 256);
-  p.off_q_scale = p.off_q + round_up(T * H, 256);
-  p.off_g = p.off_q_scale + round_up(T * (H / kFp8Block) * 4, 256);
+  p.off_q_scale = p.off_q + round_up(T, 16) * H;
+  p.off_g = p.off_q_scale + H / kFp8Block * kMoeTokens * 4;
   p.off_max = p.off_g + round_up(R * (N / 2) * 4, 256);
   p.bytes = p.off_max + round_up(R * (N / 16) * 4, 256);
   return p;
@@ -794,8 +810,11 @@ template <bool INT8, int TB>
 void launch_moe(const Moe& a, unsigned cus, hipStream_t s) {
   hipLaunchKernelGGL((k_moe_up<INT8, TB>), dim3(cus), dim3(kMoeThreads), 0, s, a);
   const dim3 grid((unsigned)((a.H + a.cw - 1) / a.cw));
-  if (a.cw <= 16) hipLaunchKernelGGL((k_moe_down<INT8, TB, 1>), grid, dim3(kMoeThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_moe_down<INT8, TB, 2>), grid, dim3(kMoeThreads), 0, s, a);
+  const dim3 block(kMoeThreads);
+  if (a.cw <= 8) hipLaunchKernelGGL((k_moe_down<INT8, TB, 1>), grid, block, 0, s, a);
+  else if (a.cw <= 16) hipLaunchKernelGGL((k_moe_down<INT8, TB, 2>), grid, block, 0, s, a);
+  else if (a.cw <= 24) hipLaunchKernelGGL((k_moe_down<INT8, TB, 3>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_moe_down<INT8, TB, 4>), grid, block, 0, s, a);
 }
 
 template <bool INT8>
