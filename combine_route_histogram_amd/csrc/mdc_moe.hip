@@ -87,7 +87,7 @@ struct MoeTable {
   float weight[kMoeRoutes];         // of each row: the sum of its routes' scales
   float copy[kMoeTokens];           // sum of the scales of the token's copy experts
   float present[kMoeTokens];        // and of all its routes
-  int64_t wave_total[kMoeWaves];
+  int wave_total[kMoeWaves];
   int experts, dropped;
 };
 
@@ -115,20 +115,50 @@ __device__ __forceinline__ void table_copy(MoeTable& to, const MoeTable& from, i
   }
 }
 
+// One route, of thread i; not live: masked, or past the last.
+struct MoeRoute {
+  int id;
+  float scale;
+  bool live;
+};
+__device__ __forceinline__ MoeRoute moe_route(const Moe& a) {
+  const int i = threadIdx.x;
+  MoeRoute r = {-1, 0.f, false};
+  if (i < a.T * a.K) {
+    r.id = a.ids[i];
+    r.scale = a.scales[i];
+    r.live = a.mask == nullptr || a.mask[a.per_route ? i : i / a.K] != 0;
+  }
+  return r;
+}
+
+// Inclusive sum over the workgroup's threads, and the sum of all of them.
+__device__ __forceinline__ int moe_scan(int v, int* wave_total, int& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  v = wave_inclusive_scan(v);
+  if (lane == 63) wave_total[wave] = v;
+  lds_barrier();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kMoeWaves; ++w) {
+    const int n = wave_total[w];
+    if (w < wave) v += n;
+    all += n;
+  }
+  lds_barrier();
+  return v;
+}
+
+// Threads meet at LDS only: loads that were issued before stay on their way.
 // tmp: L ints of LDS, free again afterwards.
-__device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
+__device__ __forceinline__ void moe_table(const Moe& a, const MoeRoute& route, MoeTable& t, int* tmp) {
   __shared__ int ids[kMoeRoutes];        // -1: not present
   __shared__ float scales[kMoeRoutes];
   const int i = threadIdx.x, R = a.T * a.K;
   const int token = i / a.K;
-  int id = -1;
-  float scale = 0.f;
-  bool live = false;
-  if (i < R) {
-    id = a.ids[i];
-    scale = a.scales[i];
-    live = a.mask == nullptr || a.mask[a.per_route ? i : token] != 0;
-  }
+  const int id = route.id;
+  const float scale = route.scale;
+  const bool live = route.live;
   const bool present = live && id >= 0 && id < a.all;
   const int e = id - a.first;
   const bool mine = present && id < a.E && e >= 0 && e < a.L;
@@ -137,28 +167,27 @@ __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
   t.tokens[i] = 0;
   ids[i] = present ? id : -1;
   scales[i] = scale;
-  __syncthreads();
+  lds_barrier();
   if (mine) atomicMin(&tmp[e], i);
   if (live && !present) atomicAdd(&t.dropped, 1);
-  __syncthreads();
+  lds_barrier();
   // place of the expert of each first route
   const bool first = mine && tmp[e] == i;
-  int64_t n;
-  const int place = (int)block_scan<kMoeThreads>(first ? 1 : 0, t.wave_total, n) - 1;
+  int n, rows;
+  const int place = moe_scan(first ? 1 : 0, t.wave_total, n) - 1;
   if (first) {
     t.expert[place] = (uint16_t)e;
     tmp[e] = -1 - place;
   }
-  if (i == 0) t.experts = (int)n;
-  __syncthreads();
+  if (i == 0) t.experts = n;
+  lds_barrier();
   const int j = mine ? -1 - tmp[e] : 0;
   if (mine) atomicOr(&t.tokens[j], 1u << token);
-  __syncthreads();
-  int64_t rows;
-  const int end = (int)block_scan<kMoeThreads>(__popc(t.tokens[i]), t.wave_total, rows);
+  lds_barrier();
+  const int end = moe_scan(__popc(t.tokens[i]), t.wave_total, rows);
   t.base[i + 1] = end;
   if (i == 0) t.base[0] = 0;
-  __syncthreads();
+  lds_barrier();
   // sums over a token's routes, in order: by the first route of an expert, and by the first of the token
   if (i < R) {
     float sum = 0.f, copy = 0.f, all = 0.f;
@@ -180,7 +209,7 @@ __device__ __forceinline__ void moe_table(const Moe& a, MoeTable& t, int* tmp) {
       t.present[token] = all;
     }
   }
-  __syncthreads();
+  lds_barrier();
 }
 
 // ---- one product of 16 weight rows x 128 k x 16 tokens ----
@@ -297,31 +326,40 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
   const int r16 = lane & 15, quad = lane >> 4;
   const int H = a.H, N = a.N, nk = H / kFp8Block;
   const int kb0 = wave * nk / kMoeWaves, steps = (wave + 1) * nk / kMoeWaves - kb0;   // this wavefront's k-blocks
+  const MoeRoute route = moe_route(a);
   // ---- the tokens' codes in the matrix instruction's layout ----
-  // (columns of tokens that there are not hold anything; nobody looks at their sums)
   v8i tok[kUpRun][TB];
   float sa[kUpRun][TB];
+  // (no branches here: the waits for the routes count the loads behind them)
+  const __amdgpu_buffer_rsrc_t rx =
+      __builtin_amdgcn_make_buffer_rsrc(a.q + kb0 * TB * 2048, (short)0, steps * TB * 2048, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(a.q_scale + kb0 * kMoeTokens, (short)0, steps * kMoeTokens * 4, 0x00020000);
 #pragma unroll
-  for (int d = 0; d < kUpRun; ++d)
+  for (int m = 0; m < TB; ++m) {
+    const bool in = 16 * m + r16 < a.T;
+    const unsigned at = in ? 16u * lane : kPastEnd, at_scale = in ? 4u * r16 : kPastEnd;
 #pragma unroll
-    for (int m = 0; m < TB; ++m)
-      if (d < steps) {
-        const v4i* p = reinterpret_cast<const v4i*>(a.q + moe_code(TB, kb0 + d, 16 * m, 0)) + lane;
-        tok[d][m] = join(p[0], p[64]);
-        sa[d][m] = INT8 ? 0.f : a.q_scale[(kb0 + d) * kMoeTokens + 16 * m + r16];
-      }
+    for (int d = 0; d < kUpRun; ++d) {
+      tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(rx, at, (d * TB + m) * 2048, 0),
+                       __builtin_amdgcn_raw_buffer_load_b128(rx, at, (d * TB + m) * 2048 + 1024, 0));
+      sa[d][m] = INT8 ? 0.f
+                      : __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, at_scale, (d * kMoeTokens + 16 * m) * 4, 0));
+    }
+  }
   float row_scale = 0.f;   // int8: of token 16 (lane / 32) + r16
   if (INT8)
     row_scale = a.q_scale[min(16 * (lane >> 5) + r16, a.T - 1)];
-  moe_table(a, tab, reinterpret_cast<int*>(ring_mem));
+  moe_table(a, route, tab, reinterpret_cast<int*>(ring_mem));
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) *a.status = mdc_device_status{tab.dropped, 0, 0, 0};
     table_copy(*a.table, tab, a.T * a.K);
   }
   const int n_exp = __builtin_amdgcn_readfirstlane(tab.experts);
   const int tiles_per = N / 16;
-  const int64_t T = (int64_t)n_exp * tiles_per;
-  const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
+  // this workgroup's tiles: as many as each has, and one more for the first ones
+  const int T = n_exp * tiles_per, each = T / (int)gridDim.x, more = T - each * (int)gridDim.x, b = blockIdx.x;
+  const int t0 = b * each + min(b, more), t1 = t0 + each + (b < more ? 1 : 0);
   if (t0 == t1) return;
 
   // ---- weights ----
@@ -361,7 +399,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
     }
   };
 
-  __syncthreads();   // the table's scratch is free
+  // (the table's scratch is free: its last barrier is behind)
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
 
@@ -531,7 +569,10 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   // (the first cells and rows before it is known how many there are: the workspace has room for every route's)
   load_cells(0, (int)min((int64_t)R * nk, (int64_t)kCells));
   table_copy(tab, *a.table, R);
-  if (INT8) row_top(tid >> 4);
+  if (INT8) {
+    row_top(tid >> 4);
+    if (R > 32) row_top(32 + (tid >> 4));
+  }
   if (tid < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[tid] = 0;
   if (tid == 0) cell_scale[kCells] = 0.f;
   __syncthreads();
@@ -569,24 +610,27 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       ++fj;
     }
   };
-#pragma unroll
-  for (int d = 0; d < kSlots; ++d) fetch();
-  if (INT8)
-    for (int r = 32 + (tid >> 4); r < tab.base[n_exp]; r += 32) row_top(r);
-
   // ---- groups: as many units as the cells hold rows of ----
   MoeGroup g = {0, 0, 0, 0};
+  // (cells before unit u: base[j] nk + (u - j nk) rows of its expert j)
   auto next_group = [&]() {
     g.u0 = g.u1;
     g.first += g.used;
-    g.used = 0;
-    const int j0 = g.u0 / nk;
-    while (g.u1 < units) {
-      const int j = g.u1 / nk, rows = __builtin_amdgcn_readfirstlane(tab.base[j + 1] - tab.base[j]);
-      const int take = INT8 && j - j0 == kGroupExperts ? 0 : min((j + 1) * nk - g.u1, (kCells - g.used) / rows);
-      if (take == 0) break;
-      g.u1 += take;
-      g.used += take * rows;
+    const int limit = g.first + kCells;
+    int whole = 0;   // experts that end inside
+    for (int j = lane; j - lane < n_exp; j += 64) whole += __popcll(__ballot(j < n_exp && tab.base[j + 1] * nk <= limit));
+    const int base = __builtin_amdgcn_readfirstlane(tab.base[whole]);
+    int rows = 0, part = 0;
+    if (whole < n_exp) {
+      rows = __builtin_amdgcn_readfirstlane(tab.base[whole + 1]) - base;
+      part = (limit - base * nk) / rows;
+    }
+    g.u1 = whole * nk + part;
+    g.used = base * nk + part * rows - g.first;
+    const int most = (g.u0 / nk + kGroupExperts) * nk;   // whole experts
+    if (INT8 && g.u1 > most) {
+      g.u1 = most;
+      g.used = __builtin_amdgcn_readfirstlane(tab.base[most / nk]) * nk - g.first;
     }
   };
   auto load_scales = [&]() {
@@ -680,11 +724,13 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   };
   unsigned read = 0;
   int mine = wave;   // this wavefront's next unit
+  // The first group's scales before the weights: loads come back in their order.
   next_group();
-  if (units != 0) {
-    load_scales();
-    lds_barrier();   // the rows' scales are there
-  }
+  if (units != 0) load_scales();
+  if (INT8)
+    for (int r = 64 + (tid >> 4); r < tab.base[n_exp]; r += 32) row_top(r);
+#pragma unroll
+  for (int d = 0; d < kSlots; ++d) fetch();
   while (g.u0 < units) {
     place_units();
     lds_barrier();
