@@ -723,29 +723,124 @@ def prepare_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_sc
     return DevicePrepared(_lib.mdc_ffn_fp8_quant_input, args, "mdc_ffn_fp8_quant_input", keep, device)
 
 
-def prepare_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None) -> DevicePrepared:
-    """Grouped int8 product: a [A][K], a_scale [A], w [L][n][K] (or [n][K]), w_scale [L][n], y [A][n] bf16, fp16 or
-    fp32; expert_token_nums [L], or None with one expert."""
+def _bind(*tensors):
+    """Pointers of the tensor arguments (tensor, name, dtypes, elements), and the GPU that holds them, in one pass.
+
+    As _need, _ptr and _one_device: raw pointers and None pass (device None if there are only those)."""
+    ptrs, device, other = [], None, None
+    for t, name, dtypes, numel in tensors:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        if t.dtype not in dtypes or t.numel() < numel:
+            _need(t, name, dtypes, numel)
+        if not t.is_contiguous():
+            raise ValueError(f"mdc: {name} must be contiguous")
+        d = t.get_device()
+        if device is None:
+            device = d
+        elif d != device:
+            other = d
+        ptrs.append(t.data_ptr())
+    if device is not None and (device < 0 or (other is not None and other < 0)):
+        raise ValueError("mdc: tensors must be on a GPU")
+    if other is not None:
+        raise ValueError(f"mdc: tensors are on different GPUs ({device} and {other})")
+    return ptrs, device
+
+
+def _launch_on(fn, name: str, args, device: Optional[int], check: bool) -> int:
+    if device is None or _raw_device() == device:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if check and st != MDC_OK:
+        raise MdcError(st, name)
+    return st
+
+
+_I8, _F32, _I32, _I64 = (torch.int8,), (torch.float32,), (torch.int32,), (torch.int64,)
+_FLOATS = tuple(_DTYPES)
+_CODES = _I8 + _E4M3
+_MASK = (torch.uint8, torch.bool)
+_BYTES = (torch.uint8, torch.int8)
+_ROWS = {dt: (dt, torch.float32) for dt in (torch.bfloat16, torch.float16)}
+
+
+def _gmm_int8_args(a, a_scale, expert_token_nums, w, w_scale, y, stream):
     if _typed(a, "a").dim() != 2 or _typed(w, "w").dim() not in (2, 3):
         raise ValueError("mdc: a must have 2 dimensions, w 2 or 3")
     A, K = a.shape
     L, n = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2]
     if w.shape[-1] != K:
         raise ValueError(f"mdc: w has rows of {w.shape[-1]} elements, a of {K}")
-    _need(a, "a", torch.int8, A * K)
-    _need(a_scale, "a_scale", torch.float32, A)
-    _need(expert_token_nums, "expert_token_nums", torch.int64, L)
-    _need(w, "w", torch.int8, L * n * K)
-    _need(w_scale, "w_scale", torch.float32, L * n)
-    _need(_typed(y, "y"), "y", tuple(_DTYPES), A * n)
-    keep = (a, a_scale, expert_token_nums, w, w_scale, y)
-    device = _one_device(*keep)
-    args = (A, L, n, K, _DTYPES[y.dtype], _ptr(a), _ptr(a_scale), _ptr(expert_token_nums), _ptr(w), _ptr(w_scale),
-            _ptr(y), _device_stream(stream, device))
-    return DevicePrepared(_lib.mdc_gmm_int8, args, "mdc_gmm_int8", keep, device)
+    ptrs, device = _bind((a, "a", _I8, A * K), (a_scale, "a_scale", _F32, A),
+                         (expert_token_nums, "expert_token_nums", _I64, L), (w, "w", _I8, L * n * K),
+                         (w_scale, "w_scale", _F32, L * n), (_typed(y, "y"), "y", _FLOATS, A * n))
+    return (A, L, n, K, _DTYPES[y.dtype], *ptrs, _device_stream(stream, device)), device
+
+
+def prepare_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None) -> DevicePrepared:
+    """Grouped int8 product: a [A][K], a_scale [A], w [L][n][K] (or [n][K]), w_scale [L][n], y [A][n] bf16, fp16 or
+    fp32; expert_token_nums [L], or None with one expert."""
+    args, device = _gmm_int8_args(a, a_scale, expert_token_nums, w, w_scale, y, stream)
+    return DevicePrepared(_lib.mdc_gmm_int8, args, "mdc_gmm_int8", (a, a_scale, expert_token_nums, w, w_scale, y), device)
 
 
 _ACTS = {"none": MDC_ACT_NONE, "sigmoid": MDC_ACT_SIGMOID, "tanh": MDC_ACT_TANH}
+
+
+def _block_rms_norm_args(x, weight, post_weight, gate, gate_every, gate_act, residual, residual_out, y, q, q_scale,
+                         block_scale, residual_scale, post_eps, eps, stream):
+    for t in (weight, post_weight, gate, residual, residual_out, q):
+        if t is not None and not isinstance(t, torch.Tensor):
+            for u, name in ((weight, "weight"), (post_weight, "post_weight"), (gate, "gate"), (residual, "residual"),
+                            (residual_out, "residual_out"), (q, "q")):
+                if u is t:
+                    _typed(t, name)
+    dtype = _typed(x, "x").dtype
+    wide = _ROWS.get(dtype)
+    if wide is None:
+        raise ValueError(f"mdc: x must be bf16 or fp16, got {dtype}")
+    if x.dim() < 1:
+        raise ValueError("mdc: x must have rows")
+    H, numel = x.shape[-1], x.numel()
+    rows = numel // H if H else 0
+    columns, every, gate_elements, gate_dtype = 1, 1, 0, dtype
+    if gate is not None:
+        gate_dtype, columns = gate.dtype, gate.shape[-1] if gate.dim() else 0
+        if columns != 1 and columns != H:
+            raise ValueError(f"mdc: gate must have rows of {H} elements or of one, got {columns}")
+        if gate_every is None:
+            every = max(rows, 1) if gate.numel() == columns else 1
+        else:
+            every = int(gate_every)
+            if every < 1:
+                raise ValueError(f"mdc: gate_every must be positive, got {every}")
+        gate_elements = -(-rows // every) * columns
+    act = _ACTS.get(gate_act)
+    if act is None:
+        raise ValueError(f"mdc: gate_act must be none, sigmoid or tanh, got {gate_act!r}")
+    quant, scales = MDC_QUANT_NONE, 0
+    if q is not None:
+        quant = MDC_QUANT_INT8 if q.dtype == torch.int8 else MDC_QUANT_FP8
+        scales = rows * (1 if quant == MDC_QUANT_INT8 else -(-H // 128))
+    elif q_scale is not None:
+        raise ValueError("mdc: q_scale without q")
+    w_any = weight if weight is not None else post_weight
+    res_any = residual if residual is not None else residual_out
+    w_dtype, res_dtype = dtype if w_any is None else w_any.dtype, dtype if res_any is None else res_any.dtype
+    if (weight is not None and weight.numel() != H) or (post_weight is not None and post_weight.numel() != H):
+        t, name = (weight, "weight") if weight is not None and weight.numel() != H else (post_weight, "post_weight")
+        raise ValueError(f"mdc: x has rows of {H} elements, {name} holds {t.numel()}")
+    ptrs, device = _bind((x, "x", wide, numel), (post_weight, "post_weight", (w_dtype,) if weight is not None else wide, H), (gate, "gate", wide, gate_elements),
+                         (residual, "residual", wide, numel), (weight, "weight", wide, H),
+                         (residual_out, "residual_out", (res_dtype,) if residual is not None else wide, numel),
+                         (y, "y", (dtype,), numel), (q, "q", _CODES, numel), (q_scale, "q_scale", _F32, scales))
+    pr = mdc_block_norm_params(rows, every, H, _DTYPES[dtype], _DTYPES[res_dtype], _DTYPES[w_dtype], _DTYPES[gate_dtype],
+                               columns, act, quant, block_scale, residual_scale, post_eps, eps)
+    return (pr, *ptrs, _device_stream(stream, device)), device
 
 
 def prepare_block_rms_norm(x, weight=None, post_weight=None, gate=None, gate_every: Optional[int] = None,
@@ -759,90 +854,34 @@ def prepare_block_rms_norm(x, weight=None, post_weight=None, gate=None, gate_eve
     (default: a gate of one row is for all rows, else each has its own); q int8 with q_scale [rows], or e4m3 (or
     uint8) with q_scale [rows][ceil(H / 128)].
     """
-    _typed(x, "x")
-    for t, name in ((weight, "weight"), (post_weight, "post_weight"), (gate, "gate"), (residual, "residual"),
-                    (residual_out, "residual_out"), (q, "q")):
-        if t is not None:
-            _typed(t, name)
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"mdc: x must be bf16 or fp16, got {x.dtype}")
-    if x.dim() < 1:
-        raise ValueError("mdc: x must have rows")
-    H, numel = x.shape[-1], x.numel()
-    rows = numel // H if H else 0
-    wide = (x.dtype, torch.float32)
-    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
-        _need(t, name, wide, H)
-        if t is not None and t.numel() != H:
-            raise ValueError(f"mdc: x has rows of {H} elements, {name} holds {t.numel()}")
-    if weight is not None and post_weight is not None and weight.dtype != post_weight.dtype:
-        raise ValueError(f"mdc: post_weight must be {weight.dtype} as weight, got {post_weight.dtype}")
-    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-        _need(t, name, wide, numel)
-    res_dtype = x.dtype if residual is None and residual_out is None else \
-        (residual if residual is not None else residual_out).dtype
-    if residual_out is not None and residual_out.dtype != res_dtype:
-        raise ValueError(f"mdc: residual_out must be {res_dtype} as residual, got {residual_out.dtype}")
-    columns, every, gate_dtype = 1, 1, x.dtype
-    if gate is not None:
-        gate_dtype, columns = gate.dtype, gate.shape[-1] if gate.dim() else 0
-        if columns not in (1, H):
-            raise ValueError(f"mdc: gate must have rows of {H} elements or of one, got {columns}")
-        gate_rows = gate.numel() // columns
-        every = (max(rows, 1) if gate_rows == 1 else 1) if gate_every is None else int(gate_every)
-        if every < 1:
-            raise ValueError(f"mdc: gate_every must be positive, got {every}")
-        _need(gate, "gate", wide, -(-rows // every) * columns)
-    if gate_act not in _ACTS:
-        raise ValueError(f"mdc: gate_act must be none, sigmoid or tanh, got {gate_act!r}")
-    _need(y, "y", x.dtype, numel)
-    quant = MDC_QUANT_NONE
-    if q is not None:
-        _need(q, "q", (torch.int8,) + _E4M3, numel)
-        quant = MDC_QUANT_INT8 if q.dtype == torch.int8 else MDC_QUANT_FP8
-        _need(q_scale, "q_scale", torch.float32, rows * (1 if quant == MDC_QUANT_INT8 else -(-H // 128)))
-    elif q_scale is not None:
-        raise ValueError("mdc: q_scale without q")
-    w_dtype = x.dtype if weight is None and post_weight is None else \
-        (weight if weight is not None else post_weight).dtype
-    pr = mdc_block_norm_params(rows, every, H, _DTYPES[x.dtype], _DTYPES[res_dtype], _DTYPES[w_dtype],
-                               _DTYPES[gate_dtype], columns, _ACTS[gate_act], quant, float(block_scale),
-                               float(residual_scale), float(post_eps), float(eps))
-    keep = (x, post_weight, gate, residual, weight, residual_out, y, q, q_scale)
-    device = _one_device(*keep)
-    args = (pr, *[_ptr(t) for t in keep], _device_stream(stream, device))
-    return DevicePrepared(_lib.mdc_block_rms_norm, args, "mdc_block_rms_norm", keep, device)
+    args, device = _block_rms_norm_args(x, weight, post_weight, gate, gate_every, gate_act, residual, residual_out, y, q,
+                                        q_scale, block_scale, residual_scale, post_eps, eps, stream)
+    return DevicePrepared(_lib.mdc_block_rms_norm, args, "mdc_block_rms_norm",
+                          (x, post_weight, gate, residual, weight, residual_out, y, q, q_scale), device)
 
 
-def _prepare_moe(int8: bool, shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2,
-                 w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups,
-                 group_top, renormalise, scale, stream) -> DevicePrepared:
+def _moe_args(int8: bool, shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2,
+              w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+              renormalise, scale, stream):
     T, H, K, N, L = shape.bs, shape.hidden, shape.topk, int(inter_n), shape.local_experts
     n = shape.num_experts + shape.zero_experts + shape.copy_experts
-    for t, name in ((x, "x"), (shared_expert_x, "shared_expert_x"), (ori_x, "ori_x"), (x_out, "x_out")):
-        _need(t, name, _BF16, T * H)
-    _need(expert_ids, "expert_ids", torch.int32, T * K)
-    _need(expert_scales, "expert_scales", torch.float32, T * K)
-    _check_mask(shape, x_active_mask, 1)
-    codes = torch.int8 if int8 else _E4M3
-    _need(w1, "w1", codes, L * N * H)
-    _need(w1_scale, "w1_scale", torch.float32, L * N if int8 else L * (N // 128) * (H // 128))
-    _need(w2, "w2", codes, L * H * (N // 2))
-    _need(w2_scale, "w2_scale", torch.float32, L * H if int8 else L * (H // 128) * (N // 256))
+    codes = _I8 if int8 else _E4M3
     pr = None
     if logits is not None:
-        _need(_typed(logits, "logits"), "logits", tuple(_DTYPES), T * n)
-        _need(bias, "bias", torch.float32, n)
+        dtype = _DTYPES.get(_typed(logits, "logits").dtype, MDC_DTYPE_FP32)   # (another type is refused below)
         if score not in _SCORES:
             raise ValueError(f"mdc: score must be softmax or sigmoid, got {score!r}")
-        pr = mdc_gate_params(_DTYPES[logits.dtype], _SCORES[score], int(groups), int(topk_groups), int(group_top),
-                             1 if renormalise else 0, float(scale))
-    keep = (x, logits, bias, expert_ids, expert_scales, x_active_mask, w1, w1_scale, w2, w2_scale, shared_expert_x,
-            ori_x, x_out, workspace)
-    device = _one_device(*keep)
-    args = (shape.c(), pr, N, *[_ptr(t) for t in keep], _nbytes(workspace), _device_stream(stream, device))
-    return DevicePrepared(_lib.mdc_moe if int8 else _lib.mdc_moe_fp8, args, "mdc_moe" if int8 else "mdc_moe_fp8", keep,
-                          device)
+        pr = mdc_gate_params(dtype, _SCORES[score], int(groups), int(topk_groups), int(group_top), 1 if renormalise else 0,
+                             float(scale))
+    ptrs, device = _bind(
+        (x, "x", _BF16, T * H), (logits, "logits", _FLOATS, T * n), (bias, "bias", _F32, n),
+        (expert_ids, "expert_ids", _I32, T * K), (expert_scales, "expert_scales", _F32, T * K),
+        (x_active_mask, "x_active_mask", _MASK, T * K if shape.mask_per_route else T),
+        (w1, "w1", codes, L * N * H), (w1_scale, "w1_scale", _F32, L * N if int8 else L * (N // 128) * (H // 128)),
+        (w2, "w2", codes, L * H * (N // 2)), (w2_scale, "w2_scale", _F32, L * H if int8 else L * (H // 128) * (N // 256)),
+        (shared_expert_x, "shared_expert_x", _BF16, T * H), (ori_x, "ori_x", _BF16, T * H), (x_out, "x_out", _BF16, T * H),
+        (workspace, "workspace", _BYTES, 0))
+    return (shape.c(), pr, N, *ptrs, _nbytes(workspace), _device_stream(stream, device)), device
 
 
 def prepare_moe(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
@@ -851,9 +890,12 @@ def prepare_moe(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_
                 stream=None) -> DevicePrepared:
     """A layer of int8 experts for shape.bs tokens x [BS][H]; logits None: the routes are given in expert_ids and
     expert_scales, else these are written (or None)."""
-    return _prepare_moe(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
-                        x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
-                        renormalise, scale, stream)
+    args, device = _moe_args(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                             x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                             renormalise, scale, stream)
+    return DevicePrepared(_lib.mdc_moe, args, "mdc_moe", (x, logits, bias, expert_ids, expert_scales, x_active_mask, w1,
+                                                          w1_scale, w2, w2_scale, shared_expert_x, ori_x, x_out, workspace),
+                          device)
 
 
 def prepare_moe_fp8(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
@@ -861,9 +903,12 @@ def prepare_moe_fp8(shape: Shape, inter_n: int, x, logits, bias, expert_ids, exp
                     groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalise: bool = True,
                     scale: float = 1.0, stream=None) -> DevicePrepared:
     """prepare_moe with e4m3 experts, scales for each block of 128."""
-    return _prepare_moe(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
-                        x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
-                        renormalise, scale, stream)
+    args, device = _moe_args(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                             x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                             renormalise, scale, stream)
+    return DevicePrepared(_lib.mdc_moe_fp8, args, "mdc_moe_fp8", (x, logits, bias, expert_ids, expert_scales, x_active_mask,
+                                                                  w1, w1_scale, w2, w2_scale, shared_expert_x, ori_x, x_out,
+                                                                  workspace), device)
 
 
 # ----------------------------------------------------------------------------
@@ -971,34 +1016,37 @@ def mdc_ffn_fp8_quant_input(shape: Shape, inter_n: int, expand_q, dynamic_scales
 
 
 def mdc_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream=None, check: bool = True) -> int:
-    return _run_on_device(prepare_gmm_int8(a, a_scale, expert_token_nums, w, w_scale, y, stream), check)
+    args, device = _gmm_int8_args(a, a_scale, expert_token_nums, w, w_scale, y, stream)
+    return _launch_on(_lib.mdc_gmm_int8, "mdc_gmm_int8", args, device, check)
 
 
 def mdc_block_rms_norm(x, weight=None, post_weight=None, gate=None, gate_every: Optional[int] = None,
                        gate_act: str = "none", residual=None, residual_out=None, y=None, q=None, q_scale=None,
                        block_scale: float = 1.0, residual_scale: float = 1.0, post_eps: float = 1e-6, eps: float = 1e-6,
                        stream=None, check: bool = True) -> int:
-    return _run_on_device(prepare_block_rms_norm(x, weight, post_weight, gate, gate_every, gate_act, residual,
-                                                 residual_out, y, q, q_scale, block_scale, residual_scale, post_eps,
-                                                 eps, stream), check)
+    args, device = _block_rms_norm_args(x, weight, post_weight, gate, gate_every, gate_act, residual, residual_out, y, q,
+                                        q_scale, block_scale, residual_scale, post_eps, eps, stream)
+    return _launch_on(_lib.mdc_block_rms_norm, "mdc_block_rms_norm", args, device, check)
 
 
 def mdc_moe(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale, x_out,
             workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax", groups: int = 1,
             topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None,
             check: bool = True) -> int:
-    return _run_on_device(_prepare_moe(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale,
-                                       w2, w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score,
-                                       groups, topk_groups, group_top, renormalise, scale, stream), check)
+    args, device = _moe_args(True, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                             x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                             renormalise, scale, stream)
+    return _launch_on(_lib.mdc_moe, "mdc_moe", args, device, check)
 
 
 def mdc_moe_fp8(shape: Shape, inter_n: int, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
                 x_out, workspace, x_active_mask=None, shared_expert_x=None, ori_x=None, score: str = "softmax",
                 groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
                 stream=None, check: bool = True) -> int:
-    return _run_on_device(_prepare_moe(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale,
-                                       w2, w2_scale, x_out, workspace, x_active_mask, shared_expert_x, ori_x, score,
-                                       groups, topk_groups, group_top, renormalise, scale, stream), check)
+    args, device = _moe_args(False, shape, inter_n, x, logits, bias, expert_ids, expert_scales, w1, w1_scale, w2, w2_scale,
+                             x_out, workspace, x_active_mask, shared_expert_x, ori_x, score, groups, topk_groups, group_top,
+                             renormalise, scale, stream)
+    return _launch_on(_lib.mdc_moe_fp8, "mdc_moe_fp8", args, device, check)
 
 
 def alloc_dispatch_outputs(shape: Shape, device="cuda"):
