@@ -237,16 +237,17 @@ __device__ __forceinline__ int thin8_split(const Gmm8& g, int experts) {
 constexpr int kWide8 = 256;   // weight rows of a tile
 constexpr int wide8_stage(int BM) { return (BM + kWide8) * kGmm8Block; }
 
-template <int BM, int W>
+template <int BM>
 struct Wide8 {
-  static constexpr int WT = BM >= (W == 8 ? 64 : 128) ? 2 : 1;   // wavefronts along the rows
+  static constexpr int W = kGmmWaves, WT = BM >= 64 ? 2 : 1;   // wavefronts, along the rows
   static constexpr int TB = BM / 32 / WT, WW = W / WT, WB = kWide8 / 32 / WW;
 };
 
-template <int BM, int W, int S, int NB>
+template <int BM, int S, int NB>
 __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, unsigned lds,
-                                            v16i (&acc)[Wide8<BM, W>::TB][Wide8<BM, W>::WB]) {
-  typedef Wide8<BM, W> C;
+                                            v16i (&acc)[Wide8<BM>::TB][Wide8<BM>::WB]) {
+  typedef Wide8<BM> C;
+  constexpr int W = C::W;
   constexpr int kStage = wide8_stage(BM), kRing = S * kStage, kTokenBytes = BM * kGmm8Block;
   constexpr int kWeightLoads = 32 / W, kTokenLoads = BM / 8 >= W ? BM / 8 / W : 1;
   constexpr int kLoads = kWeightLoads + kTokenLoads, kParts = S == 2 ? 2 : 4, kPart = (kLoads + kParts - 1) / kParts;
@@ -354,9 +355,9 @@ __device__ __forceinline__ void wide8_kloop(const Gmm8& g, const WideTile& t, un
 }
 
 // One tile: the k loop, then the outputs, 16-bit ones through LDS as whole rows.
-template <int BM, int W, int S>
+template <int BM, int S>
 __device__ __forceinline__ void wide8_tile(const Gmm8& g, const WideTile& t, uint8_t* smem) {
-  typedef Wide8<BM, W> C;
+  typedef Wide8<BM> C;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / C::WW, wn = wave % C::WW;
@@ -367,15 +368,15 @@ __device__ __forceinline__ void wide8_tile(const Gmm8& g, const WideTile& t, uin
     for (int j = 0; j < C::WB; ++j) acc[i][j] = v16i{};
   const unsigned lds = lds_at(smem);
   const int blocks = (t.rows + 32 * C::WT - 1) / (32 * C::WT);   // of each wavefront that hold rows
-  if constexpr (C::TB == 1) wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+  if constexpr (C::TB == 1) wide8_kloop<BM, S, 1>(g, t, lds, acc);
   else if constexpr (C::TB == 2) {
-    if (blocks > 1) wide8_kloop<BM, W, S, 2>(g, t, lds, acc);
-    else wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+    if (blocks > 1) wide8_kloop<BM, S, 2>(g, t, lds, acc);
+    else wide8_kloop<BM, S, 1>(g, t, lds, acc);
   } else {
-    if (blocks > 3) wide8_kloop<BM, W, S, 4>(g, t, lds, acc);
-    else if (blocks > 2) wide8_kloop<BM, W, S, 3>(g, t, lds, acc);
-    else if (blocks > 1) wide8_kloop<BM, W, S, 2>(g, t, lds, acc);
-    else wide8_kloop<BM, W, S, 1>(g, t, lds, acc);
+    if (blocks > 3) wide8_kloop<BM, S, 4>(g, t, lds, acc);
+    else if (blocks > 2) wide8_kloop<BM, S, 3>(g, t, lds, acc);
+    else if (blocks > 1) wide8_kloop<BM, S, 2>(g, t, lds, acc);
+    else wide8_kloop<BM, S, 1>(g, t, lds, acc);
   }
   const __amdgpu_buffer_rsrc_t rc = channel_scales(g, t.e);
   v4f sw[C::WB][4];
@@ -415,18 +416,18 @@ __device__ __forceinline__ void wide8_tile(const Gmm8& g, const WideTile& t, uin
     __syncthreads();
     const int unit = tid & 31, col = t.n0 + 8 * unit;
     if (col < g.Nw)
-      for (int r = tid >> 5; r < t.rows; r += 64 * W / 32)
+      for (int r = tid >> 5; r < t.rows; r += kGmmThreads / 32)
         __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(smem + r * 512 + ((unit ^ (r & 31)) << 4)),
             reinterpret_cast<v4u*>(static_cast<uint16_t*>(g.y) + (int64_t)(t.row0 + r) * g.Nw + col));
   }
   lds_barrier();   // the ring is free
 }
 
-template <int BM, int W, int S>
+template <int BM, int S>
 __device__ __forceinline__ void wide8_walk(const Gmm8& g, const GmmTable& tab, uint8_t* smem) {
   const int nn = (g.Nw + kWide8 - 1) / kWide8;
   const int T = tab.tiles[g.L] * nn;
-  for (int t = wide_line(); t < T; t += gridDim.x) wide8_tile<BM, W, S>(g, wide_place(g, tab, t, nn, BM, kWide8), smem);
+  for (int t = wide_line(); t < T; t += gridDim.x) wide8_tile<BM, S>(g, wide_place(g, tab, t, nn, BM, kWide8), smem);
 }
 
 // What a k-block of a tile of 256, 128, 64 and 32 rows takes, in tenths of a microsecond.
@@ -438,6 +439,74 @@ static_assert(kLds8Flat >= 3 * wide8_stage(64) && kLds8Flat >= 3 * wide8_stage(3
                   kLds8Deep >= kLds8Flat && kLds8Flat >= kGmmWaves * kThin8Ring + 2 * kGmmWaves * kThinBlocks * 1024,
               "LDS of the tiles");
 
+// m-tiles of BM rows of the experts, the size that takes least.
+__device__ __forceinline__ int wide8_rows(const int (&count)[4], int nn) {
+  // Tiles of 256, 128, 64 or 32 rows, whichever rounds of tiles take less time:
+  // large ones do more products per byte and stage, small ones fill the CUs.
+  constexpr int kCost[4] = {kCost8_256, kCost8_128, kCost8_64, kCost8_32};
+  const int G = gridDim.x;
+  int best = 256, cost = INT32_MAX;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = kCost[i] * ((count[i] * nn + G - 1) / G);
+    if (c < cost) {
+      best = 256 >> i;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+// The plan of up to 64 experts, lane e's expert e, by each wavefront for itself:
+// no barrier but the one behind it.  Returns the rows of a tile, 0 where no expert
+// is wide.  (One row of one expert x 7168 x 2048: the whole kernel 9.4 us, and 10.8
+// with the scans of the workgroup; 3001 rows of 6 experts x 1160 x 2000 19.1 and 20.4.)
+__device__ __forceinline__ int gmm8_few(const Gmm8& g, GmmTable& t, int nn, int& wide) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v = lane < g.L ? gmm_count(g.nums, lane, g.A) : 0;
+  // in two halves of at most 30 bits' sum each
+  const int64_t low = wave_inclusive_scan((int)(v & 0xFFFFFF));
+  const int end = (int)min(((int64_t)wave_inclusive_scan((int)(v >> 24)) << 24) + low, (int64_t)g.A);
+  const int before = __shfl_up(end, 1, 64);   // (by all lanes: of one that is off it would be zero)
+  const int n = lane < g.L ? end - (lane == 0 ? 0 : before) : 0;
+  const bool thin = n > 0 && n <= kThinRows;
+  const uint64_t thins = __ballot(thin);
+  t.n_thin = __builtin_amdgcn_readfirstlane(__popcll(thins));
+  int rows = 0;
+  wide = 0;
+  if (__any(n > kThinRows)) {
+    int count[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      count[i] = __builtin_amdgcn_readlane(wave_inclusive_scan(n > kThinRows ? (n - 1) / (256 >> i) + 1 : 0), 63);
+    rows = wide8_rows(count, nn);
+    const int tiles = wave_inclusive_scan(n > kThinRows ? (n - 1) / rows + 1 : 0);
+    wide = __builtin_amdgcn_readlane(tiles, 63) * nn;
+    if (threadIdx.x < g.L) t.tiles[lane + 1] = tiles;
+    if (threadIdx.x == 0) t.tiles[0] = 0;
+  }
+  if (threadIdx.x < g.L) t.rows[lane + 1] = end;
+  if (threadIdx.x == 0) t.rows[0] = 0;
+  if (threadIdx.x < 64 && thin) t.thin[__popcll(thins & lanes_below(lane))] = (uint16_t)lane;
+  __syncthreads();
+  return rows;
+}
+
+// The same of any number of experts.
+__device__ __forceinline__ int gmm8_many(const Gmm8& g, GmmTable& t, int nn, int& wide, int64_t* wave_total) {
+  gmm_rows<kGmmThreads>(g, t.rows, wave_total);
+  int count[4], fewer[3];
+  count[0] = gmm_tiles(g, t, 256, wave_total);
+  wide = 0;
+  if (count[0] == 0) return 0;
+  gmm_tile_counts(g, t, fewer);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) count[i + 1] = fewer[i];
+  const int rows = wide8_rows(count, nn);
+  wide = (rows == 256 ? count[0] : gmm_tiles(g, t, rows, wave_total)) * nn;
+  return rows;
+}
+
 // One workgroup per CU: the wide experts' tiles, then the thin experts'.
 template <bool DEEP>
 __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
@@ -445,32 +514,15 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[DEEP ? kLds8Deep : kLds8Flat];
   __shared__ int64_t wave_total[kGmmWaves];
   GmmTable tab{gmm_table, gmm_table + g.L + 1, reinterpret_cast<uint16_t*>(gmm_table + 2 * (g.L + 1)), 0};
-  gmm_rows<kGmmThreads>(g, tab.rows, wave_total);
   const int nn = (g.Nw + kWide8 - 1) / kWide8;
-  const int G = gridDim.x;
-  constexpr int W = kGmmWaves;
-  int wide = gmm_tiles(g, tab, 256, wave_total) * nn;
-  if (wide != 0) {
-    // Tiles of 256, 128, 64 or 32 rows, whichever rounds of tiles take less time:
-    // large ones do more products per byte and stage, small ones fill the CUs.
-    int best = 256, cost = kCost8_256 * ((wide + G - 1) / G), count[3];
-    gmm_tile_counts(g, tab, count);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int c = (i == 0 ? kCost8_128 : i == 1 ? kCost8_64 : kCost8_32) * ((count[i] * nn + G - 1) / G);
-      if (c < cost) {
-        best = 128 >> i;
-        cost = c;
-      }
-    }
-    if (best != 256) wide = gmm_tiles(g, tab, best, wave_total) * nn;
-    if (best == 32) wide8_walk<32, W, DEEP ? 4 : 3>(g, tab, smem);
-    else if (best == 64) wide8_walk<64, W, 3>(g, tab, smem);
-    else if (best == 128) wide8_walk<128, W, DEEP ? 3 : 2>(g, tab, smem);
-    else wide8_walk<256, W, 2>(g, tab, smem);
-  }
+  int wide;
+  const int rows = g.L <= 64 ? gmm8_few(g, tab, nn, wide) : gmm8_many(g, tab, nn, wide, wave_total);
+  if (rows == 32) wide8_walk<32, DEEP ? 4 : 3>(g, tab, smem);
+  else if (rows == 64) wide8_walk<64, 3>(g, tab, smem);
+  else if (rows == 128) wide8_walk<128, DEEP ? 3 : 2>(g, tab, smem);
+  else if (rows == 256) wide8_walk<256, 2>(g, tab, smem);
   if (tab.n_thin != 0) {
-    __syncthreads();   // smem is free
+    if (rows != 0) __syncthreads();   // smem is free
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     thin8_walk(g, tab, wide, thin8_split(g, tab.n_thin),
                Thin8Smem{lds_at(smem) + wave * kThin8Ring, lds_at(smem) + kGmmWaves * kThin8Ring});
