@@ -47,6 +47,7 @@ constexpr int kUpRing = 12288;        // bytes of a wavefront's ring
 constexpr int kDownRing = 12288;
 constexpr int kUpRun = 8;             // most k-blocks of a wavefront
 constexpr int kCells = 256;           // rows x k-blocks of g in LDS at a time
+constexpr int kTops = 8;              // int8: largest values of tiles in a thread's registers
 constexpr int kGroupExperts = 64;     // int8: and experts' channel scales
 static_assert(kMoeRoutes <= kMoeThreads, "a thread for each route");
 
@@ -189,6 +190,8 @@ __device__ __forceinline__ void moe_table(const Moe& a, const MoeRoute& route, M
   if (i == 0) t.base[0] = 0;
   lds_barrier();
   // sums over a token's routes, in order: by the first route of an expert, and by the first of the token
+  // (for k_moe_down: only workgroup 0 hands the table on)
+  if (blockIdx.x != 0) return;
   if (i < R) {
     float sum = 0.f, copy = 0.f, all = 0.f;
     bool lead = mine;
@@ -236,11 +239,6 @@ __device__ __forceinline__ uint32_t int8_codes4(float a, float b, float c, float
 __device__ __forceinline__ float int8_inverse(float amax) {
   const float inv = amax > 0.f ? 127.0f / amax : 0.f;
   return inv > 3.402823466e38f ? 3.402823466e38f : inv;
-}
-
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {   // over the four lanes 16 apart
-  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-  return max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
 }
 
 // Loads of eight weight rows x 128 bytes into LDS: lane l takes the chunk that
@@ -500,11 +498,19 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
 }
 
 // ---------------------------------------------------------------------------
-// LDS by its address as a number: of an array the compiler would think that the
-// direct loads write it, and wait for all of them.
+// LDS by its address as a number, and its stores written out: of an array the
+// compiler would think that the direct loads write it, and wait for all of them.
+// (A barrier waits for the stores.)
 typedef const __attribute__((address_space(3))) v4i lds_v4i;
 typedef const __attribute__((address_space(3))) v4f lds_v4f;
 typedef const __attribute__((address_space(3))) float lds_float;
+typedef const __attribute__((address_space(3))) uint32_t lds_uint;
+__device__ __forceinline__ void lds_put32(unsigned at, uint32_t v) { asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory"); }
+__device__ __forceinline__ void lds_put64(unsigned at, uint2 v) {
+  const v2f w = {__uint_as_float(v.x), __uint_as_float(v.y)};
+  asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(w) : "memory");
+}
+__device__ __forceinline__ void lds_max32(unsigned at, uint32_t v) { asm volatile("ds_max_u32 %0, %1" ::"v"(at), "v"(v) : "memory"); }
 
 struct MoeGroup {
   int u0, u1, first, used;   // units, first cell, cells
@@ -526,11 +532,11 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring_mem[kMoeWaves * kDownRing];
   __shared__ __attribute__((aligned(16))) uint8_t cells[(kCells + 1) * kFp8Block];   // the last one: zeros
   __shared__ float cell_scale[kCells + 1];   // of its values, times its row's route scale
-  __shared__ uint16_t cell_row[kCells];
+  __shared__ uint32_t cell_row[kCells];
   __shared__ v4i unit_info[kCells];          // first cell; tokens; place of w2's scales
   // w2's scales: fp8, of the first and of the last column of each block, a unit's; int8, of all columns, an expert's
   __shared__ __attribute__((aligned(16))) float w_scale[INT8 ? kGroupExperts * NB * 16 : kCells * NB * 2];
-  __shared__ float row_scale[INT8 ? kMoeRoutes : 1], row_inv[INT8 ? kMoeRoutes : 1];
+  __shared__ uint32_t row_top[INT8 ? kMoeRoutes : 1];   // int8: largest |g| of each row
   __shared__ MoeTable tab;
   static_assert(sizeof(ring_mem) >= kMoeWaves * 4 * 64 * 16, "the wavefronts' sums");
   const int tid = threadIdx.x, lane = tid & 63;
@@ -538,6 +544,9 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   const int r16 = lane & 15, quad = lane >> 4;
   const int H = a.H, K2 = a.N / 2, nk = K2 / kFp8Block, R = a.T * a.K;
   const int c0 = blockIdx.x * a.cw, cols = min(a.cw, H - c0);
+
+  const unsigned cell0 = lds_at(cells), scale0 = lds_at(cell_scale), info0 = lds_at(unit_info), w0 = lds_at(w_scale);
+  const unsigned row0 = lds_at(cell_row), top0 = lds_at(row_top), weight0 = lds_at(tab.weight);
 
   // ---- what the units' groups need of memory, in registers ----
   constexpr int kPasses = kCells * 16 / kMoeThreads;   // 16 lanes x 8 values a cell
@@ -553,25 +562,17 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       gb[p] = src[1];
     }
   };
-  // largest values of 32 rows' tiles (int8), 16 lanes a row
-  auto row_top = [&](int r) {
-    uint32_t m = 0;
-    const int per = a.N / 16;
-    const float* p = a.g_max + (int64_t)min(r, R - 1) * per;
-#pragma unroll 8
-    for (int i = r16; i < per; i += 16) m = max(m, __float_as_uint(p[i]));
-    m = row16_max(m);
-    if (r16 == 0 && r < kMoeRoutes) {
-      row_scale[r] = __uint_as_float(m) / 127.0f;
-      row_inv[r] = int8_inverse(__uint_as_float(m));
-    }
-  };
-  // (the first cells and rows before it is known how many there are: the workspace has room for every route's)
+  // (the first cells before it is known how many there are: the workspace has room for every route's)
   load_cells(0, (int)min((int64_t)R * nk, (int64_t)kCells));
   table_copy(tab, *a.table, R);
+  // int8: the largest values of the rows' tiles, as many as there are registers for
+  const int per = a.N / 16;   // a multiple of 16
+  uint32_t tops[INT8 ? kTops : 1];
   if (INT8) {
-    row_top(tid >> 4);
-    if (R > 32) row_top(32 + (tid >> 4));
+#pragma unroll
+    for (int p = 0; p < kTops; ++p)
+      tops[INT8 ? p : 0] = __float_as_uint(a.g_max[min((int64_t)tid + p * kMoeThreads, (int64_t)R * per - 1)]);
+    row_top[INT8 ? tid : 0] = 0;
   }
   if (tid < kFp8Block / 4) reinterpret_cast<uint32_t*>(cells + kCells * kFp8Block)[tid] = 0;
   if (tid == 0) cell_scale[kCells] = 0.f;
@@ -650,17 +651,16 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       gs[p] = a.w2_scale[at];
     }
   };
-  // the group's cells, scales and units into LDS
+  // the group's units, cells and scales into LDS
   auto place_units = [&]() {
     const int j0 = g.u0 / nk;
     for (int u = g.u0 + tid; u < g.u1; u += kMoeThreads) {
       const int j = u / nk, base = tab.base[j], rows = tab.base[j + 1] - base;
       const int at = base * nk + (u - j * nk) * rows - g.first;
-      unit_info[u - g.u0] = v4i{at, (int)tab.tokens[j], INT8 ? (j - j0) * NB * 16 : (u - g.u0) * NB * 2, 0};
-      for (int r = 0; r < rows; ++r) cell_row[at + r] = (uint16_t)(base + r);
+      const v4i info = {at, (int)tab.tokens[j], INT8 ? (j - j0) * NB * 16 : (u - g.u0) * NB * 2, 0};
+      lds_put(info0 + (u - g.u0) * 16, __builtin_bit_cast(v4f, info));
+      for (int r = 0; r < rows; ++r) lds_put32(row0 + (at + r) * 4, (uint32_t)(base + r));
     }
-#pragma unroll
-    for (int p = 0; p < kScales; ++p) w_scale[tid + p * kMoeThreads] = gs[p];
   };
   auto place_cells = [&]() {
 #pragma unroll
@@ -668,13 +668,13 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       const int cell = (tid + p * kMoeThreads) >> 4, u = tid & 15;
       if (cell < g.used) {
         const v4f x = ga[p], y = gb[p];
-        const int row = cell_row[cell];
+        const int row = (int)*(lds_uint*)(size_t)(row0 + cell * 4);
         uint2 code;
         float scale;
         if (INT8) {
-          const float inv = row_inv[INT8 ? row : 0];
+          const float top = *(lds_float*)(size_t)(top0 + row * 4), inv = int8_inverse(top);
           code = uint2{int8_codes4(x[0], x[1], x[2], x[3], inv), int8_codes4(y[0], y[1], y[2], y[3], inv)};
-          scale = row_scale[INT8 ? row : 0];
+          scale = top / 127.0f;
         } else {
           uint32_t top = 0;
 #pragma unroll
@@ -683,8 +683,8 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
           code = uint2{s.codes4(x[0], x[1], x[2], x[3]), s.codes4(y[0], y[1], y[2], y[3])};
           scale = s.scale;
         }
-        if (u == 0) cell_scale[cell] = scale * tab.weight[row];
-        *reinterpret_cast<uint2*>(cells + cell * kFp8Block + (((u >> 1) ^ ((cell >> 1) & 7)) << 4) + (u & 1) * 8) = code;
+        if (u == 0) lds_put32(scale0 + cell * 4, __float_as_uint(scale * *(lds_float*)(size_t)(weight0 + row * 4)));
+        lds_put64(cell0 + cell * kFp8Block + (((u >> 1) ^ ((cell >> 1) & 7)) << 4) + (u & 1) * 8, code);
       }
     }
   };
@@ -699,7 +699,6 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   // (the second half of a block that has one half: its first again, whose products nobody looks at)
   const int key8 = ((r16 & 7) >> 1) & 7;
   const unsigned h0 = ring + (r16 & 7) * kFp8Block + ((quad ^ key8) << 4), h1 = ring + (r16 & 7) * kFp8Block + (((4 + quad) ^ key8) << 4);
-  const unsigned cell0 = lds_at(cells), scale0 = lds_at(cell_scale), info0 = lds_at(unit_info), w0 = lds_at(w_scale);
   auto load_unit = [&](int u, MoeUnit<TB, NB>& x) {
     const v4i info = *(lds_v4i*)(size_t)(info0 + (u - g.u0) * 16);
     const uint32_t tokens = (uint32_t)info[1];
@@ -727,15 +726,32 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
   // The first group's scales before the weights: loads come back in their order.
   next_group();
   if (units != 0) load_scales();
-  if (INT8)
-    for (int r = 64 + (tid >> 4); r < tab.base[n_exp]; r += 32) row_top(r);
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
-  while (g.u0 < units) {
+  if (INT8) {
+    // 16 lanes look at one row (fewer than 2^30 tiles in all)
+    const unsigned n = (unsigned)(tab.base[n_exp] * per);
+    auto look = [&](unsigned i, uint32_t v) {
+      v = row16_max(v);
+      if (r16 == 0 && i < n) lds_max32(top0 + i / (unsigned)per * 4, v);
+    };
+#pragma unroll
+    for (int p = 0; p < kTops; ++p)
+      if (p * kMoeThreads < n) look(tid + p * kMoeThreads, tops[INT8 ? p : 0]);
+    for (unsigned i = tid + kTops * kMoeThreads; i - r16 < n; i += kMoeThreads) look(i, __float_as_uint(a.g_max[i]));
+  }
+  auto place_group = [&]() {
     place_units();
     lds_barrier();
     place_cells();
+#pragma unroll
+    for (int p = 0; p < kScales; ++p) lds_put32(w0 + (tid + p * kMoeThreads) * 4, __float_as_uint(gs[p]));
     lds_barrier();
+  };
+  // (The first group by itself: its loads are ahead of the weights', and the waits
+  // for them let the weights be on their way.)
+  if (units != 0) place_group();
+  while (g.u0 < units) {
     const MoeGroup cur = g;
     next_group();
     if (g.u0 < units) {   // the next group's, on their way while this one's units are multiplied
@@ -775,7 +791,10 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
       now = next;
     }
     g = ahead;
-    lds_barrier();   // the cells have been read
+    if (g.u0 < units) {
+      lds_barrier();   // the cells have been read
+      place_group();
+    }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
   __syncthreads();
