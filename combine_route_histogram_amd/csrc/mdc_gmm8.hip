@@ -65,14 +65,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t channel_scales(const Gmm8& g, 
 constexpr int kThin8Ring = 12288;   // bytes of a wavefront's ring
 constexpr int kThin8Run = 8;        // k-blocks of rows in registers
 constexpr int kThin8Nt = 2;         // cache policy: non-temporal
-constexpr int kWide8Cost = 2;       // a wide tile's time in those of 128 columns of thin work
 
 struct Thin8Smem {
   unsigned ring;   // this wavefront's, kThin8Ring bytes
   unsigned red;    // [2][8 wavefronts][2 row blocks][64] v4i
 };
 
-__device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, int wide, int ks, const Thin8Smem& sm) {
+__device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, int wide, int cost16, int ks, const Thin8Smem& sm) {
   constexpr int MB = kThinBlocks, kSlot = 2048, kSlots = kThin8Ring / kSlot;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -83,7 +82,7 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
   const int width = 16 * rs, tiles_per = (Nw + width - 1) / width;
   // this workgroup's tiles: [t0, t1) of n_thin * tiles_per
   const int64_t T = (int64_t)tab.n_thin * tiles_per;
-  const int cost = max(1, kWide8Cost * 8 / rs);
+  const int cost = max(1, cost16 / rs);
   const int t0 = (int)thin_share(T, wide, cost, wide_line()), t1 = (int)thin_share(T, wide, cost, wide_line() + 1);
   if (t0 == t1) return;
 
@@ -119,6 +118,36 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
       }
     }
   };
+
+  // ---- the expert's rows, which are on their way before the weights ----
+  v8i tok[kThin8Run][MB];
+  float sa[MB];
+  int i = c.i, n0 = c.n, have = i, held = 0, e = 0, row0 = 0, rows = 0;
+  auto expert = [&]() {
+    e = __builtin_amdgcn_readfirstlane((int)tab.thin[i]);
+    row0 = __builtin_amdgcn_readfirstlane(tab.rows[e]);
+    rows = __builtin_amdgcn_readfirstlane(tab.rows[e + 1] - row0);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) sa[m] = g.a_scale[row0 + min(16 * m + r16, rows - 1)];
+  };
+  // their k-blocks s0 ... of the run, in the matrix instruction's layout
+  auto tokens = [&](int s0) {
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
+#pragma unroll
+    for (int d = 0; d < kThin8Run; ++d) {
+      const int b = s0 + d < per ? kb0 + s0 + d : nk;
+      const unsigned k0 = (unsigned)b * kGmm8Block + 16u * quad, k1 = k0 + 64u;
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const unsigned at = (unsigned)((16 * m + r16) * K);
+        tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
+                         __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
+      }
+    }
+  };
+  expert();
+  tokens(0);
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
 
@@ -126,36 +155,15 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
   const unsigned f0 = sm.ring + r16 * kGmm8Block + ((quad ^ key) << 4);
   const unsigned f1 = sm.ring + r16 * kGmm8Block + (((4 + quad) ^ key) << 4);
   unsigned read = 0;
-  v8i tok[kThin8Run][MB];
-  float sa[MB];
-  int i = t0 / tiles_per, n0 = (t0 % tiles_per) * width, have = -1, e = 0, row0 = 0, rows = 0;
   for (int t = t0; t < t1; ++t) {
-    if (i != have) {
-      e = __builtin_amdgcn_readfirstlane((int)tab.thin[i]);
-      row0 = __builtin_amdgcn_readfirstlane(tab.rows[e]);
-      rows = __builtin_amdgcn_readfirstlane(tab.rows[e + 1] - row0);
-#pragma unroll
-      for (int m = 0; m < MB; ++m) sa[m] = g.a_scale[row0 + min(16 * m + r16, rows - 1)];
-    }
+    if (i != have) expert();
     v4i acc[MB];
 #pragma unroll
     for (int m = 0; m < MB; ++m) acc[m] = v4i{0, 0, 0, 0};
     for (int s0 = 0; s0 < per; s0 += kThin8Run) {
-      if (i != have || per > kThin8Run) {
-        // the rows' k-blocks of this run, in the matrix instruction's layout
-        const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<int8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
-#pragma unroll
-        for (int d = 0; d < kThin8Run; ++d) {
-          const int b = s0 + d < per ? kb0 + s0 + d : nk;
-          const unsigned k0 = (unsigned)b * kGmm8Block + 16u * quad, k1 = k0 + 64u;
-#pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            const unsigned at = (unsigned)((16 * m + r16) * K);
-            tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
-                             __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
-          }
-        }
+      if (i != have || s0 != held) {
+        tokens(s0);
+        held = s0;
       }
 #pragma unroll
       for (int d = 0; d < kThin8Run; ++d) {
@@ -222,7 +230,7 @@ __device__ __forceinline__ int thin8_split(const Gmm8& g, int experts) {
 
 // ---------------------------------------------------------------------------
 // Experts with more rows: tiles of BM = 32 to 256 rows x 256 weight rows, one
-// workgroup of W wavefronts per CU walking tiles.  Each k-block of 128 is one
+// workgroup per CU walking tiles.  Each k-block of 128 is one
 // stage, loaded global -> LDS directly into a ring of S stages while earlier ones
 // are multiplied.  Wavefront (wt, wn) holds the token blocks i WT + wt (32 rows
 // each, so that a short tile's blocks are shared) x WB weight blocks of 32.
@@ -430,38 +438,166 @@ __device__ __forceinline__ void wide8_walk(const Gmm8& g, const GmmTable& tab, u
   for (int t = wide_line(); t < T; t += gridDim.x) wide8_tile<BM, S>(g, wide_place(g, tab, t, nn, BM, kWide8), smem);
 }
 
-// What a k-block of a tile of 256, 128, 64 and 32 rows takes, in tenths of a microsecond.
-constexpr int kCost8_256 = 20, kCost8_128 = 12, kCost8_64 = 8, kCost8_32 = 6;
+// ---------------------------------------------------------------------------
+// Experts of more rows in a call of few tiles: tiles of 64 rows x 64 weight rows,
+// whose k-blocks go round the eight wavefronts.  A wavefront has the whole tile's
+// sums, 64 registers, and a k-block of its own in LDS, 128 bytes of each row: no
+// barrier until the eight sums are joined.  What bounds it is the 16 KB a k-block
+// from the caches, twice what a tile of 256 x 256 takes for a product, and the time
+// until they come; for one round of tiles it is the shorter way.  64 rows of one
+// expert x 4096 x 7168: 22.8 us, with tiles of 32 x 256 43; 500 x 1160 x 2000 9.6
+// and 15.8; 64 of each of four x 4096 x 7168 27.8 and 48.5.  (By 64 bytes of each
+// row at a time, in two slots, 32; straight from memory into registers, where lanes
+// side by side read different rows, 32.)
+// ---------------------------------------------------------------------------
+constexpr int kSplit8 = 64;   // rows and weight rows of a tile
+
+__device__ __forceinline__ void split8_walk(const Gmm8& g, const GmmTable& tab, uint8_t* smem) {
+  constexpr int B = kSplit8 / 16, kSlot = 2 * kSplit8 * kGmm8Block;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const int K = g.K, Nw = g.Nw;
+  const int nn = (Nw + kSplit8 - 1) / kSplit8;
+  const int T = tab.tiles[g.L] * nn;
+  const int steps = (g.nk + kGmmWaves - 1) / kGmmWaves;   // k-blocks of a wavefront
+  const unsigned lds = lds_at(smem), ring = lds + wave * kSlot;
+  const int lrow = lane >> 3, key = (r16 >> 1) & 7;
+  const unsigned f0 = ring + r16 * kGmm8Block + ((quad ^ key) << 4), f1 = ring + r16 * kGmm8Block + (((4 + quad) ^ key) << 4);
+  __amdgpu_buffer_rsrc_t ra, rw;
+  auto fetch = [&](int step) {
+    const unsigned k0 = (unsigned)(kGmmWaves * step + wave) * kGmm8Block;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // eight rows each, as a thin expert's weights
+      const unsigned chunk = (unsigned)((lane & 7) ^ ((4 * h + (lrow >> 1)) & 7)) << 4;
+      const unsigned v = k0 + chunk < (unsigned)K ? (unsigned)((8 * h + lrow) * K) + k0 + chunk : kPastEnd;   // zeros past K
+#pragma unroll
+      for (int m = 0; m < B; ++m) {
+        const unsigned rows = (unsigned)(16 * m * K);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(size_t)(ring + (2 * m + h) * 1024), 16, v + rows, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(size_t)(ring + (2 * (B + m) + h) * 1024), 16, v + rows, 0, 0, 0);
+      }
+    }
+  };
+  typedef const __attribute__((address_space(3))) v4i lds_v4i;
+  for (int t = wide_line(); t < T; t += gridDim.x) {
+    const WideTile tile = wide_place(g, tab, t, nn, kSplit8, kSplit8);
+    ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(g.a + (int64_t)tile.row0 * K), (short)0, tile.rows * K, 0x00020000);
+    rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(g.w + ((int64_t)tile.e * Nw + tile.n0) * K), (short)0,
+                                           (Nw - tile.n0) * K, 0x00020000);
+    // blocks (m, c) and (m, c + 1) of 16 x 16 are this wavefront's to store
+    const int m = wave / 2, c = wave % 2 * 2, row = 16 * m + r16;
+    const __amdgpu_buffer_rsrc_t rc = channel_scales(g, tile.e);
+    v4f sw[2];
+    const float sa = g.a_scale[tile.row0 + min(row, tile.rows - 1)];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      sw[j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, (unsigned)(tile.n0 + 16 * (c + j) + 4 * quad) * 4u, 0, 0));
+    v4i acc[B][B];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int j = 0; j < B; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    fetch(0);
+    for (int s = 0; s < steps; ++s) {
+      v4i q[2][B], w[2][B];
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // the k-block is there
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          q[h][i] = *(lds_v4i*)(size_t)((h == 0 ? f0 : f1) + i * 2048);
+          w[h][i] = *(lds_v4i*)(size_t)((h == 0 ? f0 : f1) + (B + i) * 2048);
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // it has been read
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(s + 1);   // (past the last: zeros, never used)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+          for (int j = 0; j < B; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][j], q[h][i], acc[i][j], 0, 0, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
+    lds_barrier();                        // the rings are free
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int j = 0; j < B; ++j) lds_put(lds + (((wave * B + i) * B + j) * 64 + lane) * 16, __builtin_bit_cast(v4f, acc[i][j]));
+    lds_barrier();
+    if (row - r16 < tile.rows) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v4i sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kGmmWaves; k += 2) {
+          const unsigned at = lds + (((k * B + m) * B + c + j) * 64 + lane) * 16;
+          const v8i p = lds_get2(at, at + B * B * 1024);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum[r] += p[r] + p[4 + r];
+        }
+        const int col = tile.n0 + 16 * (c + j) + 4 * quad;
+        if (row < tile.rows && col < Nw) gmm8_store(g, (int64_t)(tile.row0 + row) * Nw + col, gmm8_scale(sum, sa, sw[j]));
+      }
+    }
+    lds_barrier();   // the sums have been read
+  }
+}
+
+// What a k-block of a tile of 256, 128, 64 and 32 rows takes, and one of a tile whose
+// k-blocks are split, in hundredths of a microsecond; there the join's time too.
+// (Rounds of 56 k-blocks of the split tiles: 15.4 us; of 16: 6.)
+constexpr int kCost8[4] = {200, 120, 80, 60}, kCost8_Split = 24, kCost8_Join = 200;
 
 // LDS of the tiles; 128-row tiles take three stages and 32-row tiles four where the experts' table leaves that much.
 constexpr int kLds8Deep = 3 * wide8_stage(128), kLds8Flat = 2 * wide8_stage(256);
 static_assert(kLds8Flat >= 3 * wide8_stage(64) && kLds8Flat >= 3 * wide8_stage(32) && kLds8Deep >= 4 * wide8_stage(32) &&
-                  kLds8Deep >= kLds8Flat && kLds8Flat >= kGmmWaves * kThin8Ring + 2 * kGmmWaves * kThinBlocks * 1024,
+                  kLds8Deep >= kLds8Flat && kLds8Flat >= kGmmWaves * kThin8Ring + 2 * kGmmWaves * kThinBlocks * 1024 &&
+                  kLds8Flat >= kGmmWaves * kSplit8 * kSplit8 * 4,   // (the rings are as large)
               "LDS of the tiles");
 
-// m-tiles of BM rows of the experts, the size that takes least.
-__device__ __forceinline__ int wide8_rows(const int (&count)[4], int nn) {
+// How the experts of more than kThinRows rows are cut: tiles of `rows` rows, the
+// k-blocks of a tile one after another or over the wavefronts (split).
+struct Wide8Plan {
+  int rows = 0;   // 0: there are no such experts
+  bool split = false;
+  int tiles = 0;
+  __device__ int cost() const { return split ? 2 : 16; }   // of a tile, in those of 16 columns of thin work
+};
+
+// count: m-tiles of 256, 128, 64 and 32 rows.
+__device__ __forceinline__ Wide8Plan wide8_plan(const Gmm8& g, const int (&count)[4]) {
   // Tiles of 256, 128, 64 or 32 rows, whichever rounds of tiles take less time:
   // large ones do more products per byte and stage, small ones fill the CUs.
-  constexpr int kCost[4] = {kCost8_256, kCost8_128, kCost8_64, kCost8_32};
-  const int G = gridDim.x;
-  int best = 256, cost = INT32_MAX;
+  const int G = gridDim.x, nn = (g.Nw + kWide8 - 1) / kWide8;
+  Wide8Plan p;
+  int64_t least = INT64_MAX;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = kCost[i] * ((count[i] * nn + G - 1) / G);
-    if (c < cost) {
-      best = 256 >> i;
-      cost = c;
+    const int64_t c = (int64_t)kCost8[i] * ((count[i] * nn + G - 1) / G) * g.nk;
+    if (c < least) {
+      p.rows = 256 >> i;
+      p.tiles = count[i] * nn;
+      least = c;
     }
   }
-  return best;
+  const int tiles = count[2] * ((g.Nw + kSplit8 - 1) / kSplit8);
+  const int64_t c = (int64_t)((tiles + G - 1) / G) * (kCost8_Split * g.nk + kCost8_Join);
+  if (c < least) {
+    p.rows = kSplit8;
+    p.tiles = tiles;
+    p.split = true;
+  }
+  return p;
 }
 
 // The plan of up to 64 experts, lane e's expert e, by each wavefront for itself:
-// no barrier but the one behind it.  Returns the rows of a tile, 0 where no expert
-// is wide.  (One row of one expert x 7168 x 2048: the whole kernel 9.4 us, and 10.8
-// with the scans of the workgroup; 3001 rows of 6 experts x 1160 x 2000 19.1 and 20.4.)
-__device__ __forceinline__ int gmm8_few(const Gmm8& g, GmmTable& t, int nn, int& wide) {
+// no barrier but the one behind it.  (One row of one expert x 7168 x 2048: the whole
+// kernel 9.4 us, and 10.8 with the scans of the workgroup; 3001 rows of 6 experts x
+// 1160 x 2000 19.1 and 20.4.)
+__device__ __forceinline__ Wide8Plan gmm8_few(const Gmm8& g, GmmTable& t) {
   const int lane = threadIdx.x & 63;
   const int64_t v = lane < g.L ? gmm_count(g.nums, lane, g.A) : 0;
   // in two halves of at most 30 bits' sum each
@@ -472,16 +608,14 @@ __device__ __forceinline__ int gmm8_few(const Gmm8& g, GmmTable& t, int nn, int&
   const bool thin = n > 0 && n <= kThinRows;
   const uint64_t thins = __ballot(thin);
   t.n_thin = __builtin_amdgcn_readfirstlane(__popcll(thins));
-  int rows = 0;
-  wide = 0;
+  Wide8Plan p;
   if (__any(n > kThinRows)) {
     int count[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       count[i] = __builtin_amdgcn_readlane(wave_inclusive_scan(n > kThinRows ? (n - 1) / (256 >> i) + 1 : 0), 63);
-    rows = wide8_rows(count, nn);
-    const int tiles = wave_inclusive_scan(n > kThinRows ? (n - 1) / rows + 1 : 0);
-    wide = __builtin_amdgcn_readlane(tiles, 63) * nn;
+    p = wide8_plan(g, count);
+    const int tiles = wave_inclusive_scan(n > kThinRows ? (n - 1) / p.rows + 1 : 0);
     if (threadIdx.x < g.L) t.tiles[lane + 1] = tiles;
     if (threadIdx.x == 0) t.tiles[0] = 0;
   }
@@ -489,22 +623,21 @@ __device__ __forceinline__ int gmm8_few(const Gmm8& g, GmmTable& t, int nn, int&
   if (threadIdx.x == 0) t.rows[0] = 0;
   if (threadIdx.x < 64 && thin) t.thin[__popcll(thins & lanes_below(lane))] = (uint16_t)lane;
   __syncthreads();
-  return rows;
+  return p;
 }
 
 // The same of any number of experts.
-__device__ __forceinline__ int gmm8_many(const Gmm8& g, GmmTable& t, int nn, int& wide, int64_t* wave_total) {
+__device__ __forceinline__ Wide8Plan gmm8_many(const Gmm8& g, GmmTable& t, int64_t* wave_total) {
   gmm_rows<kGmmThreads>(g, t.rows, wave_total);
   int count[4], fewer[3];
   count[0] = gmm_tiles(g, t, 256, wave_total);
-  wide = 0;
-  if (count[0] == 0) return 0;
+  if (count[0] == 0) return Wide8Plan();
   gmm_tile_counts(g, t, fewer);
 #pragma unroll
   for (int i = 0; i < 3; ++i) count[i + 1] = fewer[i];
-  const int rows = wide8_rows(count, nn);
-  wide = (rows == 256 ? count[0] : gmm_tiles(g, t, rows, wave_total)) * nn;
-  return rows;
+  const Wide8Plan p = wide8_plan(g, count);
+  if (p.rows != 256) gmm_tiles(g, t, p.rows, wave_total);
+  return p;
 }
 
 // One workgroup per CU: the wide experts' tiles, then the thin experts'.
@@ -514,17 +647,16 @@ __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[DEEP ? kLds8Deep : kLds8Flat];
   __shared__ int64_t wave_total[kGmmWaves];
   GmmTable tab{gmm_table, gmm_table + g.L + 1, reinterpret_cast<uint16_t*>(gmm_table + 2 * (g.L + 1)), 0};
-  const int nn = (g.Nw + kWide8 - 1) / kWide8;
-  int wide;
-  const int rows = g.L <= 64 ? gmm8_few(g, tab, nn, wide) : gmm8_many(g, tab, nn, wide, wave_total);
-  if (rows == 32) wide8_walk<32, DEEP ? 4 : 3>(g, tab, smem);
-  else if (rows == 64) wide8_walk<64, 3>(g, tab, smem);
-  else if (rows == 128) wide8_walk<128, DEEP ? 3 : 2>(g, tab, smem);
-  else if (rows == 256) wide8_walk<256, 2>(g, tab, smem);
+  const Wide8Plan p = g.L <= 64 ? gmm8_few(g, tab) : gmm8_many(g, tab, wave_total);
+  if (p.split) split8_walk(g, tab, smem);
+  else if (p.rows == 32) wide8_walk<32, DEEP ? 4 : 3>(g, tab, smem);
+  else if (p.rows == 64) wide8_walk<64, 3>(g, tab, smem);
+  else if (p.rows == 128) wide8_walk<128, DEEP ? 3 : 2>(g, tab, smem);
+  else if (p.rows == 256) wide8_walk<256, 2>(g, tab, smem);
   if (tab.n_thin != 0) {
-    if (rows != 0) __syncthreads();   // smem is free
+    if (p.rows != 0) __syncthreads();   // smem is free
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    thin8_walk(g, tab, wide, thin8_split(g, tab.n_thin),
+    thin8_walk(g, tab, p.tiles, p.cost(), thin8_split(g, tab.n_thin),
                Thin8Smem{lds_at(smem) + wave * kThin8Ring, lds_at(smem) + kGmmWaves * kThin8Ring});
   }
 }

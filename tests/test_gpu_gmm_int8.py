@@ -91,6 +91,15 @@ def test_tiles(counts, dtype):
     check(counts, 4104, 400, dtype=dtype, seed=len(counts))
 
 
+# with 256 CUs: one or two rounds of tiles of 64 x 64, whose k-blocks go over the wavefronts, beside few rows an expert
+@pytest.mark.parametrize("counts,n,k,capacity", [
+    ([33], 1160, 2000, 33), ([64], 2056, 7168, 70), ([200, 5, 0, 65, 32], 328, 1040, 290), ([513], 136, 7184, 600),
+    ([40] + [1, 0, 33] * 30, 72, 1936, 1100), ([100, 2 ** 40], 200, 4112, 300), ([1, 34, 2], 8, 1168, 37)])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+def test_tiles_with_k_split(counts, n, k, capacity, dtype):
+    check(counts, n, k, capacity=capacity, dtype=dtype, seed=k)
+
+
 @pytest.mark.parametrize("counts,capacity", [([300, 20], 400), ([3, 0, 32, 9], 44), ([1, 1, 2], 4)])
 def test_the_widths_of_a_layer(counts, capacity):
     check(counts, 4096, 7168, capacity=capacity, seed=7)
