@@ -13,6 +13,14 @@ namespace {
 // The weight block is the first operand of the matrix instruction and the token
 // block the second, so that a lane ends up with runs of four consecutive output
 // columns of one token.
+//
+// Three ways in one launch, by an expert's rows and the call's tiles.  What bounds
+// them: few rows, the weights' way from memory (256 rows of 30 experts x 4096 x 7168:
+// 135 us, 6.5 TB/s); many, the matrix units at the clock that they leave (4096 x 4096
+// x 7168: 100 us, 2.4 POP/s; 89 us without the stages' direct loads, 84 without LDS
+// reads too; the library's product without scales 102); those between, the time from
+// one k-block to the next; small calls, the launch and the plan (one row x 7168 x
+// 2048: 9.4 us, 2.2 of them the weights at that rate).
 // ---------------------------------------------------------------------------
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
@@ -58,6 +66,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t channel_scales(const Gmm8& g, 
 // non-temporal policy such loads reach 6.8 TB/s, without it 6.0 (940 MB, tiles of
 // 16 rows; the same for runs of 128 to 512 bytes and rings of 8 to 18 KB).  The
 // expert's rows stay in registers from tile to tile, kThin8Run k-blocks of them.
+//
+// The border of 32 rows is that of two blocks of the instruction, for any number of
+// experts; 32 : 33 rows each, in us: one expert x 4096 x 7168 14.1 : 20.4, four 26.4 :
+// 25.5, 16 x 4096 x 2048 31 : 24, 8 x 2048 x 1024 11.3 : 8.8.
 //
 // LDS accesses are written out with their waits: the compiler would make each wait
 // for every direct load in flight.
@@ -230,10 +242,10 @@ __device__ __forceinline__ int thin8_split(const Gmm8& g, int experts) {
 
 // ---------------------------------------------------------------------------
 // Experts with more rows: tiles of BM = 32 to 256 rows x 256 weight rows, one
-// workgroup per CU walking tiles.  Each k-block of 128 is one
-// stage, loaded global -> LDS directly into a ring of S stages while earlier ones
-// are multiplied.  Wavefront (wt, wn) holds the token blocks i WT + wt (32 rows
-// each, so that a short tile's blocks are shared) x WB weight blocks of 32.
+// workgroup per CU walking tiles.  Each k-block of 128 is one stage, loaded global ->
+// LDS directly into a ring of S stages while earlier ones are multiplied.  Wavefront
+// (wt, wn) holds the token blocks i WT + wt (32 rows each, so that a short tile's
+// blocks are shared) x WB weight blocks of 32.
 //
 // A stage is four steps of 32 k.  The fragments of a step are read while the one
 // before it is multiplied; the last step's products run behind the barrier that

@@ -23,10 +23,10 @@ namespace {
 //
 // k_moe_up: a tile is 8 gate columns and the 8 up columns that go with them, one
 // 16-row block of the matrix instruction; the wavefronts split k.  Every token is
-// an operand row for every expert, so the tokens stay in registers, quantised
-// there once, for the whole kernel; rows of tokens that an expert does not have
-// are computed and dropped.  The sums of the eight wavefronts are joined through
-// LDS, by another wavefront for each tile.
+// an operand row for every expert, so the tokens' codes stay in registers for the
+// whole kernel; rows of tokens that an expert does not have are computed and
+// dropped.  The sums of the eight wavefronts are joined through LDS, by another
+// wavefront for each tile.
 //
 // k_moe_down: a workgroup has the columns [cw b, cw (b + 1)) of the output and
 // walks all experts: no sum leaves the workgroup.  A unit of work is a k-block of
@@ -36,7 +36,21 @@ namespace {
 // holds cells (a cell is 128 values of one row).
 //
 // Sums are fp32 (int32 inside an int8 product), in an order that depends on the
-// routes only.
+// routes only.  g stays fp32 until it is quantised: a block of it (int8: a row) is
+// the work of several workgroups of k_moe_up, so that its scale is known in
+// k_moe_down first, which quantises it for each workgroup anew.
+//
+// Bound: the weights' way from memory, and what stands before it in each launch.
+// 8 experts of fp8, 7168 x 4096, one token: 4.8 + 38.7 + 23.3 us, the products at
+// 6.1 and 5.0 TB/s, where such loads alone reach 6.8; 13 of them for 32 tokens 5.0 +
+// 63 + 42.6; 12 of int8 for 16 tokens 4.7 + 55.5 + 38; 32 of int8, 2048 x 1536, for
+// 5 tokens 4 + 22 + 21.4 (1536 columns: 22 us of weights in all); 4 of 1024 x 1024,
+// one token 2.6 + 6.6 + 7.6.  Before its first product k_moe_up takes 4 us (routes,
+// table, the tokens' codes), k_moe_down 5 to 7 (the table, g and its quantisation),
+// by clocks read in the kernel; weights are on their way for half of that.  Held
+// against it: the tokens quantised inside k_moe_up (spills; one token 98 us, 85 with
+// k_moe_prep), the rows' largest values by atomics instead of one for each tile (8 us
+// more at 16 tokens, all workgroups meet at few words).
 // ---------------------------------------------------------------------------
 constexpr int kMoeThreads = 512;
 constexpr int kMoeWaves = kMoeThreads / 64;
