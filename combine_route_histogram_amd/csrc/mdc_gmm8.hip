@@ -68,14 +68,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t channel_scales(const Gmm8& g, 
 // expert's rows stay in registers from tile to tile, kThin8Run k-blocks of them.
 //
 // The border of 32 rows is that of two blocks of the instruction, for any number of
-// experts; 32 : 33 rows each, in us: one expert x 4096 x 7168 14.1 : 20.4, four 26.4 :
-// 25.5, 16 x 4096 x 2048 31 : 24, 8 x 2048 x 1024 11.3 : 8.8.
+// experts; 32 : 33 rows each, in us: one expert x 4096 x 7168 12.7 : 20.4, four 24.1 :
+// 25.5, 16 x 4096 x 2048 28.3 : 24.3, 8 x 2048 x 1024 11.2 : 8.8.
 //
 // LDS accesses are written out with their waits: the compiler would make each wait
 // for every direct load in flight.
 // ---------------------------------------------------------------------------
 constexpr int kThin8Ring = 12288;   // bytes of a wavefront's ring
 constexpr int kThin8Run = 8;        // k-blocks of rows in registers
+constexpr int kThin8Direct = 16;    // most rows that are always loaded in the instruction's layout
 constexpr int kThin8Nt = 2;         // cache policy: non-temporal
 
 struct Thin8Smem {
@@ -108,7 +109,7 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
   } c = {t0 / tiles_per, (t0 % tiles_per) * width, 0, t1 - t0};
   __amdgpu_buffer_rsrc_t rw = weights(c.i);
   unsigned slot = 0;   // of the next load
-  const int lrow = lane >> 3;
+  const int lrow = lane >> 3, key = (r16 >> 1) & 7;
   auto fetch = [&]() {
     const bool in = c.left > 0;
     const unsigned k0 = in ? (unsigned)min(kb0 + c.step, nk) * kGmm8Block : (unsigned)nk * kGmm8Block;
@@ -142,28 +143,55 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
 #pragma unroll
     for (int m = 0; m < MB; ++m) sa[m] = g.a_scale[row0 + min(16 * m + r16, rows - 1)];
   };
-  // their k-blocks s0 ... of the run, in the matrix instruction's layout
+  // Their k-blocks s0 ... of the run, in the matrix instruction's layout.  Loaded in it,
+  // lanes side by side take 16 bytes of different rows, and a load costs by its rows; of
+  // many rows and k-blocks a row's 128 bytes are loaded by eight lanes, and place() turns
+  // them.  Loaded so : turned, in us, 32 rows each: 16 experts x 4096 x 2048 31.3 : 28.3,
+  // one x 4096 x 7168 14.0 : 12.7; 16 rows of it 11.7 : 12.3; 32 rows and two k-blocks a
+  // wavefront (one x 7168 x 2048) 10.9 : 12.1.
+  auto direct = [&]() { return rows <= kThin8Direct || per <= kThin8Run / 2; };
   auto tokens = [&](int s0) {
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int8_t*>(g.a + (int64_t)row0 * K), (short)0, rows * K, 0x00020000);
+    const bool in = direct();
+    const int row = in ? r16 : lrow, far = in ? 0 : 8 * K;   // of the two halves of a block
+    const unsigned c0 = 16u * (in ? quad : lane & 7), c1 = in ? c0 + 64u : c0;
 #pragma unroll
     for (int d = 0; d < kThin8Run; ++d) {
       const int b = s0 + d < per ? kb0 + s0 + d : nk;
-      const unsigned k0 = (unsigned)b * kGmm8Block + 16u * quad, k1 = k0 + 64u;
+      const unsigned k0 = (unsigned)b * kGmm8Block + c0, k1 = (unsigned)b * kGmm8Block + c1;
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        const unsigned at = (unsigned)((16 * m + r16) * K);
+        const unsigned at = (unsigned)((16 * m + row) * K);
         tok[d][m] = join(__builtin_amdgcn_raw_buffer_load_b128(ra, k0 < (unsigned)K ? at + k0 : kPastEnd, 0, 0),
-                         __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + k1 : kPastEnd, 0, 0));
+                         __builtin_amdgcn_raw_buffer_load_b128(ra, k1 < (unsigned)K ? at + far + k1 : kPastEnd, 0, 0));
       }
     }
+  };
+  // through the wavefront's place for the sums of tile t
+  auto place = [&](int t) {
+    if (direct()) return;
+    const unsigned at = sm.red + (t & 1) * (kGmmWaves * MB * 1024) + wave * (MB * 1024);
+    const unsigned put = at + lrow * kGmm8Block + (((lane & 7) ^ (lrow >> 1)) << 4), far = at + (8 + lrow) * kGmm8Block +
+                                                                                          (((lane & 7) ^ (4 + (lrow >> 1))) << 4);
+    const unsigned g0 = at + r16 * kGmm8Block + ((quad ^ key) << 4), g1 = at + r16 * kGmm8Block + (((4 + quad) ^ key) << 4);
+#pragma unroll
+    for (int d = 0; d < kThin8Run; ++d)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const v8i q = tok[d][m];
+        lds_put(put, __builtin_bit_cast(v4f, v4i{q[0], q[1], q[2], q[3]}));
+        lds_put(far, __builtin_bit_cast(v4f, v4i{q[4], q[5], q[6], q[7]}));
+        tok[d][m] = lds_get2(g0, g1);   // (a wavefront's LDS accesses keep their order)
+      }
   };
   expert();
   tokens(0);
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) fetch();
 
-  const int key = (r16 >> 1) & 7;
+  place(t0);
+
   const unsigned f0 = sm.ring + r16 * kGmm8Block + ((quad ^ key) << 4);
   const unsigned f1 = sm.ring + r16 * kGmm8Block + (((4 + quad) ^ key) << 4);
   unsigned read = 0;
@@ -175,6 +203,7 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
     for (int s0 = 0; s0 < per; s0 += kThin8Run) {
       if (i != have || s0 != held) {
         tokens(s0);
+        place(t);
         held = s0;
       }
 #pragma unroll

@@ -91,6 +91,12 @@ def test_tiles(counts, dtype):
     check(counts, 4104, 400, dtype=dtype, seed=len(counts))
 
 
+# workgroups that pass from expert to expert, with up to eight and with nine k-blocks a wavefront
+@pytest.mark.parametrize("counts,n,k", [([20, 32, 0, 17, 8] * 8, 1040, 1936), ([32, 5, 18] * 14, 520, 4112), ([31] * 70, 264, 1040)])
+def test_streams_of_many_experts(counts, n, k):
+    check(counts, n, k, seed=n)
+
+
 # with 256 CUs: one or two rounds of tiles of 64 x 64, whose k-blocks go over the wavefronts, beside few rows an expert
 @pytest.mark.parametrize("counts,n,k,capacity", [
     ([33], 1160, 2000, 33), ([64], 2056, 7168, 70), ([200, 5, 0, 65, 32], 328, 1040, 290), ([513], 136, 7184, 600),
