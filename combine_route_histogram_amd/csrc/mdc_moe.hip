@@ -102,6 +102,7 @@ struct MoeTable {
   float weight[kMoeRoutes];         // of each row: the sum of its routes' scales
   float copy[kMoeTokens];           // sum of the scales of the token's copy experts
   float present[kMoeTokens];        // and of all its routes
+  uint32_t has[kMoeTokens];         // bit 0: it has a route to a copy expert; bit 1: a present route
   int wave_total[kMoeWaves];
   int experts, dropped;
 };
@@ -121,8 +122,10 @@ __device__ __forceinline__ void table_copy(MoeTable& to, const MoeTable& from, i
   }
   if (i < kMoeTokens) {
     const float c = from.copy[i], p = from.present[i];
+    const uint32_t h = from.has[i];
     to.copy[i] = c;
     to.present[i] = p;
+    to.has[i] = h;
   }
   if (i == 0) {
     to.base[0] = 0;
@@ -208,6 +211,7 @@ __device__ __forceinline__ void moe_table(const Moe& a, const MoeRoute& route, M
   if (blockIdx.x != 0) return;
   if (i < R) {
     float sum = 0.f, copy = 0.f, all = 0.f;
+    uint32_t has = 0;
     bool lead = mine;
     const int r0 = token * a.K;
 #pragma unroll 4
@@ -219,11 +223,13 @@ __device__ __forceinline__ void moe_table(const Moe& a, const MoeRoute& route, M
       lead = lead && !(same && r < i);
       copy += other >= a.EZ ? s : 0.f;
       all += s;
+      has |= (other >= a.EZ ? 1u : 0u) | (other >= 0 ? 2u : 0u);
     }
     if (lead) t.weight[t.base[j] + __popc(t.tokens[j] & ((1u << token) - 1))] = sum;
     if (i == r0) {
       t.copy[token] = copy;
       t.present[token] = all;
+      t.has[token] = has;
     }
   }
   lds_barrier();
@@ -830,8 +836,10 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_down(Moe a) {
 #pragma unroll
     for (int w = 0; w < kMoeWaves; ++w) v += part[((w * TB + m) * NB + n) * 256 + at];
     const int64_t o = (int64_t)token * H + col;
-    if (a.ori != nullptr) v = __builtin_fmaf(tab.copy[token], __uint_as_float((uint32_t)a.ori[o] << 16), v);
-    if (a.shared != nullptr) v = __builtin_fmaf(tab.present[token], __uint_as_float((uint32_t)a.shared[o] << 16), v);
+    // (what no route looks at may be infinite or NaN)
+    const uint32_t has = tab.has[token];
+    if (a.ori != nullptr && (has & 1)) v = __builtin_fmaf(tab.copy[token], __uint_as_float((uint32_t)a.ori[o] << 16), v);
+    if (a.shared != nullptr && (has & 2)) v = __builtin_fmaf(tab.present[token], __uint_as_float((uint32_t)a.shared[o] << 16), v);
     a.out[o] = (uint16_t)bf16_rne(v);
   }
 }

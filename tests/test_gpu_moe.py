@@ -289,6 +289,26 @@ def test_what_is_not_finite_reaches_its_tokens_only(fmt):
 
 
 @FMT
+def test_what_is_not_finite_where_no_route_looks(fmt):
+    """The rows of masked tokens, the copy row of a token without a copy expert, the scales of masked and dropped routes."""
+    m = Layer(fmt, 18, 2, 256, 512, 8, copy=2, seed=17)
+    m.ids[:] = torch.tensor([0, 1])
+    m.ids[2] = torch.tensor([3, 9])    # one copy expert
+    m.ids[5] = torch.tensor([-1, 10])   # no present route
+    m.mask = torch.ones(18, dtype=torch.bool)
+    m.mask[[1, 17]] = False
+    ori = m.x.clone()
+    clean = m.run(ori_x=ori.to(DEV))
+    for t in (1, 17):
+        m.x[t, 3], m.shared[t, 7], m.scales[t, 0] = float("nan"), float("inf"), float("nan")
+    m.shared[5], m.scales[5] = float("nan"), float("inf")
+    ori[[0, 1, 3, 5, 17]] = float("nan")
+    got = m.run(ori_x=ori.to(DEV))
+    assert torch.equal(got, clean) and not got[[1, 5, 17]].any()
+    assert torch.isfinite(got.float()).all()
+
+
+@FMT
 def test_zero_rows_and_rows_of_other_sizes(fmt):
     m = Layer(fmt, 6, 2, 256, 512, 4, seed=14)
     m.x[1] = 0
