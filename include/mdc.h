@@ -843,8 +843,9 @@ mdc_status mdc_block_rms_norm(const mdc_block_norm_params* params,
  *   logits (both may be NULL then), else read; x_active_mask [BS], or [BS][K] with
  *   mask_per_route, or NULL; weights and their scales as mdc_ffn's and
  *   mdc_ffn_fp8's; shared_expert_x, ori_x [BS][H] bf16 or NULL; x_out [BS][H] bf16
- * A token with no present route gets a row of zeros.  x_out may be x, ori_x or
- * shared_expert_x; other overlaps are not allowed.  BS <= MDC_MAX_MOE_TOKENS, H a
+ * A token with no present route gets a row of zeros, and ori_x counts only where
+ * a copy expert is among its routes, whatever the rows hold there.  x_out may be
+ * x, ori_x or shared_expert_x; other overlaps are not allowed.  BS <= MDC_MAX_MOE_TOKENS, H a
  * multiple of 128 and at most 8192, inter_n = N a multiple of 256, N * H < 2^31
  * (else MDC_ERR_UNSUPPORTED); with logits the bounds of mdc_gate.  capacity and
  * flags of shape are checked and otherwise ignored.
