@@ -226,6 +226,7 @@ __device__ __forceinline__ void thin8_walk(const Gmm8& g, const GmmTable& tab, i
     }
     // join the runs of k-blocks: job (column block, row block) by another wavefront for each tile
     const unsigned red = sm.red + (t & 1) * (kGmmWaves * MB * 1024);
+    matrix_done(acc);
 #pragma unroll
     for (int m = 0; m < MB; ++m) lds_put(red + ((wave * MB + m) * 64 + lane) * 16, __builtin_bit_cast(v4f, acc[m]));
     lds_barrier();
@@ -563,6 +564,7 @@ __device__ __forceinline__ void split8_walk(const Gmm8& g, const GmmTable& tab, 
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);   // no direct load into LDS is left in flight
     lds_barrier();                        // the rings are free
+    matrix_done(acc);
 #pragma unroll
     for (int i = 0; i < B; ++i)
 #pragma unroll

@@ -29,6 +29,24 @@ __device__ __forceinline__ unsigned lds_at(const void* p) { return (unsigned)(si
 __device__ __forceinline__ void lds_put(unsigned at, v4f v) {
   asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
 }
+// Sums of v_mfma_i32_16x16x64_i8 that lds_put writes next: of an instruction in inline
+// assembly the compiler does not know that it reads them, and leaves out the 8 wait
+// states that the matrix instruction's results take.
+template <int n>
+__device__ __forceinline__ void matrix_hold(v4i (&acc)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm volatile("" : "+v"(acc[i]));
+}
+template <int m, int n>
+__device__ __forceinline__ void matrix_hold(v4i (&acc)[m][n]) {
+#pragma unroll
+  for (int i = 0; i < m; ++i) matrix_hold(acc[i]);
+}
+template <typename Sums>
+__device__ __forceinline__ void matrix_done(Sums& acc) {
+  matrix_hold(acc);
+  asm volatile("s_nop 7");
+}
 __device__ __forceinline__ v8i lds_get2(unsigned a, unsigned b) {
   v4i x, y;
   asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"

@@ -463,6 +463,7 @@ __global__ __launch_bounds__(kMoeThreads) void k_moe_up(Moe a) {
       }
     }
     const unsigned buf = lds_at(red[t & 1]);
+    if constexpr (INT8) matrix_done(acc);
 #pragma unroll
     for (int m = 0; m < TB; ++m) lds_put(buf + ((wave * TB + m) * 64 + lane) * 16, __builtin_bit_cast(v4f, acc[m]));
     lds_barrier();
