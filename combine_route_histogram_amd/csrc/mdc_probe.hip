@@ -21,6 +21,9 @@
 //   probe_rows_reduce for each output row, read its listed rows and one more
 //                     row of its own and write the XOR of them (the combine's
 //                     access pattern without its metadata prologue)
+// One more shows what the products' kernels rely on:
+//   probe_bounded_read  loads through a buffer descriptor, the offset in the
+//                     scalar operand, at and past the descriptor's end
 
 #include <hip/hip_runtime.h>
 
@@ -163,6 +166,22 @@ __global__ __launch_bounds__(64) void k_rows_reduce(const v4u* __restrict__ src,
   if (i < nvec) st(dst + (int64_t)t * nvec + i, acc);
 }
 
+// One wavefront: lane l takes bytes 16 l ... of the 1024 at the scalar offset, into
+// registers and straight into LDS.
+typedef __attribute__((address_space(3))) void lds_void;
+__global__ __launch_bounds__(64) void k_bounded_read(const void* src, unsigned bound, unsigned offset, v4u* dst) {
+  __shared__ __attribute__((aligned(16))) v4u lds[64];
+  const int lane = threadIdx.x;
+  lds[lane] = v4u{~0u, ~0u, ~0u, ~0u};
+  __syncthreads();
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(src), (short)0, bound, 0x00020000);
+  dst[lane] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(r, 16u * lane, offset, 0));
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, 16u * lane, offset, 0, 0);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  dst[64 + lane] = lds[lane];
+}
+
 int status_of(hipError_t e) { return e == hipSuccess ? 0 : 1; }
 
 }  // namespace
@@ -255,6 +274,13 @@ int mdc_probe_rows_reduce(const void* src, const int32_t* rows, int32_t k, const
   else
     hipLaunchKernelGGL(k_rows_reduce<16>, grid, dim3(64), 0, (hipStream_t)stream, (const v4u*)src, rows, k,
                        (const v4u*)own, (v4u*)dst, n_out, nvec, ntiles);
+  return status_of(hipGetLastError());
+}
+
+int mdc_probe_bounded_read(const void* src, uint32_t bound, uint32_t scalar_offset, void* dst, void* stream) {
+  if (src == nullptr || dst == nullptr || (bound & 15) || (scalar_offset & 15)) return 2;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(k_bounded_read, dim3(1), dim3(64), 0, (hipStream_t)stream, src, bound, scalar_offset, (v4u*)dst);
   return status_of(hipGetLastError());
 }
 

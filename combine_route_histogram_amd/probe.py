@@ -20,7 +20,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 EXPORTS = ("mdc_probe_read", "mdc_probe_write", "mdc_probe_copy", "mdc_probe_rows_read", "mdc_probe_rows_write",
-           "mdc_probe_rows_fanout", "mdc_probe_rows_reduce")
+           "mdc_probe_rows_fanout", "mdc_probe_rows_reduce", "mdc_probe_bounded_read")
 
 _P, _U64, _I32, _U32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_uint32
 _lib.mdc_probe_read.argtypes = [_P, _U64, _P, _P]
@@ -30,6 +30,7 @@ _lib.mdc_probe_rows_read.argtypes = [_P, _P, _I32, _I32, _P, _P]
 _lib.mdc_probe_rows_write.argtypes = [_P, _P, _P, _I32, _I32, _P]
 _lib.mdc_probe_rows_fanout.argtypes = [_P, _P, _P, _P, _P, _I32, _I32, _P]
 _lib.mdc_probe_rows_reduce.argtypes = [_P, _P, _I32, _P, _P, _I32, _I32, _P]
+_lib.mdc_probe_bounded_read.argtypes = [_P, _U32, _U32, _P, _P]
 for _n in EXPORTS:
     getattr(_lib, _n).restype = ctypes.c_int
 
@@ -85,3 +86,9 @@ def rows_reduce(src, rows, k: int, own, dst, row_bytes: int, stream) -> None:
     assert rows.dtype == torch.int32 and rows.numel() % k == 0
     _ok(_lib.mdc_probe_rows_reduce(src.data_ptr(), rows.data_ptr(), k, own.data_ptr(), dst.data_ptr(),
                                    rows.numel() // k, row_bytes, stream), "mdc_probe_rows_reduce")
+
+
+def bounded_read(src, bound: int, scalar_offset: int, dst, stream) -> None:
+    """dst: what the two kinds of loads give for the 1024 bytes at scalar_offset of a descriptor over `bound` bytes."""
+    assert max(bound, scalar_offset + 1024) <= _bytes(src) and _bytes(dst) >= 2048
+    _ok(_lib.mdc_probe_bounded_read(src.data_ptr(), bound, scalar_offset, dst.data_ptr(), stream), "mdc_probe_bounded_read")

@@ -60,6 +60,14 @@ int mdc_probe_rows_fanout(const void* src, const int32_t* src_rows, const int32_
 int mdc_probe_rows_reduce(const void* src, const int32_t* rows, int32_t k, const void* own, void* dst, int32_t n_out,
                           int32_t row_bytes, void* stream);
 
+/* What a buffer descriptor over the first `bound` bytes of src gives for the
+ * 1024 bytes at scalar_offset, where the offset stands in the loads' scalar
+ * operand: the kernels of libmdc rely on zeros from `bound` on, also for an
+ * offset past it.  dst (2048 bytes) takes what loads into registers and what
+ * loads into LDS give.  src holds scalar_offset + 1024 bytes in any case; both
+ * sizes are multiples of 16 and may be 0. */
+int mdc_probe_bounded_read(const void* src, uint32_t bound, uint32_t scalar_offset, void* dst, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
