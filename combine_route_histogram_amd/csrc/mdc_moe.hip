@@ -913,14 +913,14 @@ mdc_status moe_impl(const mdc_shape* shape, const mdc_gate_params* params, int32
                     size_t workspace_bytes, void* stream) {
   const mdc_status st = check_moe(shape, inter_n);
   if (st != MDC_OK) return st;
-  if ((params != nullptr) != (logits != nullptr)) return MDC_ERR_NULLPTR;
-  if ((expert_ids != nullptr) != (expert_scales != nullptr)) return MDC_ERR_NULLPTR;
   const int64_t E = (int64_t)shape->num_experts + shape->zero_experts + shape->copy_experts;
   if (params != nullptr) {
     const mdc_status gate = check_gate(*params, E, shape->topk);
     if (gate != MDC_OK) return gate;
   }
-  if (shape->bs == 0) return MDC_OK;
+  if (shape->bs == 0) return MDC_OK;   // (tensors of no tokens may be NULL, logits among them)
+  if ((params != nullptr) != (logits != nullptr)) return MDC_ERR_NULLPTR;
+  if ((expert_ids != nullptr) != (expert_scales != nullptr)) return MDC_ERR_NULLPTR;
   const MoePlan p = make_moe_plan(shape, inter_n);
   if (x == nullptr || w1 == nullptr || w1_scale == nullptr || w2 == nullptr || w2_scale == nullptr || x_out == nullptr ||
       workspace == nullptr || (params == nullptr && expert_ids == nullptr) ||

@@ -852,7 +852,8 @@ mdc_status mdc_block_rms_norm(const mdc_block_norm_params* params,
  * The workspace (size from mdc_moe_workspace, mdc_moe_fp8_workspace) holds the
  * status block (dropped_ids: active routes of these tokens whose id is out of
  * range), the routes where the caller takes none, and g; two calls may share it if
- * they do not run at the same time.  With BS == 0 nothing is written.
+ * they do not run at the same time.  With BS == 0 nothing is written, and the
+ * tensors may be NULL.
  * ------------------------------------------------------------------------ */
 #define MDC_MAX_MOE_TOKENS 32
 
