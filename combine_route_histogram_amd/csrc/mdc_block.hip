@@ -10,14 +10,15 @@ namespace {
 // with inv_x = 1 / sqrt(mean(x^2) + post_eps) known only after the row was read.
 // Everything a row needs is loaded before the sum of x^2: p = x * post * gate and
 // the scaled residual stay in registers, and one FMA with inv_x makes h of them.
-// (Where both norms are inside fp32's range, p is: it is h divided by inv_x.)
+// (Where both norms are inside fp32's range, p is: it is h's part divided by inv_x.
+// With no norm of h, h alone may be larger than that leaves room for.)
 // Then h^2 is summed and the outputs leave as for mdc_add_rms_norm.
 //
 // Sums and everything up to the outputs are fp32; residual_out, y and q are
 // rounded once each, from the unrounded values.
 //
 // Bound: memory.  16384 rows of 7168 (bf16, residual in and out, y, fp8 rows and
-// scales: 1.06 GB) 196 us, 5.4 TB/s, where mdc_add_rms_norm takes 184 and a plain
+// scales: 1.06 GB) 196-203 us, 5.2-5.4 TB/s, where mdc_add_rms_norm takes 184 and a plain
 // read and write of its bytes 172: a row waits at one sum more.  With a gate value
 // for each element 226 us (5.7 TB/s), with its sigmoid 241: two exact functions of
 // fp32, an exponential and a quotient.
@@ -185,10 +186,13 @@ void launch_block_quant(const BlockArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(kernel, grid_of(a.rows), dim3(threads), 0, s, a);
   };
   // Two vectors a thread from 257 on: smaller workgroups, of which a CU holds more,
-  // so that one's waits at its sums are another's loads.  16384 rows of 7168 (bf16,
-  // a gate row for 2048 rows, y and fp8 out) take 227 us with one vector a thread,
-  // 196 with two, 201 with four; 2051 x 5000 36, 33 and 38; 8192 rows of 16384 228
-  // with two, 242 with four.
+  // so that one's waits at its sums are another's loads.  With one, two and four, in
+  // us: 16384 rows of 7168 (bf16, a gate row for 2048 rows, y and fp8 out) 238, 202 and
+  // 204; 2048 x 7168 with one gate row 36, 33 and 33, 256 rows 7.4, 7.5 and 9.2, 32
+  // rows 5.6, 5.6 and 7.1; 2051 x 5000 27.5, 26.0 and 27.8, its int8 rows alone 25.8,
+  // 22.2 and 23.6; fp16 with residual and weights in fp32, a sigmoid gate for each
+  // element, int8 out 38.1, 38.2 and 39.1; 1000 x 2048 6.9, 7.3 and 9.1; 8192 rows of
+  // 16384 234 with two, 242 with four.
   if (a.nvec <= kNormThreads / 4) go(std::integral_constant<int, 1>(), k_block_rms_norm<T, R, Wt, QUANT, 1>);
   else if (a.nvec <= 2 * kNormThreads) go(std::integral_constant<int, 2>(), k_block_rms_norm<T, R, Wt, QUANT, 2>);
   else go(std::integral_constant<int, 4>(), k_block_rms_norm<T, R, Wt, QUANT, 4>);

@@ -683,7 +683,10 @@ __device__ __forceinline__ Wide8Plan gmm8_many(const Gmm8& g, GmmTable& t, int64
   return p;
 }
 
-// One workgroup per CU: the wide experts' tiles, then the thin experts'.
+// One workgroup per CU: the wide experts' tiles, then the thin experts'.  All ways in
+// one kernel take 256 registers, and ten more that spill (44 bytes of scratch): they
+// come back once a tile around the k loop of the 256-row tiles and in their outputs,
+// never inside a loop over k.
 template <bool DEEP>
 __global__ __launch_bounds__(kGmmThreads) void k_gmm8(Gmm8 g) {
   extern __shared__ int gmm_table[];

@@ -22,6 +22,9 @@ __device__ __forceinline__ float scalar(float v) { return __int_as_float(__built
 
 __device__ __forceinline__ v8i join(v4i a, v4i b) { return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}; }
 
+// By the hardware's exp and reciprocal, about 1 ulp each (the exponential's argument is
+// rounded to fp32 before, so that its error grows with |a|): what follows rounds the
+// value to 8 bits, and exact functions would cost several times the instructions.
 __device__ __forceinline__ float gmm_silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
 constexpr unsigned kPastEnd = 0x80000000u;   // an offset past every buffer: loads there read zero

@@ -771,8 +771,11 @@ mdc_status mdc_gmm_int8(int64_t capacity,
  * each channel), 1 a row for each, a sequence's length one for each sequence.
  * A gate row has H values or (gate_columns 1) a single one.
  * Squares are summed in fp32: with x or h of about 1e19 and up, or of 1e-19 and
- * below with an eps of 0, a row's norm leaves its range; so may, without a
- * post_weight, x times gate and block_scale.
+ * below with an eps of 0, a row's norm leaves its range; so may x times
+ * post_weight, gate and block_scale, which is formed before the row's factor.
+ * Without post_weight and gate and with scales of 1, residual_out is that of
+ * mdc_add_rms_norm bit by bit; y, q and q_scale are up to H = 2048, beyond it the
+ * squares are added in another order.
  *
  *   x [rows][H] and y of dtype (bf16 or fp16); gate [ceil(rows / gate_every)]
  *   [gate_columns] of gate_dtype; residual, residual_out of residual_dtype;
@@ -830,7 +833,10 @@ mdc_status mdc_block_rms_norm(const mdc_block_norm_params* params,
  *   mdc_moe      as mdc_ffn, int8 with scales for each row and channel, but g and
  *                y are not rounded to 16 bits (q2, s2 are of the fp32 g)
  *   mdc_moe_fp8  as mdc_ffn_fp8, y not rounded either
- * Sums are fp32, in an order that the routes decide.
+ * Sums are fp32, in an order that the routes decide.  silu is that of
+ * mdc_ffn_fp8, with the hardware exp and reciprocal (about 1 ulp each), and e4m3
+ * products are cut as those of mdc_gmm_fp8: a value of g that lies that near the
+ * border of two 8-bit codes may get the other one.
  * The local experts are those of shape->rank, [rank * L, (rank + 1) * L): with
  * world > 1 the tokens are given on every rank, x_out is the rank's part of the
  * sum, and ori_x and shared_expert_x are for one of the ranks (else NULL); with
