@@ -12,8 +12,8 @@ from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-CSRC = os.path.join(ROOT, "combine_route_histogram_amd", "csrc")
+from combine_route_histogram_amd.build import HIPCC_FLAGS, INC, PKG, hipcc
+
 STATES = {"v_mfma_i32_16x16x64_i8": 8, "v_mfma_i32_32x32x32_i8": 12}   # any other: 20
 MOST = 20
 
@@ -101,11 +101,8 @@ def short_waits(ops, before):
 
 
 def listing(name, out):
-    sources = [os.path.join(CSRC, f"mdc_{name}.hip")]
-    flags = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Xclang", "-target-feature",
-             "-Xclang", "-packed-fp32-ops", "-w", "-I", os.path.join(ROOT, "include"), "--cuda-device-only", "-S"]
-    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
-    subprocess.run([hipcc, *flags, *sources, "-o", out], check=True, capture_output=True, timeout=600)
+    subprocess.run([hipcc(), *HIPCC_FLAGS, "-w", "-I", INC, "--cuda-device-only", "-S", os.path.join(PKG, "csrc", f"mdc_{name}.hip"),
+                    "-o", out], check=True, capture_output=True, timeout=600)
     with open(out) as f:
         return f.read().splitlines()
 
@@ -136,7 +133,7 @@ _Zk:
     assert [(w, s) for w, _, s in short_waits(ops, before)] == [("ds_write_b128 v12, v[0:3]", 2), ("ds_write_b32 v12, v1", 7)]
 
 
-@pytest.mark.skipif(shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"), reason="needs hipcc")
+@pytest.mark.skipif(shutil.which(hipcc()) is None, reason="needs hipcc")
 def test_waits_before_hand_written_lds_writes(tmp_path):
     names = ("gmm", "gmm8", "moe")   # the sources with such writes
     with ThreadPoolExecutor(len(names)) as pool:
