@@ -17,7 +17,7 @@ WORDS = 1 << 18
 
 
 @pytest.mark.parametrize("bound,offset", [
-    (4096, 0), (4096, 3072), (4096, 3584), (4096, 4080), (4096, 4096), (4096, 4112), (4096, 65536), (4096, (1 << 20) - 1024),
+    (4096, 0), (4096, 2048), (4096, 3584), (4096, 4080), (4096, 4096), (4096, 4112), (4096, 65536), (4096, (1 << 20) - 1024),
     (16, 0), (16, 16), (0, 0), (0, 2048), (1 << 19, (1 << 19) - 1024), (1 << 19, (1 << 19) - 16), (1 << 19, 1 << 19),
     (1 << 19, (1 << 19) + 8192)])
 def test_zeros_from_the_bound_on(bound, offset):
